@@ -74,6 +74,7 @@ extern "C" {
 /* ---- output dtypes ---- */
 #define HSQ_F32   0
 #define HSQ_BF16  1
+#define HSQ_F16   2  /* the 16-bit linear and the layer normalisation only */
 
 /* ---- kernel choice for the residual contraction ---- */
 #define HSQ_KERNEL_AUTO    0  /* SKINNY for M <= 64, TILED otherwise */
@@ -432,6 +433,105 @@ size_t hsq_closed_form_l2_workspace_bytes(int K, int N, int r);
 int hsq_closed_form_l2(const float *HL1, const double *Cinv, int K, int N, int r, int group,
                        const uint16_t *W, const uint8_t *packed_w, const uint16_t *sw, float *L2,
                        void *workspace, size_t ws_bytes, void *stream);
+
+/* ---- 16-bit linear layer with bias, activation and residual ----
+ * The unquantized form of the layer, for the projections a W4A4 model keeps
+ * in 16 bits and for tuning around the quantized ones:
+ *
+ *   Z[m,n] = sum_k X[m,k] W[k,n] + bias[n]
+ *   Y[m,n] = act(Z[m,n]) + residual[m,n]
+ *
+ * with 16-bit operands, fp32 sums and an fp32 epilogue, rounded once at each
+ * store.  Any M, K, N >= 1 with M * K, K * N, M * N < 2^30 (K and N
+ * rounded up to 8 where they are row lengths).
+ *   X         in : M x K of `dtype` (HSQ_BF16 or HSQ_F16)
+ *   W         in : K x N of `dtype` (input channel x output channel)
+ *   bias      in : N of `dtype`, or NULL
+ *   act          : HSQ_ACT_IDENTITY, HSQ_ACT_GELU_TANH, HSQ_ACT_GELU (0.5 z
+ *                  (1 + erf(z / sqrt 2))) or HSQ_ACT_SILU (z / (1 + exp(-z)))
+ *   residual  in : M x N of `y_dtype`, or NULL; may be Y itself
+ *   Y         out: M x N of `y_dtype`, which is HSQ_F32 or `dtype`
+ *   Z         out: M x N of `dtype`, or NULL: the values before the
+ *                  activation, as hsq_linear_backward takes them
+ *   workspace    : ws_bytes >= hsq_linear_workspace_bytes(M, K, N) device
+ *                  bytes (NULL is fine where that is 0)
+ * No output may overlap an input, except Y the residual.  Results do not
+ * depend on earlier calls or on timing: sums run in a fixed order.
+ * Errors: HSQ_E_INVAL, HSQ_E_ALIGN, HSQ_E_WORKSPACE, HSQ_E_HIP. */
+#define HSQ_ACT_GELU       2  /* the 16-bit linear only */
+#define HSQ_ACT_SILU       3  /* the 16-bit linear only */
+size_t hsq_linear_workspace_bytes(int M, int K, int N);
+int hsq_linear(const uint16_t *X, int M, int K, int N, int dtype, const uint16_t *W,
+               const uint16_t *bias, int act, const void *residual, void *Y, int y_dtype,
+               uint16_t *Z, void *workspace, size_t ws_bytes, void *stream);
+
+/* Its backward pass, from dY = dL/dY:
+ *
+ *   dZ = dY * act'(Z)      dX = dZ W^T      dW = X^T dZ      dbias[n] = sum_m dZ[m,n]
+ *
+ * (dL/dresidual is dY itself.)  dZ is rounded to `dtype` as the operand of
+ * the two products; dbias sums the unrounded dZ.
+ *   dY      in : M x N of `y_dtype` (HSQ_F32 or `dtype`)
+ *   X, W    in : as for hsq_linear
+ *   Z       in : M x N of `dtype`, from hsq_linear (ignored and may be NULL
+ *                for HSQ_ACT_IDENTITY)
+ *   dX      out: M x K of `dtype`, or NULL: not wanted
+ *   dW      out: K x N of `dtype`, or NULL: not wanted
+ *   dbias   out: N of `dtype`, or NULL: not wanted
+ *   workspace  : ws_bytes >= hsq_linear_backward_workspace_bytes(M, K, N)
+ * W may be NULL where dX is, X where dW is; one output at least is wanted.
+ * No output may overlap an input.
+ * Errors: HSQ_E_INVAL, HSQ_E_ALIGN, HSQ_E_WORKSPACE, HSQ_E_HIP. */
+size_t hsq_linear_backward_workspace_bytes(int M, int K, int N);
+int hsq_linear_backward(const void *dY, int y_dtype, const uint16_t *X, int M, int K, int N,
+                        int dtype, const uint16_t *W, const uint16_t *Z, int act, uint16_t *dX,
+                        uint16_t *dW, uint16_t *dbias, void *workspace, size_t ws_bytes,
+                        void *stream);
+
+/* ---- layer normalisation ----
+ * The norm before the layer, per row of X over its C channels:
+ *
+ *   mean = (1/C) sum_c x[c]     rstd = ((1/C) sum_c (x[c] - mean)^2 + eps)^(-1/2)
+ *   y[c] = (x[c] - mean) * rstd * weight[c] + bias[c]
+ *
+ * weight and bias are given per group of M / groups consecutive rows: groups =
+ * 1 is the usual affine norm, one group per image the modulated norm of a
+ * diffusion transformer (weight = 1 + scale, bias = shift).
+ *   X        in : M x C of x_dtype (HSQ_F32, HSQ_BF16, HSQ_F16)
+ *   weight   in : groups x C of p_dtype, or NULL (1)
+ *   bias     in : groups x C of p_dtype, or NULL (0)
+ *   Y        out: M x C of y_dtype; may be X itself where the types are equal
+ *   mean,
+ *   rstd     out: M fp32 each, or NULL: as the backward pass takes them
+ * y_dtype is x_dtype, or any of the three where x_dtype is HSQ_F32; p_dtype
+ * is HSQ_F32 or y_dtype.  1 <= C <= 16384, groups divides M (HSQ_E_SHAPE)
+ * and is at most 65535, M * C < 2^31; eps is finite and not negative.
+ * Arithmetic is fp32, the variance taken around the finished mean.
+ * Errors: HSQ_E_INVAL, HSQ_E_SHAPE, HSQ_E_ALIGN, HSQ_E_HIP. */
+int hsq_layer_norm(const void *X, int x_dtype, int M, int C, int groups, const void *weight,
+                   const void *bias, int p_dtype, float eps, void *Y, int y_dtype, float *mean,
+                   float *rstd, void *stream);
+
+/* Its backward pass, from dY = dL/dY, with xh = (x - mean) * rstd and
+ * g = dy * weight:
+ *
+ *   dx = rstd (g - mean_c(g) - xh mean_c(g xh))
+ *   dweight[c] = sum over the group's rows of dy xh,   dbias[c] = sum of dy
+ *
+ *   dY       in : M x C of y_dtype       X, weight, mean, rstd in: as above
+ *   dX       out: M x C of x_dtype, or NULL: not wanted
+ *   dweight,
+ *   dbias    out: groups x C of p_dtype, or NULL: not wanted
+ *   workspace   : ws_bytes >= hsq_layer_norm_backward_workspace_bytes(M, C,
+ *                 groups) (NULL is fine where neither dweight nor dbias is wanted)
+ * One output at least is wanted; no output may overlap an input.  Sums run in
+ * a fixed order.
+ * Errors: HSQ_E_INVAL, HSQ_E_SHAPE, HSQ_E_ALIGN, HSQ_E_WORKSPACE, HSQ_E_HIP. */
+size_t hsq_layer_norm_backward_workspace_bytes(int M, int C, int groups);
+int hsq_layer_norm_backward(const void *dY, int y_dtype, const void *X, int x_dtype, int M, int C,
+                            int groups, const float *mean, const float *rstd, const void *weight,
+                            int p_dtype, void *dX, void *dweight, void *dbias, void *workspace,
+                            size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -23,10 +23,12 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "hsq.h")
 
 OK, E_INVAL, E_SHAPE, E_ALIGN, E_WORKSPACE, E_HIP, E_SCRATCH = 0, -1, -2, -3, -4, -5, -6
 NOALLOC_SCRATCH_BYTES = 64 << 20
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2
 KERNEL_AUTO, KERNEL_TILED, KERNEL_SKINNY = 0, 1, 2
 ACT_IDENTITY, ACT_GELU_TANH = 0, 1
+ACT_GELU, ACT_SILU = 2, 3            # the 16-bit linear only
 _ACTS = {"identity": ACT_IDENTITY, "gelu_tanh": ACT_GELU_TANH}
+_LINEAR_ACTS = {**_ACTS, "gelu": ACT_GELU, "silu": ACT_SILU}
 _KERNELS = {"auto": KERNEL_AUTO, "tiled": KERNEL_TILED, "skinny": KERNEL_SKINNY}
 
 _lib = None
@@ -89,6 +91,13 @@ def _load():
             "hsq_deflate_workspace_bytes": ([I, I], S),
             "hsq_deflate_hessian": ([P, I, P, I, P, P, P, P, S, P], I),
             "hsq_closed_form_l2_workspace_bytes": ([I, I, I], S),
+            "hsq_linear_workspace_bytes": ([I, I, I], S),
+            "hsq_linear": ([P, I, I, I, I, P, P, I, P, P, I, P, P, S, P], I),
+            "hsq_linear_backward_workspace_bytes": ([I, I, I], S),
+            "hsq_linear_backward": ([P, I, P, I, I, I, I, P, P, I, P, P, P, P, S, P], I),
+            "hsq_layer_norm": ([P, I, I, I, I, P, P, I, ctypes.c_float, P, I, P, P, P], I),
+            "hsq_layer_norm_backward_workspace_bytes": ([I, I, I], S),
+            "hsq_layer_norm_backward": ([P, I, P, I, I, I, I, P, P, P, I, P, P, P, P, S, P], I),
             "hsq_closed_form_l2": ([P, P, I, I, I, I, P, P, P, P, P, S, P], I),
         }
         for name, (args, res) in sig.items():
@@ -528,3 +537,221 @@ def closed_form_l2(HL1, Cinv, W, packed_w, sw, group: int = 64, out=None, worksp
            "hsq_closed_form_l2")
     return out
 
+
+
+# ------------------------------------------- 16-bit linear, layer normalisation
+_DTYPES = {}
+
+
+def _dtypes():
+    """torch dtype -> HSQ_* code, and its name -> torch dtype."""
+    if not _DTYPES:
+        torch = _torch()
+        for name, code in (("f32", F32), ("bf16", BF16), ("f16", F16)):
+            t = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[name]
+            _DTYPES[t] = code
+            _DTYPES[name] = t
+    return _DTYPES
+
+
+def _half16():
+    torch = _torch()
+    return (torch.bfloat16, torch.float16)
+
+
+def _on_current_device(*tensors):
+    """The kernels run on the current stream of the current device: every
+    tensor has to live there."""
+    torch = _torch()
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+
+
+def _y_type(y_dtype, x_dtype, allowed):
+    torch = _torch()
+    if y_dtype is None:
+        return x_dtype
+    if y_dtype not in ("f32", "bf16", "f16"):
+        raise ValueError(f"y_dtype {y_dtype!r} is not 'f32', 'bf16' or 'f16'")
+    t = _dtypes()[y_dtype]
+    if t not in allowed:
+        raise TypeError(f"y_dtype {y_dtype} does not go with {x_dtype} inputs")
+    return t
+
+
+def _scratch(workspace, need: int, device):
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    return _dev_tensor(workspace, "workspace", (torch.uint8,))
+
+
+def linear_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(_load().hsq_linear_workspace_bytes(M, K, N))
+
+
+def linear(X, W, bias=None, residual=None, *, act: str = "identity", y_dtype=None, out=None,
+           preact_out=None, return_preact: bool = False, workspace=None):
+    """Y = act(X W + bias) + residual: X (M, K), W (K, N), bias (N,) bf16 or
+    fp16, residual (M, N) of Y's type.  Y is of X's type, or fp32 with
+    y_dtype="f32".  ``out`` may be ``residual`` (added in place).  With
+    preact_out or return_preact the values before the activation are written
+    in X's type, as linear_backward takes them; return_preact returns
+    (Y, Z)."""
+    torch = _torch()
+    lib = _load()
+    _dev_tensor(X, "X", _half16())
+    M, K = X.shape
+    dt = X.dtype
+    _dev_tensor(W, "W", (dt,))
+    if W.dim() != 2 or W.shape[0] != K:
+        raise ValueError(f"W: shape {tuple(W.shape)} does not follow X {tuple(X.shape)}")
+    N = int(W.shape[1])
+    if act not in _LINEAR_ACTS:
+        raise ValueError(f"act {act!r} not in {sorted(_LINEAR_ACTS)}")
+    ydt = _y_type(y_dtype, dt, (torch.float32, dt))
+    if bias is not None:
+        _dev_tensor(bias, "bias", (dt,), (N,))
+    if residual is not None:
+        _dev_tensor(residual, "residual", (ydt,), (M, N))
+    if out is None:
+        out = torch.empty((M, N), dtype=ydt, device=X.device)
+    else:
+        _dev_tensor(out, "out", (ydt,), (M, N))
+    if preact_out is not None:
+        _dev_tensor(preact_out, "preact_out", (dt,), (M, N))
+    elif return_preact:
+        preact_out = torch.empty((M, N), dtype=dt, device=X.device)
+    if workspace is None:
+        need = int(lib.hsq_linear_workspace_bytes(M, K, N))
+        workspace = _scratch(None, need, X.device) if need else None
+    else:
+        _dev_tensor(workspace, "workspace", (torch.uint8,))
+    _on_current_device(X, W, bias, residual, out, preact_out, workspace)
+    _check(lib.hsq_linear(_ptr(X), M, K, N, _dtypes()[dt], _ptr(W), _ptr(bias), _LINEAR_ACTS[act],
+                          _ptr(residual), _ptr(out), _dtypes()[ydt], _ptr(preact_out), _ptr(workspace),
+                          0 if workspace is None else workspace.numel(), _stream()), "hsq_linear")
+    return (out, preact_out) if return_preact else out
+
+
+def linear_backward_workspace_bytes(M: int, K: int, N: int) -> int:
+    return int(_load().hsq_linear_backward_workspace_bytes(M, K, N))
+
+
+def linear_backward(dY, X, W, preact=None, *, act: str = "identity", need_input: bool = True,
+                    need_weight: bool = True, need_bias: bool = True, workspace=None):
+    """Gradients of ``linear``: dY (M, N) of X's type or fp32, X (M, K), W
+    (K, N), preact (M, N) as ``linear`` returned it (not needed for the
+    identity).  Returns (dX, dW, dbias) in X's type, None where not needed;
+    the residual's gradient is dY itself."""
+    torch = _torch()
+    lib = _load()
+    _dev_tensor(X, "X", _half16())
+    M, K = X.shape
+    dt = X.dtype
+    _dev_tensor(W, "W", (dt,))
+    if W.dim() != 2 or W.shape[0] != K:
+        raise ValueError(f"W: shape {tuple(W.shape)} does not follow X {tuple(X.shape)}")
+    N = int(W.shape[1])
+    if act not in _LINEAR_ACTS:
+        raise ValueError(f"act {act!r} not in {sorted(_LINEAR_ACTS)}")
+    _dev_tensor(dY, "dY", (dt, torch.float32), (M, N))
+    if act != "identity":
+        _dev_tensor(preact, "preact", (dt,), (M, N))
+    else:
+        preact = None
+    dX = torch.empty((M, K), dtype=dt, device=X.device) if need_input else None
+    dW = torch.empty((K, N), dtype=dt, device=X.device) if need_weight else None
+    db = torch.empty((N,), dtype=dt, device=X.device) if need_bias else None
+    workspace = _scratch(workspace, 0 if workspace is not None else
+                         int(lib.hsq_linear_backward_workspace_bytes(M, K, N)), X.device)
+    _on_current_device(dY, X, W, preact, workspace)
+    _check(lib.hsq_linear_backward(_ptr(dY), _dtypes()[dY.dtype], _ptr(X), M, K, N, _dtypes()[dt], _ptr(W),
+                                   _ptr(preact), _LINEAR_ACTS[act], _ptr(dX), _ptr(dW), _ptr(db),
+                                   _ptr(workspace), workspace.numel(), _stream()), "hsq_linear_backward")
+    return dX, dW, db
+
+
+def _norm_param(p, name, ydt, C):
+    """weight / bias (C,) or (groups, C), fp32 or of Y's type -> groups."""
+    torch = _torch()
+    _dev_tensor(p, name, (torch.float32, ydt))
+    if p.dim() not in (1, 2) or p.shape[-1] != C:
+        raise ValueError(f"{name}: shape {tuple(p.shape)} is neither ({C},) nor (groups, {C})")
+    return 1 if p.dim() == 1 else int(p.shape[0])
+
+
+def layer_norm(X, weight=None, bias=None, *, eps: float = 1e-5, y_dtype=None, out=None,
+               return_stats: bool = False):
+    """Layer normalisation of the rows of X (M, C), fp32, bf16 or fp16.
+    weight and bias are (C,), or (groups, C) for groups of M / groups
+    consecutive rows (the modulated norm: weight = 1 + scale, bias = shift per
+    image); both of one type, fp32 or Y's.  Y is of X's type, or for fp32 X
+    of y_dtype.  ``out`` may be X where the types are equal.  return_stats:
+    (Y, mean, rstd), fp32 (M,), for layer_norm_backward."""
+    torch = _torch()
+    lib = _load()
+    dts = _dtypes()
+    _dev_tensor(X, "X", (torch.float32, torch.bfloat16, torch.float16))
+    M, C = X.shape
+    ydt = _y_type(y_dtype, X.dtype, (X.dtype,) if X.dtype != torch.float32 else
+                  (torch.float32, torch.bfloat16, torch.float16))
+    groups, pdt = 1, torch.float32
+    for p, name in ((weight, "weight"), (bias, "bias")):
+        if p is not None:
+            groups, pdt = _norm_param(p, name, ydt, C), p.dtype
+    if weight is not None and bias is not None and (weight.shape != bias.shape or weight.dtype != bias.dtype):
+        raise ValueError("weight and bias differ in shape or type")
+    if out is None:
+        out = torch.empty((M, C), dtype=ydt, device=X.device)
+    else:
+        _dev_tensor(out, "out", (ydt,), (M, C))
+    mean = rstd = None
+    if return_stats:
+        mean = torch.empty((M,), dtype=torch.float32, device=X.device)
+        rstd = torch.empty((M,), dtype=torch.float32, device=X.device)
+    _on_current_device(X, weight, bias, out)
+    _check(lib.hsq_layer_norm(_ptr(X), dts[X.dtype], M, C, groups, _ptr(weight), _ptr(bias), dts[pdt],
+                              eps, _ptr(out), dts[ydt], _ptr(mean), _ptr(rstd), _stream()), "hsq_layer_norm")
+    return (out, mean, rstd) if return_stats else out
+
+
+def layer_norm_backward_workspace_bytes(M: int, C: int, groups: int = 1) -> int:
+    return int(_load().hsq_layer_norm_backward_workspace_bytes(M, C, groups))
+
+
+def layer_norm_backward(dY, X, mean, rstd, weight=None, *, groups: int = 1, need_input: bool = True,
+                        need_params: bool = True, workspace=None):
+    """Gradients of ``layer_norm``: dY (M, C) of Y's type, X, and the mean and
+    rstd it returned -> (dX of X's type, dweight, dbias).  The parameter
+    gradients have weight's shape and type; without a weight they are
+    (groups, C) fp32.  None where not needed."""
+    torch = _torch()
+    lib = _load()
+    dts = _dtypes()
+    _dev_tensor(X, "X", (torch.float32, torch.bfloat16, torch.float16))
+    M, C = X.shape
+    _dev_tensor(dY, "dY", (X.dtype,) if X.dtype != torch.float32 else
+                (torch.float32, torch.bfloat16, torch.float16), (M, C))
+    _dev_tensor(mean, "mean", (torch.float32,), (M,))
+    _dev_tensor(rstd, "rstd", (torch.float32,), (M,))
+    shape, pdt = (groups, C), torch.float32
+    if weight is not None:
+        if groups not in (1, wg := _norm_param(weight, "weight", dY.dtype, C)):
+            raise ValueError(f"groups {groups} does not go with weight {tuple(weight.shape)}")
+        groups, shape, pdt = wg, weight.shape, weight.dtype
+    dX = torch.empty((M, C), dtype=X.dtype, device=X.device) if need_input else None
+    dw = db = None
+    if need_params:
+        dw = torch.empty(shape, dtype=pdt, device=X.device)
+        db = torch.empty(shape, dtype=pdt, device=X.device)
+        workspace = _scratch(workspace, 0 if workspace is not None else
+                             int(lib.hsq_layer_norm_backward_workspace_bytes(M, C, groups)), X.device)
+    _on_current_device(dY, X, mean, rstd, weight, workspace)
+    _check(lib.hsq_layer_norm_backward(_ptr(dY), dts[dY.dtype], _ptr(X), dts[X.dtype], M, C, groups, _ptr(mean),
+                                       _ptr(rstd), _ptr(weight), dts[pdt], _ptr(dX), _ptr(dw), _ptr(db),
+                                       _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                       _stream()), "hsq_layer_norm_backward")
+    return dX, dw, db

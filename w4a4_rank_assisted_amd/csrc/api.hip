@@ -5,6 +5,7 @@
 #include "hsq_internal.h"
 
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <cstdlib>
 #include <cstdint>
@@ -108,6 +109,32 @@ int calib_sizes(int K) {
   if (K < kGroup || K > kCalibMaxK) return HSQ_E_INVAL;
   if (K % kGroup != 0) return HSQ_E_SHAPE;
   return HSQ_OK;
+}
+
+// 16-bit linear: every matrix, its row length rounded up to 8, stays below
+// 2^31 bytes (32-bit buffer offsets).
+constexpr long long kLinMaxElems = 1LL << 30;
+
+int lin_sizes(int M, int K, int N) {
+  if (M < 1 || K < 1 || N < 1) return HSQ_E_INVAL;
+  const long long kp = ((long long)K + 7) / 8 * 8, np = ((long long)N + 7) / 8 * 8;
+  if (M * kp >= kLinMaxElems || K * np >= kLinMaxElems || M * np >= kLinMaxElems) return HSQ_E_INVAL;
+  return HSQ_OK;
+}
+
+bool lin_types_ok(int dtype, int y_dtype) {
+  return (dtype == HSQ_BF16 || dtype == HSQ_F16) && (y_dtype == HSQ_F32 || y_dtype == dtype);
+}
+
+bool lin_act_ok(int act) { return act >= HSQ_ACT_IDENTITY && act <= HSQ_ACT_SILU; }
+
+int norm_check(int M, int C, int groups, int x_dtype, int y_dtype, int p_dtype) {
+  auto known = [](int t) { return t == HSQ_F32 || t == HSQ_BF16 || t == HSQ_F16; };
+  if (!known(x_dtype) || !known(y_dtype) || !known(p_dtype)) return HSQ_E_INVAL;
+  if ((y_dtype != x_dtype && x_dtype != HSQ_F32) || (p_dtype != HSQ_F32 && p_dtype != y_dtype)) return HSQ_E_INVAL;
+  if (M < 1 || C < 1 || C > kNormMaxC || (long long)M * C >= INT_MAX || groups < 1 || groups > 65535)
+    return HSQ_E_INVAL;
+  return M % groups == 0 ? HSQ_OK : HSQ_E_SHAPE;
 }
 
 size_t workspace_bytes(int M, int K, int N, int r, int batch, int group) {
@@ -723,6 +750,163 @@ int hsq_closed_form_l2(const float *HL1, const double *Cinv, int K, int N, int r
   a.Tpart = (float *)workspace;
   a.K = K; a.N = N; a.r = r; a.group = group;
   return debug_check(hip_status(launch_l2(a, (hipStream_t)stream)), stream);
+}
+
+// ---------------------------------------------------------------- 16-bit linear
+
+size_t hsq_linear_workspace_bytes(int M, int K, int N) {
+  return lin_sizes(M, K, N) == HSQ_OK ? plan_linear(M, K, N).total : 0;
+}
+
+int hsq_linear(const uint16_t *X, int M, int K, int N, int dtype, const uint16_t *W,
+               const uint16_t *bias, int act, const void *residual, void *Y, int y_dtype,
+               uint16_t *Z, void *workspace, size_t ws_bytes, void *stream) {
+  const int st = lin_sizes(M, K, N);
+  if (st != HSQ_OK) return st;
+  if (!lin_types_ok(dtype, y_dtype) || !lin_act_ok(act)) return HSQ_E_INVAL;
+  if (!X || !W || !Y) return HSQ_E_INVAL;
+  const void *ptrs[] = {X, W, bias, residual, Y, Z, workspace};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return HSQ_E_ALIGN;
+  const LinPlan L = plan_linear(M, K, N);
+  if (L.total > 0 && (!workspace || ws_bytes < L.total)) return HSQ_E_WORKSPACE;
+  char *ws = (char *)workspace;
+  hipStream_t s = (hipStream_t)stream;
+  LinGemm a{};
+  a.A = X; a.lda = K;
+  a.B = W; a.ldb = N; a.b_rows = 1;
+  a.I = M; a.J = N; a.R = K;
+  a.dtype = dtype;
+  a.bias = bias; a.res = residual; a.out = Y; a.out_f32 = y_dtype == HSQ_F32; a.Z = Z; a.act = act;
+  a.part = (float *)(ws + L.part_off);
+  a.splits = L.splits;
+  hipError_t e = hipSuccess;
+  if (L.pad_x) {
+    e = launch_pad_rows(X, M, K, (uint16_t *)(ws + L.x_off), L.kp, s);
+    a.A = (const uint16_t *)(ws + L.x_off); a.lda = L.kp;
+  }
+  if (e == hipSuccess && L.pad_w) {
+    e = launch_pad_rows(W, K, N, (uint16_t *)(ws + L.w_off), L.np, s);
+    a.B = (const uint16_t *)(ws + L.w_off); a.ldb = L.np;
+  }
+  if (e == hipSuccess) e = launch_linear(a, L.skinny, s);
+  return debug_check(hip_status(e), stream);
+}
+
+size_t hsq_linear_backward_workspace_bytes(int M, int K, int N) {
+  return lin_sizes(M, K, N) == HSQ_OK ? plan_linear_backward(M, K, N).total : 0;
+}
+
+int hsq_linear_backward(const void *dY, int y_dtype, const uint16_t *X, int M, int K, int N,
+                        int dtype, const uint16_t *W, const uint16_t *Z, int act, uint16_t *dX,
+                        uint16_t *dW, uint16_t *dbias, void *workspace, size_t ws_bytes,
+                        void *stream) {
+  const int st = lin_sizes(M, K, N);
+  if (st != HSQ_OK) return st;
+  if (!lin_types_ok(dtype, y_dtype) || !lin_act_ok(act)) return HSQ_E_INVAL;
+  if (!dY || (!dX && !dW && !dbias) || (dX && !W) || (dW && !X) || !workspace) return HSQ_E_INVAL;
+  if (act != HSQ_ACT_IDENTITY && !Z) return HSQ_E_INVAL;
+  const void *ptrs[] = {dY, X, W, Z, dX, dW, dbias, workspace};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return HSQ_E_ALIGN;
+  const LinPlan L = plan_linear_backward(M, K, N);
+  if (ws_bytes < L.total) return HSQ_E_WORKSPACE;
+  char *ws = (char *)workspace;
+  hipStream_t s = (hipStream_t)stream;
+  hipError_t e = hipSuccess;
+  // dZ is dY itself where nothing changes it: no activation, the operand
+  // type, rows of whole 16-byte runs
+  const bool same = act == HSQ_ACT_IDENTITY && y_dtype == dtype && L.np == N;
+  const uint16_t *dz = same ? (const uint16_t *)dY : (const uint16_t *)(ws + L.dz_off);
+  if (dbias || !same) {
+    LinDz d{};
+    d.dY = dY; d.dy_f32 = y_dtype == HSQ_F32;
+    d.Z = act == HSQ_ACT_IDENTITY ? nullptr : Z;
+    d.dZ = same || (!dX && !dW) ? nullptr : (uint16_t *)(ws + L.dz_off);
+    d.db = dbias;
+    d.part = (float *)(ws + L.db_off);
+    d.M = M; d.N = N; d.np = L.np; d.act = act; d.dtype = dtype; d.slices = L.slices;
+    e = launch_linear_dz(d, s);
+  }
+  LinGemm a{};
+  a.dtype = dtype; a.act = HSQ_ACT_IDENTITY;
+  a.part = (float *)(ws + L.part_off);
+  if (e == hipSuccess && dX) {
+    a.A = dz; a.lda = L.np; a.a_rows = 0;
+    a.B = W; a.ldb = N; a.b_rows = 0;
+    if (L.pad_w) {
+      e = launch_pad_rows(W, K, N, (uint16_t *)(ws + L.w_off), L.np, s);
+      a.B = (const uint16_t *)(ws + L.w_off); a.ldb = L.np;
+    }
+    a.I = M; a.J = K; a.R = N;
+    a.out = dX; a.splits = L.splits_dx;
+    if (e == hipSuccess) e = launch_linear(a, false, s);
+  }
+  if (e == hipSuccess && dW) {
+    a.A = X; a.lda = K; a.a_rows = 1;
+    if (L.pad_x) {
+      e = launch_pad_rows(X, M, K, (uint16_t *)(ws + L.x_off), L.kp, s);
+      a.A = (const uint16_t *)(ws + L.x_off); a.lda = L.kp;
+    }
+    a.B = dz; a.ldb = L.np; a.b_rows = 1;
+    a.I = K; a.J = N; a.R = M;
+    a.out = dW; a.splits = L.splits_dw;
+    if (e == hipSuccess) e = launch_linear(a, false, s);
+  }
+  return debug_check(hip_status(e), stream);
+}
+
+// ---------------------------------------------------------------- layer normalisation
+
+int hsq_layer_norm(const void *X, int x_dtype, int M, int C, int groups, const void *weight,
+                   const void *bias, int p_dtype, float eps, void *Y, int y_dtype, float *mean,
+                   float *rstd, void *stream) {
+  const int st = norm_check(M, C, groups, x_dtype, y_dtype, p_dtype);
+  if (st != HSQ_OK) return st;
+  if (!X || !Y || !(eps >= 0.0f) || !(eps <= FLT_MAX)) return HSQ_E_INVAL;
+  const void *ptrs[] = {X, weight, bias, Y, mean, rstd};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return HSQ_E_ALIGN;
+  NormArgs a{};
+  a.X = X; a.w = weight; a.b = bias; a.Y = Y; a.mean = mean; a.rstd = rstd;
+  a.M = M; a.C = C; a.groups = groups; a.rows = M / groups;
+  a.x_dtype = x_dtype; a.y_dtype = y_dtype; a.p_dtype = p_dtype;
+  a.eps = eps;
+  return debug_check(hip_status(launch_layer_norm(a, (hipStream_t)stream)), stream);
+}
+
+size_t hsq_layer_norm_backward_workspace_bytes(int M, int C, int groups) {
+  if (norm_check(M, C, groups, HSQ_F32, HSQ_F32, HSQ_F32) != HSQ_OK) return 0;
+  return (size_t)norm_backward_parts(M, C, groups) * groups * 2 * C * sizeof(float);
+}
+
+int hsq_layer_norm_backward(const void *dY, int y_dtype, const void *X, int x_dtype, int M, int C,
+                            int groups, const float *mean, const float *rstd, const void *weight,
+                            int p_dtype, void *dX, void *dweight, void *dbias, void *workspace,
+                            size_t ws_bytes, void *stream) {
+  const int st = norm_check(M, C, groups, x_dtype, y_dtype, p_dtype);
+  if (st != HSQ_OK) return st;
+  if (!dY || !X || !mean || !rstd || (!dX && !dweight && !dbias)) return HSQ_E_INVAL;
+  const void *ptrs[] = {dY, X, mean, rstd, weight, dX, dweight, dbias, workspace};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return HSQ_E_ALIGN;
+  const bool params = dweight || dbias;
+  if (params && (!workspace || ws_bytes < hsq_layer_norm_backward_workspace_bytes(M, C, groups)))
+    return HSQ_E_WORKSPACE;
+  hipStream_t s = (hipStream_t)stream;
+  NormArgs a{};
+  a.dY = dY; a.X = X; a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd); a.w = weight;
+  a.dX = dX;
+  a.part = params ? (float *)workspace : nullptr;
+  a.M = M; a.C = C; a.groups = groups; a.rows = M / groups;
+  a.x_dtype = x_dtype; a.y_dtype = y_dtype; a.p_dtype = p_dtype;
+  a.parts = norm_backward_parts(M, C, groups);
+  hipError_t e = launch_layer_norm_backward(a, s);
+  if (e == hipSuccess && dweight)
+    e = launch_sum_parts(a.part, (size_t)2 * C, a.parts, groups, C, dweight, p_dtype, s);
+  if (e == hipSuccess && dbias)
+    e = launch_sum_parts(a.part + C, (size_t)2 * C, a.parts, groups, C, dbias, p_dtype, s);
+  return debug_check(hip_status(e), stream);
 }
 
 }  // extern "C"

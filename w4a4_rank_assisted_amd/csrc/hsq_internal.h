@@ -290,6 +290,85 @@ int l2_slices(int K, int N, int r);
 size_t l2_workspace_bytes(int K, int N, int r);
 hipError_t launch_l2(const L2Args &a, hipStream_t s);
 
+// ---------------------------------------------------------------------------
+// 16-bit linear (linear.hip) and layer normalisation (layer_norm.hip)
+// ---------------------------------------------------------------------------
+// Element types of the C interface (HSQ_F32, HSQ_BF16, HSQ_F16).
+constexpr int kF32 = 0, kBf16 = 1, kF16 = 2;
+constexpr int kActGelu = 2, kActSilu = 3;   // after kActIdentity, kActGeluTanh
+
+// One product out(i, j) = sum_r A(i, r) B(r, j) with its epilogue.  An
+// operand is stored either with r contiguous (A: I x lda, B: J x ldb) or
+// with r as its rows (A: R x lda, B: R x ldb); strides are multiples of 8
+// elements and the elements past R of an r-contiguous row are zero.
+struct LinGemm {
+  const uint16_t *A, *B;
+  int I, J, R, lda, ldb;
+  int a_rows, b_rows;      // 1: r runs along the rows of the stored operand
+  int dtype;               // kBf16 or kF16: A, B, bias, Z
+  // epilogue: v = sum + bias[j]; Z = v; out = act(v) + res
+  const uint16_t *bias;    // J, or null
+  const void *res;         // I x J of the output's type, or null
+  void *out;               // I x J, fp32 or dtype
+  int out_f32;
+  uint16_t *Z;             // I x J, or null
+  int act;
+  float *part;             // split partial sums (workspace)
+  int splits;
+};
+
+struct LinPlan {
+  bool skinny = false;     // weight-streaming kernel (forward, few rows)
+  int splits = 1;          // splits of the reduction (forward)
+  int splits_dx = 1, splits_dw = 1, slices = 1;   // backward: splits, row slices of the bias gradient
+  int kp = 0, np = 0;      // K and N rounded up to 8
+  bool pad_x = false, pad_w = false;
+  size_t x_off = 0, w_off = 0, dz_off = 0, part_off = 0, db_off = 0, total = 0;
+};
+
+constexpr int kLinSkinnyMaxM = 64;
+
+LinPlan plan_linear(int M, int K, int N);
+LinPlan plan_linear_backward(int M, int K, int N);
+hipError_t launch_linear(const LinGemm &a, bool skinny, hipStream_t s);
+// rows x cols (dense) -> rows x ld with zeros past cols
+hipError_t launch_pad_rows(const uint16_t *src, int rows, int cols, uint16_t *dst, int ld, hipStream_t s);
+
+struct LinDz {
+  const void *dY;          // M x N, fp32 or dtype
+  int dy_f32;
+  const uint16_t *Z;       // M x N dtype (null for the identity)
+  uint16_t *dZ;            // M x np dtype, zeros past N (null: only the column sums)
+  void *db;                // N dtype (null: not wanted)
+  float *part;             // slices x N fp32
+  int M, N, np, act, dtype, slices;
+};
+hipError_t launch_linear_dz(const LinDz &a, hipStream_t s);
+
+// Sums `parts` rows of fp32 per group in row order: dst[g][c] = sum_p
+// src[(g * parts + p) * ld + c], stored as dtype.
+hipError_t launch_sum_parts(const float *src, size_t ld, int parts, int groups, int C, void *dst, int dtype,
+                            hipStream_t s);
+
+constexpr int kNormMaxC = 16384;   // a row is held in the registers of one workgroup
+
+struct NormArgs {
+  const void *X;           // M x C
+  const void *w, *b;       // groups x C (or null)
+  void *Y;                 // M x C (forward)
+  float *mean, *rstd;      // M (forward: outputs or null; backward: inputs)
+  const void *dY;          // backward
+  void *dX;                // backward (or null)
+  float *part;             // backward: parts x groups x 2 x C fp32 (null: no parameter gradients)
+  int M, C, groups, rows;  // rows = M / groups
+  int x_dtype, y_dtype, p_dtype;
+  int parts;               // workgroups per group of the backward pass
+  float eps;
+};
+int norm_backward_parts(int M, int C, int groups);
+hipError_t launch_layer_norm(const NormArgs &a, hipStream_t s);
+hipError_t launch_layer_norm_backward(const NormArgs &a, hipStream_t s);
+
 }  // namespace hsq
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,345 @@
+// layer_norm.hip -- layer normalisation over the last dimension, forward and
+// backward, for 16-bit and fp32 rows.
+//
+//   mean = (1/C) sum_c x,  rstd = (mean of (x - mean)^2 + eps)^(-1/2)
+//   y    = (x - mean) rstd w + b
+// and, with xh = (x - mean) rstd and g = dy w,
+//   dx   = rstd (g - mean_c(g) - xh mean_c(g xh))
+//   dw   = sum over the rows of a group of dy xh,  db = sum of dy.
+//
+// Both passes are bound by HBM: a row is read once into registers (the
+// variance is summed from the registers around the finished mean, so a
+// large common offset costs no precision) and written once.  A row belongs
+// to one wave, four waves or eight, the fewest whose registers hold it.
+// Statistics and parameter sums are fp32.
+#include "hsq_internal.h"
+
+#include <algorithm>
+
+namespace hsq {
+
+namespace {
+
+// Eight consecutive elements of a row.  Rows of a length that is no
+// multiple of 8 start at any element, so the 16-byte accesses are typed
+// with the element's alignment (global memory takes them as they come).
+struct __attribute__((packed, aligned(2))) V16 { uint32_t d[4]; };
+struct __attribute__((packed, aligned(4))) V32 { float f[8]; };
+
+template <int DT>
+__device__ __forceinline__ float elem(const void *p, size_t i) {
+  if constexpr (DT == kF32) return static_cast<const float *>(p)[i];
+  const uint16_t h = static_cast<const uint16_t *>(p)[i];
+  if constexpr (DT == kBf16) return bf16_to_f32(h);
+  return f16_to_f32(h);
+}
+
+template <int DT>
+__device__ __forceinline__ void put(void *p, size_t i, float v) {
+  if constexpr (DT == kF32) static_cast<float *>(p)[i] = v;
+  if constexpr (DT == kBf16) static_cast<__bf16 *>(p)[i] = (__bf16)v;
+  if constexpr (DT == kF16) static_cast<_Float16 *>(p)[i] = (_Float16)v;
+}
+
+// n of the eight elements from i on exist; the others read 0
+template <int DT>
+__device__ __forceinline__ void load8(const void *p, size_t i, int n, float v[8]) {
+  if (n >= 8) {
+    if constexpr (DT == kF32) {
+      const V32 t = *reinterpret_cast<const V32 *>(static_cast<const float *>(p) + i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = t.f[e];
+    } else {
+      const V16 t = *reinterpret_cast<const V16 *>(static_cast<const uint16_t *>(p) + i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t h = (t.d[e / 2] >> (16 * (e & 1))) & 0xFFFFu;
+        v[e] = DT == kBf16 ? bf16_to_f32(h) : f16_to_f32((uint16_t)h);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < n ? elem<DT>(p, i + e) : 0.0f;
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void *p, size_t i, int n, const float v[8]) {
+  if (n >= 8) {
+    if constexpr (DT == kF32) {
+      V32 t;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t.f[e] = v[e];
+      *reinterpret_cast<V32 *>(static_cast<float *>(p) + i) = t;
+    } else {
+      uint16_t h[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) put<DT>(h, e, v[e]);
+      V16 t;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t.d[e] = (uint32_t)h[2 * e] | ((uint32_t)h[2 * e + 1] << 16);
+      *reinterpret_cast<V16 *>(static_cast<uint16_t *>(p) + i) = t;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) put<DT>(p, i + e, v[e]);
+  }
+}
+
+// parameters are fp32 or of the 16-bit type of Y
+template <int DT>
+__device__ __forceinline__ void load8p(const void *p, bool f32, size_t i, int n, float v[8]) {
+  if (f32) load8<kF32>(p, i, n, v);
+  else load8<DT>(p, i, n, v);
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+  v = row16_sum(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// Sum over the W waves of a row; every lane of the row returns it.  Two
+// sums of one row alternate between two LDS slots, so one barrier each.
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float *slot, int wave) {
+  v = wave_sum(v);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) slot[wave] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) v += slot[w];
+  }
+  return v;
+}
+
+constexpr int kRowThreads = 256;   // threads of a workgroup with one or four waves to a row
+
+template <int W>
+constexpr int norm_threads() { return W > 4 ? W * 64 : kRowThreads; }
+
+// W waves to a row, NV runs of 8 elements to a lane: C <= 512 W NV.
+template <int TX, int TY, int W, int NV>
+__global__ __launch_bounds__(norm_threads<W>()) void k_layer_norm(NormArgs a) {
+  constexpr int RPB = norm_threads<W>() / (64 * W);     // rows per workgroup
+  __shared__ float red[2][W > 1 ? W : 1];
+  const int t = threadIdx.x % (64 * W), wave = t >> 6;
+  const size_t row = (size_t)blockIdx.x * RPB + threadIdx.x / (64 * W);
+  if (RPB > 1 && row >= (size_t)a.M) return;            // whole waves, and no barrier with W = 1
+  const size_t base = row * a.C;
+  float x[NV][8];
+  float s = 0.0f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = 8 * (t + v * 64 * W);
+    load8<TX>(a.X, base + c, a.C - c, x[v]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += x[v][e];
+  }
+  const float mean = row_sum<W>(s, red[0], wave) / (float)a.C;
+  float q = 0.0f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = 8 * (t + v * 64 * W);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float d = c + e < a.C ? x[v][e] - mean : 0.0f;
+      q = fmaf(d, d, q);
+    }
+  }
+  const float rstd = 1.0f / sqrtf(row_sum<W>(q, red[1], wave) / (float)a.C + a.eps);
+  if (t == 0) {
+    if (a.mean) a.mean[row] = mean;
+    if (a.rstd) a.rstd[row] = rstd;
+  }
+  const size_t g = (size_t)((int)row / a.rows) * a.C;
+  const bool pf = a.p_dtype == kF32;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = 8 * (t + v * 64 * W), n = a.C - c;
+    if (n <= 0) continue;
+    float y[8], p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = (x[v][e] - mean) * rstd;
+    if (a.w) {
+      load8p<TY>(a.w, pf, g + c, n, p);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= p[e];
+    }
+    if (a.b) {
+      load8p<TY>(a.b, pf, g + c, n, p);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] += p[e];
+    }
+    store8<TY>(a.Y, base + c, n, y);
+  }
+}
+
+// Backward: workgroup p of group gi takes rows p, p + parts, ... of the
+// group (RPB at a time where a row is one wave's), keeps its columns' sums of
+// dy xh and dy in registers and writes them as one partial row; the partial
+// rows are summed by k_sum_parts.
+template <int TX, int TY, int W, int NV>
+__global__ __launch_bounds__(norm_threads<W>()) void k_layer_norm_bwd(NormArgs a) {
+  constexpr int NT = norm_threads<W>(), RPB = NT / (64 * W);
+  __shared__ float red[4][W > 1 ? W : 1];
+  __shared__ float comb[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? 512 * 2 : 1];
+  const int t = threadIdx.x % (64 * W), wave = t >> 6, sub = threadIdx.x / (64 * W);
+  const int gi = blockIdx.y;
+  const size_t g = (size_t)gi * a.C;
+  const bool pf = a.p_dtype == kF32;
+  float w[NV][8], dw[NV][8], db[NV][8];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = 8 * (t + v * 64 * W);
+    if (a.w) load8p<TY>(a.w, pf, g + c, a.C - c, w[v]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (!a.w) w[v][e] = 1.0f;
+      dw[v][e] = db[v][e] = 0.0f;
+    }
+  }
+  int turn = 0;
+  for (int r = blockIdx.x * RPB + sub; r < a.rows; r += gridDim.x * RPB, turn ^= 2) {
+    const size_t row = (size_t)gi * a.rows + r, base = row * a.C;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float xh[NV][8], gr[NV][8];
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = 8 * (t + v * 64 * W);
+      load8<TX>(a.X, base + c, a.C - c, xh[v]);
+      load8<TY>(a.dY, base + c, a.C - c, gr[v]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float h = c + e < a.C ? (xh[v][e] - mean) * rstd : 0.0f;
+        const float dy = gr[v][e];
+        dw[v][e] = fmaf(dy, h, dw[v][e]);
+        db[v][e] += dy;
+        xh[v][e] = h;
+        gr[v][e] = dy * w[v][e];
+        s1 += gr[v][e];
+        s2 = fmaf(gr[v][e], h, s2);
+      }
+    }
+    if (a.dX) {
+      const float c1 = row_sum<W>(s1, red[turn], wave) / (float)a.C;
+      const float c2 = row_sum<W>(s2, red[turn + 1], wave) / (float)a.C;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = 8 * (t + v * 64 * W);
+        if (a.C - c <= 0) continue;
+        float d[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] = rstd * (gr[v][e] - c1 - xh[v][e] * c2);
+        store8<TX>(a.dX, base + c, a.C - c, d);
+      }
+    }
+  }
+  if (!a.part) return;
+  // the workgroup's rows in order of its waves (one wave to a row), 512 columns at a time
+  float *out = a.part + ((size_t)gi * a.parts + blockIdx.x) * 2 * a.C;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = 8 * (t + v * 64 * W), n = a.C - c;
+    if constexpr (RPB > 1) {
+      __syncthreads();
+      if (sub > 0)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          comb[sub - 1][e * 64 + t] = dw[v][e];
+          comb[sub - 1][512 + e * 64 + t] = db[v][e];
+        }
+      __syncthreads();
+      if (sub == 0)
+        for (int k = 0; k < RPB - 1; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            dw[v][e] += comb[k][e * 64 + t];
+            db[v][e] += comb[k][512 + e * 64 + t];
+          }
+    }
+    if (sub == 0 && n > 0) {
+      store8<kF32>(out, c, n, dw[v]);
+      store8<kF32>(out, (size_t)a.C + c, n, db[v]);
+    }
+  }
+}
+
+// One thread per column and 1/8 of the partial rows; eight shares summed
+// in order through LDS.
+constexpr int kSumCols = 32, kSumShares = 8;
+__global__ __launch_bounds__(kSumCols * kSumShares) void k_sum_parts(const float *src, size_t ld, int parts, int C,
+                                                                     void *dst, int dtype) {
+  __shared__ float sh[kSumShares][kSumCols];
+  const int cx = threadIdx.x % kSumCols, y = threadIdx.x / kSumCols;
+  const int c = blockIdx.x * kSumCols + cx, g = blockIdx.y;
+  float s = 0.0f;
+  if (c < C)
+    for (int p = y; p < parts; p += kSumShares) s += src[((size_t)g * parts + p) * ld + c];
+  sh[y][cx] = s;
+  __syncthreads();
+  if (y == 0 && c < C) {
+#pragma unroll
+    for (int k = 1; k < kSumShares; ++k) s += sh[k][cx];
+    const size_t o = (size_t)g * C + c;
+    if (dtype == kF32) put<kF32>(dst, o, s);
+    else if (dtype == kBf16) put<kBf16>(dst, o, s);
+    else put<kF16>(dst, o, s);
+  }
+}
+
+template <int TX, int TY, int W, int NV>
+hipError_t run_norm(const NormArgs &a, bool backward, hipStream_t s) {
+  constexpr int RPB = norm_threads<W>() / (64 * W);
+  if (backward)
+    hipLaunchKernelGGL((k_layer_norm_bwd<TX, TY, W, NV>), dim3((unsigned)a.parts, (unsigned)a.groups),
+                       dim3(norm_threads<W>()), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_layer_norm<TX, TY, W, NV>), dim3((unsigned)ceil_div(a.M, RPB)), dim3(norm_threads<W>()), 0,
+                       s, a);
+  return hipGetLastError();
+}
+
+template <int TX, int TY>
+hipError_t pick_width(const NormArgs &a, bool backward, hipStream_t s) {
+  if (a.C <= 512) return run_norm<TX, TY, 1, 1>(a, backward, s);
+  if (a.C <= 1024) return run_norm<TX, TY, 1, 2>(a, backward, s);
+  if (a.C <= 1536) return run_norm<TX, TY, 1, 3>(a, backward, s);
+  if (a.C <= 2048) return run_norm<TX, TY, 4, 1>(a, backward, s);
+  if (a.C <= 4096) return run_norm<TX, TY, 4, 2>(a, backward, s);
+  if (a.C <= 8192) return run_norm<TX, TY, 4, 4>(a, backward, s);
+  return run_norm<TX, TY, 8, 4>(a, backward, s);
+}
+
+hipError_t pick_types(const NormArgs &a, bool backward, hipStream_t s) {
+  if (a.x_dtype == kBf16) return pick_width<kBf16, kBf16>(a, backward, s);
+  if (a.x_dtype == kF16) return pick_width<kF16, kF16>(a, backward, s);
+  if (a.y_dtype == kBf16) return pick_width<kF32, kBf16>(a, backward, s);
+  if (a.y_dtype == kF16) return pick_width<kF32, kF16>(a, backward, s);
+  return pick_width<kF32, kF32>(a, backward, s);
+}
+
+}  // namespace
+
+// Workgroups per group of the backward pass: about four per CU over all
+// groups, at least 8 rows (two per wave of a four-row workgroup) each.
+int norm_backward_parts(int M, int C, int groups) {
+  const int rows = M / groups;
+  const int rpb = C <= 1536 ? 4 : 1;
+  return std::max(1, std::min(ceil_div(rows, 2 * rpb), std::max(1, 1024 / groups)));
+}
+
+hipError_t launch_layer_norm(const NormArgs &a, hipStream_t s) { return pick_types(a, false, s); }
+hipError_t launch_layer_norm_backward(const NormArgs &a, hipStream_t s) { return pick_types(a, true, s); }
+
+hipError_t launch_sum_parts(const float *src, size_t ld, int parts, int groups, int C, void *dst, int dtype,
+                            hipStream_t s) {
+  hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)ceil_div(C, kSumCols), (unsigned)groups),
+                     dim3(kSumCols * kSumShares), 0, s, src, ld, parts, C, dst, dtype);
+  return hipGetLastError();
+}
+
+}  // namespace hsq
