@@ -774,21 +774,24 @@ int hsq_linear(const uint16_t *X, int M, int K, int N, int dtype, const uint16_t
   hipStream_t s = (hipStream_t)stream;
   LinGemm a{};
   a.A = X; a.lda = K;
-  a.B = W; a.ldb = N; a.b_rows = 1;
+  a.B = W; a.ldb = N;
   a.I = M; a.J = N; a.R = K;
   a.dtype = dtype;
   a.bias = bias; a.res = residual; a.out = Y; a.out_f32 = y_dtype == HSQ_F32; a.Z = Z; a.act = act;
   a.part = (float *)(ws + L.part_off);
   a.splits = L.splits;
-  hipError_t e = hipSuccess;
+  LinPrep p{};
   if (L.pad_x) {
-    e = launch_pad_rows(X, M, K, (uint16_t *)(ws + L.x_off), L.kp, s);
-    a.A = (const uint16_t *)(ws + L.x_off); a.lda = L.kp;
+    p.X = X; p.x_rows = M; p.x_cols = K; p.x_ld = L.kp;
+    p.Xp = (uint16_t *)(ws + L.x_off);
+    a.A = p.Xp; a.lda = L.kp;
   }
-  if (e == hipSuccess && L.pad_w) {
-    e = launch_pad_rows(W, K, N, (uint16_t *)(ws + L.w_off), L.np, s);
-    a.B = (const uint16_t *)(ws + L.w_off); a.ldb = L.np;
+  if (L.pad_w) {
+    p.W = W; p.w_rows = K; p.w_cols = N; p.w_ld = L.np;
+    p.Wp = (uint16_t *)(ws + L.w_off);
+    a.B = p.Wp; a.ldb = L.np;
   }
+  hipError_t e = launch_linear_prep(p, dtype, s);
   if (e == hipSuccess) e = launch_linear(a, L.skinny, s);
   return debug_check(hip_status(e), stream);
 }
@@ -813,46 +816,49 @@ int hsq_linear_backward(const void *dY, int y_dtype, const uint16_t *X, int M, i
   if (ws_bytes < L.total) return HSQ_E_WORKSPACE;
   char *ws = (char *)workspace;
   hipStream_t s = (hipStream_t)stream;
-  hipError_t e = hipSuccess;
   // dZ is dY itself where nothing changes it: no activation, the operand
   // type, rows of whole 16-byte runs
   const bool same = act == HSQ_ACT_IDENTITY && y_dtype == dtype && L.np == N;
   const uint16_t *dz = same ? (const uint16_t *)dY : (const uint16_t *)(ws + L.dz_off);
-  if (dbias || !same) {
-    LinDz d{};
+  LinPrep p{};
+  LinGemm x{}, w{};
+  if (dX) {
+    x.dtype = dtype;
+    x.A = dz; x.lda = L.np;
+    x.B = W; x.ldb = N;
+    if (L.pad_w) {
+      p.W = W; p.w_rows = K; p.w_cols = N; p.w_ld = L.np;
+      p.Wp = (uint16_t *)(ws + L.w_off);
+      x.B = p.Wp; x.ldb = L.np;
+    }
+    x.I = M; x.J = K; x.R = N;
+    x.out = dX; x.splits = L.splits_dx;
+    x.part = (float *)(ws + L.part_off);
+  }
+  if (dW) {
+    w.dtype = dtype;
+    w.A = X; w.lda = K;
+    if (L.pad_x) {
+      p.X = X; p.x_rows = M; p.x_cols = K; p.x_ld = L.kp;
+      p.Xp = (uint16_t *)(ws + L.x_off);
+      w.A = p.Xp; w.lda = L.kp;
+    }
+    w.B = dz; w.ldb = L.np;
+    w.I = K; w.J = N; w.R = M;
+    w.out = dW; w.splits = L.splits_dw;
+    w.part = (float *)(ws + L.part_w_off);
+  }
+  if (dbias || (!same && (dX || dW))) {
+    LinDz &d = p.dz;
     d.dY = dY; d.dy_f32 = y_dtype == HSQ_F32;
     d.Z = act == HSQ_ACT_IDENTITY ? nullptr : Z;
     d.dZ = same || (!dX && !dW) ? nullptr : (uint16_t *)(ws + L.dz_off);
     d.db = dbias;
     d.part = (float *)(ws + L.db_off);
     d.M = M; d.N = N; d.np = L.np; d.act = act; d.dtype = dtype; d.slices = L.slices;
-    e = launch_linear_dz(d, s);
   }
-  LinGemm a{};
-  a.dtype = dtype; a.act = HSQ_ACT_IDENTITY;
-  a.part = (float *)(ws + L.part_off);
-  if (e == hipSuccess && dX) {
-    a.A = dz; a.lda = L.np; a.a_rows = 0;
-    a.B = W; a.ldb = N; a.b_rows = 0;
-    if (L.pad_w) {
-      e = launch_pad_rows(W, K, N, (uint16_t *)(ws + L.w_off), L.np, s);
-      a.B = (const uint16_t *)(ws + L.w_off); a.ldb = L.np;
-    }
-    a.I = M; a.J = K; a.R = N;
-    a.out = dX; a.splits = L.splits_dx;
-    if (e == hipSuccess) e = launch_linear(a, false, s);
-  }
-  if (e == hipSuccess && dW) {
-    a.A = X; a.lda = K; a.a_rows = 1;
-    if (L.pad_x) {
-      e = launch_pad_rows(X, M, K, (uint16_t *)(ws + L.x_off), L.kp, s);
-      a.A = (const uint16_t *)(ws + L.x_off); a.lda = L.kp;
-    }
-    a.B = dz; a.ldb = L.np; a.b_rows = 1;
-    a.I = K; a.J = N; a.R = M;
-    a.out = dW; a.splits = L.splits_dw;
-    if (e == hipSuccess) e = launch_linear(a, false, s);
-  }
+  hipError_t e = launch_linear_prep(p, dtype, s);
+  if (e == hipSuccess && (dX || dW)) e = launch_linear_backward(x, w, s);
   return debug_check(hip_status(e), stream);
 }
 
@@ -902,10 +908,8 @@ int hsq_layer_norm_backward(const void *dY, int y_dtype, const void *X, int x_dt
   a.x_dtype = x_dtype; a.y_dtype = y_dtype; a.p_dtype = p_dtype;
   a.parts = norm_backward_parts(M, C, groups);
   hipError_t e = launch_layer_norm_backward(a, s);
-  if (e == hipSuccess && dweight)
-    e = launch_sum_parts(a.part, (size_t)2 * C, a.parts, groups, C, dweight, p_dtype, s);
-  if (e == hipSuccess && dbias)
-    e = launch_sum_parts(a.part + C, (size_t)2 * C, a.parts, groups, C, dbias, p_dtype, s);
+  if (e == hipSuccess && params)
+    e = launch_sum_parts(SumArgs{a.part, (size_t)2 * C, a.parts, C, dweight, dbias, p_dtype}, groups, s);
   return debug_check(hip_status(e), stream);
 }
 

@@ -304,7 +304,6 @@ constexpr int kActGelu = 2, kActSilu = 3;   // after kActIdentity, kActGeluTanh
 struct LinGemm {
   const uint16_t *A, *B;
   int I, J, R, lda, ldb;
-  int a_rows, b_rows;      // 1: r runs along the rows of the stored operand
   int dtype;               // kBf16 or kF16: A, B, bias, Z
   // epilogue: v = sum + bias[j]; Z = v; out = act(v) + res
   const uint16_t *bias;    // J, or null
@@ -315,6 +314,9 @@ struct LinGemm {
   int act;
   float *part;             // split partial sums (workspace)
   int splits;
+  // units of the launch (set there): nbi x nbj tiles of 256 x 256, of which
+  // `full` whole, the others in `cut` parts, `parts` units in all
+  int nbi, nbj, full, cut, parts;
 };
 
 struct LinPlan {
@@ -323,16 +325,18 @@ struct LinPlan {
   int splits_dx = 1, splits_dw = 1, slices = 1;   // backward: splits, row slices of the bias gradient
   int kp = 0, np = 0;      // K and N rounded up to 8
   bool pad_x = false, pad_w = false;
-  size_t x_off = 0, w_off = 0, dz_off = 0, part_off = 0, db_off = 0, total = 0;
+  size_t x_off = 0, w_off = 0, dz_off = 0, part_off = 0, part_w_off = 0, db_off = 0, total = 0;
 };
 
 constexpr int kLinSkinnyMaxM = 64;
 
 LinPlan plan_linear(int M, int K, int N);
 LinPlan plan_linear_backward(int M, int K, int N);
+// Forward: A = X with r contiguous, B = W with r as rows.
 hipError_t launch_linear(const LinGemm &a, bool skinny, hipStream_t s);
-// rows x cols (dense) -> rows x ld with zeros past cols
-hipError_t launch_pad_rows(const uint16_t *src, int rows, int cols, uint16_t *dst, int ld, hipStream_t s);
+// Backward, each with out == nullptr where not wanted: dX = dZ W^T (both
+// operands r-contiguous) and dW = X^T dZ (both with r as rows).
+hipError_t launch_linear_backward(const LinGemm &dx, const LinGemm &dw, hipStream_t s);
 
 struct LinDz {
   const void *dY;          // M x N, fp32 or dtype
@@ -343,12 +347,30 @@ struct LinDz {
   float *part;             // slices x N fp32
   int M, N, np, act, dtype, slices;
 };
-hipError_t launch_linear_dz(const LinDz &a, hipStream_t s);
 
-// Sums `parts` rows of fp32 per group in row order: dst[g][c] = sum_p
-// src[(g * parts + p) * ld + c], stored as dtype.
-hipError_t launch_sum_parts(const float *src, size_t ld, int parts, int groups, int C, void *dst, int dtype,
-                            hipStream_t s);
+// What the products read that is not there yet: X and W with rows of a
+// multiple of 8 (src null: not needed), dZ and the bias gradient (dY null: not
+// needed).
+struct LinPrep {
+  const uint16_t *X, *W;
+  uint16_t *Xp, *Wp;
+  int x_rows, x_cols, x_ld, w_rows, w_cols, w_ld;
+  LinDz dz;
+  int x_blocks, w_blocks;  // set by the launch
+};
+hipError_t launch_linear_prep(LinPrep p, int dtype, hipStream_t s);
+
+// Sums of fp32 partial rows of stride ld, `parts` of them per group, columns 0
+// .. C - 1 into dst and columns C .. 2 C - 1 into dst2 (either null: not
+// wanted), groups x C of dtype.
+struct SumArgs {
+  const float *src;
+  size_t ld;
+  int parts, C;
+  void *dst, *dst2;
+  int dtype;
+};
+hipError_t launch_sum_parts(const SumArgs &a, int groups, hipStream_t s);
 
 constexpr int kNormMaxC = 16384;   // a row is held in the registers of one workgroup
 

@@ -27,40 +27,52 @@ struct __attribute__((packed, aligned(2))) V16 { uint32_t d[4]; };
 struct __attribute__((packed, aligned(4))) V32 { float f[8]; };
 
 template <int DT>
-__device__ __forceinline__ float elem(const void *p, size_t i) {
-  if constexpr (DT == kF32) return static_cast<const float *>(p)[i];
-  const uint16_t h = static_cast<const uint16_t *>(p)[i];
-  if constexpr (DT == kBf16) return bf16_to_f32(h);
-  return f16_to_f32(h);
-}
-
-template <int DT>
 __device__ __forceinline__ void put(void *p, size_t i, float v) {
   if constexpr (DT == kF32) static_cast<float *>(p)[i] = v;
   if constexpr (DT == kBf16) static_cast<__bf16 *>(p)[i] = (__bf16)v;
   if constexpr (DT == kF16) static_cast<_Float16 *>(p)[i] = (_Float16)v;
 }
 
-// n of the eight elements from i on exist; the others read 0
+// Eight elements as loaded; n of them from i on exist, the others read 0.
 template <int DT>
-__device__ __forceinline__ void load8(const void *p, size_t i, int n, float v[8]) {
+struct Run { uint32_t d[DT == kF32 ? 8 : 4]; };
+
+template <int DT>
+__device__ __forceinline__ Run<DT> load_run(const void *p, size_t i, int n) {
+  Run<DT> r{};
   if (n >= 8) {
     if constexpr (DT == kF32) {
       const V32 t = *reinterpret_cast<const V32 *>(static_cast<const float *>(p) + i);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = t.f[e];
+      for (int e = 0; e < 8; ++e) r.d[e] = __float_as_uint(t.f[e]);
     } else {
       const V16 t = *reinterpret_cast<const V16 *>(static_cast<const uint16_t *>(p) + i);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t h = (t.d[e / 2] >> (16 * (e & 1))) & 0xFFFFu;
-        v[e] = DT == kBf16 ? bf16_to_f32(h) : f16_to_f32((uint16_t)h);
-      }
+      for (int e = 0; e < 4; ++e) r.d[e] = t.d[e];
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? elem<DT>(p, i + e) : 0.0f;
+    for (int e = 0; e < 8; ++e)
+      if (e < n) {
+        if constexpr (DT == kF32) r.d[e] = static_cast<const uint32_t *>(p)[i + e];
+        else r.d[e / 2] |= (uint32_t)static_cast<const uint16_t *>(p)[i + e] << (16 * (e & 1));
+      }
   }
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ float value(const Run<DT> &r, int e) {
+  if constexpr (DT == kF32) return __uint_as_float(r.d[e]);
+  const uint32_t h = (r.d[e / 2] >> (16 * (e & 1))) & 0xFFFFu;
+  return DT == kBf16 ? bf16_to_f32(h) : f16_to_f32((uint16_t)h);
+}
+
+template <int DT>
+__device__ __forceinline__ void load8(const void *p, size_t i, int n, float v[8]) {
+  const Run<DT> r = load_run<DT>(p, i, n);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = value<DT>(r, e);
 }
 
 template <int DT>
@@ -129,15 +141,26 @@ __global__ __launch_bounds__(norm_threads<W>()) void k_layer_norm(NormArgs a) {
   const size_t row = (size_t)blockIdx.x * RPB + threadIdx.x / (64 * W);
   if (RPB > 1 && row >= (size_t)a.M) return;            // whole waves, and no barrier with W = 1
   const size_t base = row * a.C;
-  float x[NV][8];
+  const size_t g = (size_t)((int)row / a.rows) * a.C;
+  const bool pf = a.p_dtype == kF32;
+  // the parameters travel with the row, not behind its statistics
+  float x[NV][8], w[NV][8], b[NV][8];
   float s = 0.0f;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = 8 * (t + v * 64 * W);
     load8<TX>(a.X, base + c, a.C - c, x[v]);
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = 8 * (t + v * 64 * W);
+    if (a.w) load8p<TY>(a.w, pf, g + c, a.C - c, w[v]);
+    if (a.b) load8p<TY>(a.b, pf, g + c, a.C - c, b[v]);
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
 #pragma unroll
     for (int e = 0; e < 8; ++e) s += x[v][e];
-  }
   const float mean = row_sum<W>(s, red[0], wave) / (float)a.C;
   float q = 0.0f;
 #pragma unroll
@@ -154,24 +177,20 @@ __global__ __launch_bounds__(norm_threads<W>()) void k_layer_norm(NormArgs a) {
     if (a.mean) a.mean[row] = mean;
     if (a.rstd) a.rstd[row] = rstd;
   }
-  const size_t g = (size_t)((int)row / a.rows) * a.C;
-  const bool pf = a.p_dtype == kF32;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int c = 8 * (t + v * 64 * W), n = a.C - c;
     if (n <= 0) continue;
-    float y[8], p[8];
+    float y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = (x[v][e] - mean) * rstd;
     if (a.w) {
-      load8p<TY>(a.w, pf, g + c, n, p);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= p[e];
+      for (int e = 0; e < 8; ++e) y[e] *= w[v][e];
     }
     if (a.b) {
-      load8p<TY>(a.b, pf, g + c, n, p);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] += p[e];
+      for (int e = 0; e < 8; ++e) y[e] += b[v][e];
     }
     store8<TY>(a.Y, base + c, n, y);
   }
@@ -180,10 +199,15 @@ __global__ __launch_bounds__(norm_threads<W>()) void k_layer_norm(NormArgs a) {
 // Backward: workgroup p of group gi takes rows p, p + parts, ... of the
 // group (RPB at a time where a row is one wave's), keeps its columns' sums of
 // dy xh and dy in registers and writes them as one partial row; the partial
-// rows are summed by k_sum_parts.
+// rows are summed by k_sum_parts.  The next row is loaded while this one is
+// worked on, where the registers allow it (NV < 4).
+constexpr int kBwdThreads = 512;
+template <int W>
+constexpr int bwd_rows() { return W > 1 ? 1 : kBwdThreads / 64; }
+
 template <int TX, int TY, int W, int NV>
-__global__ __launch_bounds__(norm_threads<W>()) void k_layer_norm_bwd(NormArgs a) {
-  constexpr int NT = norm_threads<W>(), RPB = NT / (64 * W);
+__global__ __launch_bounds__(64 * W * bwd_rows<W>()) void k_layer_norm_bwd(NormArgs a) {
+  constexpr int RPB = bwd_rows<W>();
   __shared__ float red[4][W > 1 ? W : 1];
   __shared__ float comb[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? 512 * 2 : 1];
   const int t = threadIdx.x % (64 * W), wave = t >> 6, sub = threadIdx.x / (64 * W);
@@ -201,21 +225,38 @@ __global__ __launch_bounds__(norm_threads<W>()) void k_layer_norm_bwd(NormArgs a
       dw[v][e] = db[v][e] = 0.0f;
     }
   }
-  int turn = 0;
-  for (int r = blockIdx.x * RPB + sub; r < a.rows; r += gridDim.x * RPB, turn ^= 2) {
+  constexpr bool kAhead = NV < 4;
+  Run<TX> nx[NV];
+  Run<TY> ny[NV];
+  float nmean = 0.0f, nrstd = 0.0f;
+  auto fetch = [&](int r) __attribute__((always_inline)) {
     const size_t row = (size_t)gi * a.rows + r, base = row * a.C;
-    const float mean = a.mean[row], rstd = a.rstd[row];
+    nmean = a.mean[row];
+    nrstd = a.rstd[row];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = 8 * (t + v * 64 * W);
+      nx[v] = load_run<TX>(a.X, base + c, a.C - c);
+      ny[v] = load_run<TY>(a.dY, base + c, a.C - c);
+    }
+  };
+  const int stride = gridDim.x * RPB;
+  int turn = 0;
+  int r = blockIdx.x * RPB + sub;
+  if (kAhead && r < a.rows) fetch(r);
+  for (; r < a.rows; r += stride, turn ^= 2) {
+    if (!kAhead) fetch(r);
+    const size_t base = ((size_t)gi * a.rows + r) * a.C;
+    const float mean = nmean, rstd = nrstd;
     float xh[NV][8], gr[NV][8];
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = 8 * (t + v * 64 * W);
-      load8<TX>(a.X, base + c, a.C - c, xh[v]);
-      load8<TY>(a.dY, base + c, a.C - c, gr[v]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float h = c + e < a.C ? (xh[v][e] - mean) * rstd : 0.0f;
-        const float dy = gr[v][e];
+        const float h = c + e < a.C ? (value<TX>(nx[v], e) - mean) * rstd : 0.0f;
+        const float dy = value<TY>(ny[v], e);
         dw[v][e] = fmaf(dy, h, dw[v][e]);
         db[v][e] += dy;
         xh[v][e] = h;
@@ -224,6 +265,7 @@ __global__ __launch_bounds__(norm_threads<W>()) void k_layer_norm_bwd(NormArgs a
         s2 = fmaf(gr[v][e], h, s2);
       }
     }
+    if (kAhead && r + stride < a.rows) fetch(r + stride);
     if (a.dX) {
       const float c1 = row_sum<W>(s1, red[turn], wave) / (float)a.C;
       const float c2 = row_sum<W>(s2, red[turn + 1], wave) / (float)a.C;
@@ -268,27 +310,38 @@ __global__ __launch_bounds__(norm_threads<W>()) void k_layer_norm_bwd(NormArgs a
   }
 }
 
-// One thread per column and 1/8 of the partial rows; eight shares summed
-// in order through LDS.
-constexpr int kSumCols = 32, kSumShares = 8;
-__global__ __launch_bounds__(kSumCols * kSumShares) void k_sum_parts(const float *src, size_t ld, int parts, int C,
-                                                                     void *dst, int dtype) {
-  __shared__ float sh[kSumShares][kSumCols];
+// Sums of partial rows: 32 columns per workgroup, 32 shares of the rows each
+// with four rows in flight, the shares summed in order.  Grid z: the
+// second half of a partial row (the norm's db beside dw).
+constexpr int kSumCols = 32, kSumShares = 32;
+__global__ __launch_bounds__(kSumCols * kSumShares) void k_sum_parts(SumArgs a) {
+  __shared__ float sh[kSumShares][kSumCols + 1];
+  void *dst = blockIdx.z == 0 ? a.dst : a.dst2;
   const int cx = threadIdx.x % kSumCols, y = threadIdx.x / kSumCols;
   const int c = blockIdx.x * kSumCols + cx, g = blockIdx.y;
-  float s = 0.0f;
-  if (c < C)
-    for (int p = y; p < parts; p += kSumShares) s += src[((size_t)g * parts + p) * ld + c];
-  sh[y][cx] = s;
-  __syncthreads();
-  if (y == 0 && c < C) {
+  const float *src = a.src + (size_t)g * a.parts * a.ld + (blockIdx.z == 0 ? 0 : a.C) + c;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < a.C) {
+    int p = y;
+    for (; p + 3 * kSumShares < a.parts; p += 4 * kSumShares) {
+      float v[4];
 #pragma unroll
-    for (int k = 1; k < kSumShares; ++k) s += sh[k][cx];
-    const size_t o = (size_t)g * C + c;
-    if (dtype == kF32) put<kF32>(dst, o, s);
-    else if (dtype == kBf16) put<kBf16>(dst, o, s);
-    else put<kF16>(dst, o, s);
+      for (int k = 0; k < 4; ++k) v[k] = src[(size_t)(p + k * kSumShares) * a.ld];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += v[k];
+    }
+    for (; p < a.parts; p += kSumShares) s[0] += src[(size_t)p * a.ld];
   }
+  sh[y][cx] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (y != 0 || c >= a.C) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kSumShares; ++k) v += sh[k][cx];
+  const size_t o = (size_t)g * a.C + c;
+  if (a.dtype == kF32) put<kF32>(dst, o, v);
+  else if (a.dtype == kBf16) put<kBf16>(dst, o, v);
+  else put<kF16>(dst, o, v);
 }
 
 template <int TX, int TY, int W, int NV>
@@ -296,7 +349,7 @@ hipError_t run_norm(const NormArgs &a, bool backward, hipStream_t s) {
   constexpr int RPB = norm_threads<W>() / (64 * W);
   if (backward)
     hipLaunchKernelGGL((k_layer_norm_bwd<TX, TY, W, NV>), dim3((unsigned)a.parts, (unsigned)a.groups),
-                       dim3(norm_threads<W>()), 0, s, a);
+                       dim3(64 * W * bwd_rows<W>()), 0, s, a);
   else
     hipLaunchKernelGGL((k_layer_norm<TX, TY, W, NV>), dim3((unsigned)ceil_div(a.M, RPB)), dim3(norm_threads<W>()), 0,
                        s, a);
@@ -310,7 +363,7 @@ hipError_t pick_width(const NormArgs &a, bool backward, hipStream_t s) {
   if (a.C <= 1536) return run_norm<TX, TY, 1, 3>(a, backward, s);
   if (a.C <= 2048) return run_norm<TX, TY, 4, 1>(a, backward, s);
   if (a.C <= 4096) return run_norm<TX, TY, 4, 2>(a, backward, s);
-  if (a.C <= 8192) return run_norm<TX, TY, 4, 4>(a, backward, s);
+  if (a.C <= 8192) return run_norm<TX, TY, 8, 2>(a, backward, s);
   return run_norm<TX, TY, 8, 4>(a, backward, s);
 }
 
@@ -324,21 +377,27 @@ hipError_t pick_types(const NormArgs &a, bool backward, hipStream_t s) {
 
 }  // namespace
 
-// Workgroups per group of the backward pass: about four per CU over all
-// groups, at least 8 rows (two per wave of a four-row workgroup) each.
+// Workgroups per group of the backward pass: the rows of one workgroup are
+// summed in registers, so fewer workgroups write fewer partial rows, and
+// more keep more rows in flight.  One workgroup of eight rows per CU, four
+// of one row.
 int norm_backward_parts(int M, int C, int groups) {
-  const int rows = M / groups;
-  const int rpb = C <= 1536 ? 4 : 1;
-  return std::max(1, std::min(ceil_div(rows, 2 * rpb), std::max(1, 1024 / groups)));
+  const int rows = M / groups, rpb = C <= 1536 ? 8 : 1, wgs = C <= 1536 ? 256 : 1024;
+  return std::max(1, std::min(ceil_div(rows, 2 * rpb), std::max(1, wgs / groups)));
 }
 
 hipError_t launch_layer_norm(const NormArgs &a, hipStream_t s) { return pick_types(a, false, s); }
 hipError_t launch_layer_norm_backward(const NormArgs &a, hipStream_t s) { return pick_types(a, true, s); }
 
-hipError_t launch_sum_parts(const float *src, size_t ld, int parts, int groups, int C, void *dst, int dtype,
-                            hipStream_t s) {
-  hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)ceil_div(C, kSumCols), (unsigned)groups),
-                     dim3(kSumCols * kSumShares), 0, s, src, ld, parts, C, dst, dtype);
+hipError_t launch_sum_parts(const SumArgs &a, int groups, hipStream_t s) {
+  SumArgs b = a;
+  const bool both = a.dst && a.dst2;
+  if (!a.dst) {
+    b.src += a.C;
+    b.dst = a.dst2;
+  }
+  hipLaunchKernelGGL(k_sum_parts, dim3((unsigned)ceil_div(a.C, kSumCols), (unsigned)groups, both ? 2u : 1u),
+                     dim3(kSumCols * kSumShares), 0, s, b);
   return hipGetLastError();
 }
 

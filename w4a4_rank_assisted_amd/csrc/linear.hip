@@ -171,82 +171,88 @@ __device__ __forceinline__ void load_bias(const LinGemm &a, int j, float *b) {
 int part_ld(int J) { return ceil_div(J, 16) * 16; }   // row stride of the fp32 partial sums
 
 // ---------------------------------------------------------------- tiled product
-// Workgroup tile TI x TJ, WI x WJ waves of (16 NI) x (16 NJ) each, BK of the
+// Workgroup tile TI x TJ, WI x WJ waves of (16 NI) x 64 each, 32 of the
 // reduction per stage, NS stage buffers in LDS.
-template <int TI_, int TJ_, int WI_, int WJ_, int BK_, int NS_, int MINW_>
+constexpr int BK = 32;
+
+template <int TI_, int TJ_, int WI_, int WJ_, int NS_>
 struct Cfg {
-  static constexpr int TI = TI_, TJ = TJ_, WI = WI_, WJ = WJ_, BK = BK_, NS = NS_, MINW = MINW_;
-  static constexpr int NW = WI * WJ, NT = 64 * NW, NI = TI / WI / 16, NJ = TJ / WJ / 16;
+  static constexpr int TI = TI_, TJ = TJ_, WI = WI_, WJ = WJ_, NS = NS_;
+  static constexpr int NW = WI * WJ, NI = TI / WI / 16, NJ = TJ / WJ / 16;
   static constexpr int kA = TI * BK * 2, kB = TJ * BK * 2;          // stage bytes
   static constexpr int PA = kA / 1024 / NW, PB = kB / 1024 / NW;    // 1 KB loads per wave and stage
-  static_assert(NJ == 4, "a lane holds 16 consecutive columns");
+  static_assert(NW == 8 && NJ == 4, "eight waves; a lane holds 16 consecutive columns");
   static_assert(PA * NW * 1024 == kA && PB * NW * 1024 == kB, "whole loads per wave");
 };
 
+using Big = Cfg<256, 256, 2, 4, 4>;
+using Half = Cfg<256, 128, 4, 2, 5>;
+using Quarter = Cfg<128, 128, 4, 2, 8>;
+constexpr int kLinLds = 131072;   // four, five and eight stages of these: one workgroup per CU
+
 // Position of a 16-byte chunk in a staged row.
 //
-// r-contiguous operand: rows of BK elements (4 or 8 chunks), read 16 rows
-// at a time, one chunk each.  The rows of one read are consecutive (A) or
-// four runs of four, 16 rows apart (B, see the output layout below); the XOR
-// moves them to 16 different chunk positions of 256 bytes.
-template <int BK, bool ISB>
+// r-contiguous operand: rows of BK elements (4 chunks), 16 rows read at a
+// time, one chunk each.  The LDS serves a 16-byte read in four turns of 16
+// lanes, which are not the lanes of one chunk column: lanes 0-3, 12-15 and
+// 20-27 share a turn, 4-11, 16-19 and 28-31 the next.  With quad t of
+// four rows at chunk c ^ f(t), f = 0, 2, 3, 1, each turn reaches 16 different
+// chunk positions of 256 bytes.  The rows of one read are consecutive (A) or
+// four runs of four, 16 rows apart (B, see the output layout below).
+template <bool ISB>
 __device__ __forceinline__ int swz_cont(int row) {
-  if constexpr (BK == 32) return ISB ? (row >> 4) & 3 : (row >> 2) & 3;
-  return ISB ? ((row >> 1) & 1) | (((row >> 4) & 3) << 1) : (row >> 1) & 7;
+  const int t = (ISB ? row >> 4 : row >> 2) & 3;
+  return ((t & 1) << 1) ^ (3 * (t >> 1));
 }
-// r-strided operand: rows of TI or TJ elements.  A transposing read of 16
-// lanes touches four rows (r = 8 g + jt) at two adjacent chunks (A) or at
-// four chunks two apart (B).
+// r-strided operand: rows of TI or TJ elements.  A transposing read of 32
+// lanes touches eight rows (r = 8 g + jt) at two adjacent chunks (A), or at
+// four chunks two apart of which every other lane takes the other half (B).
 template <bool ISB>
 __device__ __forceinline__ int swz_strided(int r) {
-  if constexpr (ISB) return (r & 1) | (((r >> 1) & 1) << 3);
+  if constexpr (ISB) return (r & 3) | (r & 8);
   return 2 * ((r & 3) | (((r >> 3) & 1) << 2));
 }
 
 // Operand staging of one workgroup: this wave's P direct-to-LDS loads of a
 // stage.  Rows past the matrix and r past R read zero (an offset beyond the
-// buffer); the chunks past the last column of an r-strided operand only reach
-// output columns that are not stored.
-template <int T, int BK, int P, bool STRIDED, bool ISB>
+// buffer), so stages past the end may be issued like any other; the chunks
+// past the last column of an r-strided operand only reach output columns
+// that are not stored.
+template <int T, int P, bool STRIDED, bool ISB>
 struct Stager {
   v4u rs;
   uint32_t voff[P];
-  int ld, R, n, x0, wave, lane;
+  int ld, R, wave, lane;
   static constexpr uint32_t kBad = 0x80000000u;   // operands are below 2^31 bytes
   static constexpr int CPR = STRIDED ? T / 8 : BK / 8;   // chunks of a staged row
-  static constexpr int RPL = 64 / CPR > 0 ? 64 / CPR : 1;   // staged rows per 1 KB load
+  static constexpr int RPL = 64 / CPR;                    // staged rows per 1 KB load
   static_assert(CPR <= 64, "a load covers whole staged rows");
 
-  __device__ __forceinline__ void init(const uint16_t *p, int n_, int x0_, int R_, int ld_, int w, int l) {
-    ld = ld_; R = R_; n = n_; x0 = x0_; wave = w; lane = l;
+  __device__ __forceinline__ void init(const uint16_t *p, int n, int x0, int R_, int ld_, int w, int l) {
+    ld = ld_; R = R_; wave = w; lane = l;
     rs = raw_rsrc(p, (uint32_t)((size_t)(STRIDED ? R : n) * ld * 2));
 #pragma unroll
-    for (int u = 0; u < P; ++u) voff[u] = offset(u, 0, false);
-  }
-  // byte offset of this lane's chunk of load u, stage start r0 (0: the start is
-  // in the scalar offset); `tail` tests r against R
-  __device__ __forceinline__ uint32_t offset(int u, int r0, bool tail) const {
-    const int row = (wave * P + u) * RPL + lane / CPR, pos = lane % CPR;
-    if constexpr (STRIDED) {
-      const int col = x0 + 8 * (pos ^ swz_strided<ISB>(row));
-      if (col >= n || (tail && r0 + row >= R)) return kBad;
-      return ((uint32_t)row * (uint32_t)ld + (uint32_t)col) * 2u;
-    } else {
-      const int k = 8 * (pos ^ swz_cont<BK, ISB>(row));
-      if (x0 + row >= n || (tail && r0 + k >= R)) return kBad;
-      return ((uint32_t)(x0 + row) * (uint32_t)ld + (uint32_t)k) * 2u;
+    for (int u = 0; u < P; ++u) {
+      const int row = (wave * P + u) * RPL + lane / CPR;
+      if constexpr (STRIDED) {
+        const int col = x0 + 8 * (lane % CPR ^ swz_strided<ISB>(row));
+        voff[u] = col < n ? ((uint32_t)row * (uint32_t)ld + (uint32_t)col) * 2u : kBad;
+      } else {
+        voff[u] = x0 + row < n ? ((uint32_t)(x0 + row) * (uint32_t)ld + (uint32_t)chunk_r(u)) * 2u : kBad;
+      }
     }
   }
-  __device__ __forceinline__ void issue(int r0, uint32_t lds) const {
-    const uint32_t soff = (uint32_t)r0 * (STRIDED ? (uint32_t)ld * 2u : 2u);
-    const uint32_t dst = lds + (uint32_t)(wave * P) * 1024u;
-    if (r0 + BK <= R) {
-#pragma unroll
-      for (int u = 0; u < P; ++u) block_to_lds(rs, dst + u * 1024, voff[u], soff);
-    } else {
-#pragma unroll
-      for (int u = 0; u < P; ++u) block_to_lds(rs, dst + u * 1024, offset(u, r0, true), soff);
-    }
+  // first r (within the stage) of this lane's chunk of load u
+  __device__ __forceinline__ int chunk_r(int u) const {
+    const int row = (wave * P + u) * RPL + lane / CPR;
+    return STRIDED ? row : 8 * (lane % CPR ^ swz_cont<ISB>(row));
+  }
+  // load u of the stage whose first r is r0, into the operand's buffer at lds
+  __device__ __forceinline__ void issue(int u, int r0, uint32_t lds) const {
+    // the scalar offset stays inside the buffer, behind the last stage too: the
+    // bounds test compares the lane's offset with the buffer's size less it
+    const uint32_t soff = r0 < R ? (uint32_t)r0 * (STRIDED ? (uint32_t)ld * 2u : 2u) : 0u;
+    block_to_lds(rs, lds + (uint32_t)(wave * P + u) * 1024u, chunk_r(u) < R - r0 ? voff[u] : kBad, soff);
   }
 };
 
@@ -255,22 +261,21 @@ __device__ __forceinline__ void stage_wait() {   // all but this wave's N newest
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// One tile of a job: rows i0 .. + TI, columns j0 .. + TJ, split z of the
+// reduction (PART: the sum goes to the split's partial matrix).
 template <class C, int DT, bool ASTR, bool BSTR, bool PART>
-__global__ __launch_bounds__(C::NT, C::MINW) void k_lin_gemm(LinGemm a) {
+__device__ __forceinline__ void lin_tile(const LinGemm &a, char *lds, int i0, int j0, int z) {
   struct alignas(16) Stage { char a[C::kA]; char b[C::kB]; };
-  __shared__ Stage sm[C::NS];
+  static_assert(sizeof(Stage) * C::NS <= kLinLds, "stage buffers");
+  Stage *sm = reinterpret_cast<Stage *>(lds);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave / C::WJ, wj = wave % C::WJ;
-  const int nbi = (a.I + C::TI - 1) / C::TI, nbj = (a.J + C::TJ - 1) / C::TJ;
-  int bi, bj;
-  xcd_tile_of(blockIdx.x, nbj, nbi, 4, bi, bj);
-  const int i0 = bi * C::TI, j0 = bj * C::TJ;
-  const int nst = (a.R + C::BK - 1) / C::BK, z = PART ? (int)blockIdx.y : 0;
-  const int s0 = PART ? (int)((long long)z * nst / a.splits) : 0;
-  const int s1 = PART ? (int)((long long)(z + 1) * nst / a.splits) : nst;
+  const int nst = (a.R + BK - 1) / BK;
+  const int s0 = PART ? __builtin_amdgcn_readfirstlane((int)((long long)z * nst / a.splits)) : 0;
+  const int s1 = PART ? __builtin_amdgcn_readfirstlane((int)((long long)(z + 1) * nst / a.splits)) : nst;
 
-  Stager<C::TI, C::BK, C::PA, ASTR, false> la;
-  Stager<C::TJ, C::BK, C::PB, BSTR, true> lb;
+  Stager<C::TI, C::PA, ASTR, false> la;
+  Stager<C::TJ, C::PB, BSTR, true> lb;
   la.init(a.A, a.I, i0, a.R, a.lda, wave, lane);
   lb.init(a.B, a.J, j0, a.R, a.ldb, wave, lane);
 
@@ -280,8 +285,10 @@ __global__ __launch_bounds__(C::NT, C::MINW) void k_lin_gemm(LinGemm a) {
   // 16 and, in its four registers, MFMA rows 4 g .. 4 g + 3 (g = l / 16).
   // MFMA row rr of column tile jj is output column 16 (rr / 4) + 4 jj + rr %
   // 4 of the wave's 64, so a lane's four tiles are 16 consecutive columns.
+  // An r-strided B has tiles jj and jj ^ 1 changed over in odd runs rr / 4,
+  // which spreads its reads over the banks; odd g undo it at the end.
   const int g = lane >> 4, rr = lane & 15, jt = rr >> 2, q = rr & 3;
-  uint32_t oa[ASTR ? C::NI : 2], ob[2];
+  uint32_t oa[ASTR ? C::NI : 1], ob[BSTR ? C::NJ : 1];
   if constexpr (ASTR) {
     // lane 4 jt + q of a transposing read addresses r = 8 g + jt (then + 4)
     // and columns 4 q .. 4 q + 3; lane i gets column i of the 16
@@ -292,39 +299,38 @@ __global__ __launch_bounds__(C::NT, C::MINW) void k_lin_gemm(LinGemm a) {
     }
   } else {
     const int row = wi * 16 * C::NI + rr;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) oa[h] = (uint32_t)(row * C::BK * 2 + (((4 * h + g) & (C::BK / 8 - 1)) ^ swz_cont<C::BK, false>(row)) * 16);
+    oa[0] = (uint32_t)(row * BK * 2 + (g ^ swz_cont<false>(row)) * 16);
   }
   if constexpr (BSTR) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int ch = wj * 8 + 2 * q + h;
-      ob[h] = (uint32_t)((8 * g + jt) * C::TJ * 2 + (ch ^ swz_strided<true>(8 * g + jt)) * 16);
+    for (int jj = 0; jj < C::NJ; ++jj) {
+      const int ch = wj * 8 + 2 * q + (jj >> 1);
+      ob[jj] = (uint32_t)((8 * g + jt) * C::TJ * 2 + (ch ^ swz_strided<true>(8 * g + jt)) * 16 + ((jj ^ q) & 1) * 8);
     }
   } else {
     const int row = wj * 64 + 16 * (rr >> 2) + (rr & 3);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) ob[h] = (uint32_t)(row * C::BK * 2 + (((4 * h + g) & (C::BK / 8 - 1)) ^ swz_cont<C::BK, true>(row)) * 16);
+    ob[0] = (uint32_t)(row * BK * 2 + (g ^ swz_cont<true>(row)) * 16);
   }
   auto tr = [&](const char *p) __attribute__((always_inline)) -> v2u {
     return __builtin_bit_cast(v2u, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)p));
   };
-  auto read_a = [&](const char *p, int i, int kk) __attribute__((always_inline)) -> v4u {
-    if constexpr (ASTR) {
-      const char *b = p + oa[i] + kk * 32 * C::TI * 2;
-      const v2u lo = tr(b), hi = tr(b + 4 * C::TI * 2);
-      return (v4u){lo[0], lo[1], hi[0], hi[1]};
+  struct Frags { v4u a[C::NI], b[C::NJ]; };
+  auto read_b = [&](int buf, int jj, Frags &f) __attribute__((always_inline)) {
+    if constexpr (BSTR) {
+      const char *p = sm[buf].b + ob[jj];
+      const v2u lo = tr(p), hi = tr(p + 4 * C::TJ * 2);
+      f.b[jj] = (v4u){lo[0], lo[1], hi[0], hi[1]};
     } else {
-      return *reinterpret_cast<const v4u *>(p + oa[kk] + i * 16 * C::BK * 2);
+      f.b[jj] = *reinterpret_cast<const v4u *>(sm[buf].b + ob[0] + jj * 4 * BK * 2);
     }
   };
-  auto read_b = [&](const char *p, int jj, int kk) __attribute__((always_inline)) -> v4u {
-    if constexpr (BSTR) {
-      const char *b = p + ob[jj >> 1] + (jj & 1) * 8 + kk * 32 * C::TJ * 2;
-      const v2u lo = tr(b), hi = tr(b + 4 * C::TJ * 2);
-      return (v4u){lo[0], lo[1], hi[0], hi[1]};
+  auto read_a = [&](int buf, int i, Frags &f) __attribute__((always_inline)) {
+    if constexpr (ASTR) {
+      const char *p = sm[buf].a + oa[i];
+      const v2u lo = tr(p), hi = tr(p + 4 * C::TI * 2);
+      f.a[i] = (v4u){lo[0], lo[1], hi[0], hi[1]};
     } else {
-      return *reinterpret_cast<const v4u *>(p + ob[kk] + jj * 4 * C::BK * 2);
+      f.a[i] = *reinterpret_cast<const v4u *>(sm[buf].a + oa[0] + i * 16 * BK * 2);
     }
   };
 
@@ -333,37 +339,63 @@ __global__ __launch_bounds__(C::NT, C::MINW) void k_lin_gemm(LinGemm a) {
   for (int i = 0; i < C::NI; ++i)
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j) acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-
-  auto issue = [&](int s, int buf) __attribute__((always_inline)) {
-    la.issue(s * C::BK, lds_addr(sm[buf].a));
-    lb.issue(s * C::BK, lds_addr(sm[buf].b));
+  constexpr int P = C::PA + C::PB;       // this wave's loads of a stage
+  auto issue = [&](int u, int s, int buf) __attribute__((always_inline)) {
+    if (u < C::PA) la.issue(u, s * BK, lds_addr(sm[buf].a));
+    else lb.issue(u - C::PA, s * BK, lds_addr(sm[buf].b));
   };
-  // NS - 1 stages ahead.  At stage s's barrier every wave has its loads of
-  // stage s and its reads of stage s - 1 behind it, so the loads issued after
-  // it may overwrite the buffer of stage s - 1 = s + NS - 1 (mod NS).
+
+  // The operands of stage s are in registers when stage s is multiplied: they
+  // are read from LDS between the MFMAs of stage s - 1, and their buffer takes
+  // the loads of stage s + NS.  One barrier per stage: behind it every wave
+  // has its operands of stage s (its buffer is free) and its loads of stage s +
+  // 1 (they may be read).  A stage's work is dealt into P parts of one load, a
+  // share of the next operands' reads and a share of the MFMAs, so that
+  // neither the loads of eight waves nor their reads meet in one burst.
+  // Stages past s1 are loaded and read, not multiplied.
 #pragma unroll
-  for (int p = 0; p < C::NS - 1; ++p)
-    if (s0 + p < s1) issue(s0 + p, p);
-  int buf = 0;
-  for (int s = s0; s < s1; ++s) {
-    if (s + C::NS - 2 < s1) stage_wait<(C::NS - 2) * (C::PA + C::PB)>();
-    else stage_wait<0>();
-    if (s + C::NS - 1 < s1) issue(s + C::NS - 1, buf == 0 ? C::NS - 1 : buf - 1);
-    const char *pa = sm[buf].a, *pb = sm[buf].b;
+  for (int p = 0; p < C::NS; ++p)
 #pragma unroll
-    for (int kk = 0; kk < C::BK / 32; ++kk) {
-      v4u fa[C::NI], fb[C::NJ];
+    for (int u = 0; u < P; ++u) issue(u, s0 + p, p);
+  int buf = 0;               // of the stage in registers
+  auto step = [&](int s, const Frags &cur, Frags &nxt) __attribute__((always_inline)) {
+    stage_wait<(C::NS - 2) * P>();
+    const int next = buf + 1 == C::NS ? 0 : buf + 1;
 #pragma unroll
-      for (int j = 0; j < C::NJ; ++j) fb[j] = read_b(pb, j, kk);
+    for (int u = 0; u < P; ++u) {
+      issue(u, s + C::NS, buf);
 #pragma unroll
-      for (int i = 0; i < C::NI; ++i) fa[i] = read_a(pa, i, kk);
+      for (int x = u * (C::NJ + C::NI) / P; x < (u + 1) * (C::NJ + C::NI) / P; ++x) {
+        if (x < C::NJ) read_b(next, x, nxt);
+        else read_a(next, x - C::NJ, nxt);
+      }
 #pragma unroll
-      for (int i = 0; i < C::NI; ++i)
+      for (int i = u * C::NI / P; i < (u + 1) * C::NI / P; ++i)
 #pragma unroll
-        for (int j = 0; j < C::NJ; ++j) acc[i][j] = mfma<DT>(fb[j], fa[i], acc[i][j]);
+        for (int j = 0; j < C::NJ; ++j) acc[i][j] = mfma<DT>(cur.b[j], cur.a[i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    buf = buf + 1 == C::NS ? 0 : buf + 1;
+    buf = next;
+  };
+  Frags f0, f1;
+  stage_wait<(C::NS - 1) * P>();
+#pragma unroll
+  for (int j = 0; j < C::NJ; ++j) read_b(0, j, f0);
+#pragma unroll
+  for (int i = 0; i < C::NI; ++i) read_a(0, i, f0);
+  int s = s0;
+  for (; s + 1 < s1; s += 2) {
+    step(s, f0, f1);
+    step(s + 1, f1, f0);
   }
+  if (s < s1) {
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i)
+#pragma unroll
+      for (int j = 0; j < C::NJ; ++j) acc[i][j] = mfma<DT>(f0.b[j], f0.a[i], acc[i][j]);
+  }
+  // no load may land in LDS that the next workgroup owns
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   const int j = j0 + wj * 64 + 16 * g;
   if constexpr (PART) {
@@ -375,7 +407,8 @@ __global__ __launch_bounds__(C::NT, C::MINW) void k_lin_gemm(LinGemm a) {
         const int row = i0 + wi * 16 * C::NI + 16 * i + rr;
         if (row < a.I)
 #pragma unroll
-          for (int jj = 0; jj < C::NJ; ++jj) *reinterpret_cast<v4f *>(dst + (size_t)row * ld + 4 * jj) = acc[i][jj];
+          for (int jj = 0; jj < C::NJ; ++jj)
+            *reinterpret_cast<v4f *>(dst + (size_t)row * ld + 4 * (BSTR ? jj ^ (g & 1) : jj)) = acc[i][jj];
       }
     }
   } else {
@@ -386,15 +419,78 @@ __global__ __launch_bounds__(C::NT, C::MINW) void k_lin_gemm(LinGemm a) {
       const int row = i0 + wi * 16 * C::NI + 16 * i + rr;
       float v[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = acc[i][e >> 2][e & 3];
+      for (int e = 0; e < 16; ++e) {
+        v[e] = acc[i][e >> 2][e & 3];
+        if (BSTR && (g & 1)) v[e] = acc[i][(e >> 2) ^ 1][e & 3];
+      }
       if (row < a.I) finish<DT, 16>(a, row, j, bias, v);
     }
   }
 }
 
-// Sums the splits' partial sums in split order and finishes eight columns per thread.
+// The tile of unit u among `count` units, t = first + u / cut in the walking
+// order, and its part u % cut.  Workgroup ids go round the XCDs, each with its
+// own L2: XCD x gets a contiguous range of the order, which walks the matrix
+// in bands of four tile rows, so the tiles it runs at once share rows of A and
+// columns of B.
+__device__ __forceinline__ void lin_unit(const LinGemm &a, int u, int first, int count, int cut, int &bi, int &bj,
+                                         int &part) {
+  const int per = count / 8, rem = count % 8, x = u % 8;
+  const int v = x * per + min(x, rem) + u / 8, t = first + v / cut;
+  part = v % cut;
+  constexpr int kBand = 4;
+  const int span = kBand * a.nbj, band = t / span, top = band * kBand, rows = min(a.nbi - top, kBand), w = t % span;
+  bi = top + w % rows;
+  bj = w / rows;
+}
+
+// The units of one job: `full` whole 256 x 256 tiles, then the remaining tiles
+// as two 256 x 128 or four 128 x 128 parts (`cut`), or all tiles in four for
+// each split of the reduction.
+template <int DT, bool AS, bool BS>
+__device__ __forceinline__ void lin_full(const LinGemm &a, char *lds, int u) {
+  int bi, bj, part;
+  lin_unit(a, u, 0, a.full, 1, bi, bj, part);
+  lin_tile<Big, DT, AS, BS, false>(a, lds, bi * 256, bj * 256, 0);
+}
+template <int DT, bool AS, bool BS>
+__device__ __forceinline__ void lin_part(const LinGemm &a, char *lds, int u) {
+  int bi, bj, part;
+  const int count = (a.nbi * a.nbj - a.full) * a.cut, z = u / count;
+  lin_unit(a, u % count, a.full, count, a.cut, bi, bj, part);
+  const int i0 = bi * 256 + (a.cut == 4 ? part >> 1 : 0) * 128, j0 = bj * 256 + (part & 1) * 128;
+  if (i0 >= a.I || j0 >= a.J) return;
+  if (a.splits > 1) lin_tile<Quarter, DT, AS, BS, true>(a, lds, i0, j0, z);
+  else if (a.cut == 4) lin_tile<Quarter, DT, AS, BS, false>(a, lds, i0, j0, 0);
+  else lin_tile<Half, DT, AS, BS, false>(a, lds, i0, j0, 0);
+}
+
+// Forward: one job.  Backward: dX and dW in one launch, so that the last
+// tiles of the one run beside those of the other; whole tiles first.
 template <int DT>
-__global__ __launch_bounds__(256) void k_lin_reduce(LinGemm a) {
+__global__ __launch_bounds__(512, 2) void k_lin_fwd(LinGemm a) {
+  __shared__ __attribute__((aligned(16))) char lds[kLinLds];
+  const int u = blockIdx.x;
+  if (u < a.full) lin_full<DT, false, true>(a, lds, u);
+  else lin_part<DT, false, true>(a, lds, u - a.full);
+}
+template <int DT>
+__global__ __launch_bounds__(512, 2) void k_lin_bwd(LinGemm x, LinGemm w) {
+  __shared__ __attribute__((aligned(16))) char lds[kLinLds];
+  int u = blockIdx.x;
+  if (u < x.full) return lin_full<DT, false, false>(x, lds, u);
+  u -= x.full;
+  if (u < w.full) return lin_full<DT, true, true>(w, lds, u);
+  u -= w.full;
+  if (u < x.parts) return lin_part<DT, false, false>(x, lds, u);
+  lin_part<DT, true, true>(w, lds, u - x.parts);
+}
+
+// Sums the splits' partial sums in split order and finishes eight columns per thread.
+// Grid y: the job.
+template <int DT>
+__global__ __launch_bounds__(256) void k_lin_reduce(LinGemm first, LinGemm second) {
+  const LinGemm &a = blockIdx.y == 0 ? first : second;
   const int ld = (a.J + 15) / 16 * 16, cols = (a.J + 7) / 8;
   const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
   if (t >= (long long)a.I * cols) return;
@@ -539,8 +635,10 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_lin_skinny(LinGemm a) {
 }
 
 // ---------------------------------------------------------------- staging passes
-__global__ __launch_bounds__(256) void k_pad_rows(const uint16_t *src, int rows, int cols, uint16_t *dst, int ld) {
-  const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
+// Rows of a length that is no multiple of 8 elements, copied to a multiple
+// with zeros behind them (the direct-to-LDS loads are 16 bytes, aligned).
+__device__ __forceinline__ void pad_rows(const uint16_t *src, int rows, int cols, uint16_t *dst, int ld, int block) {
+  const long long t = (long long)block * 256 + threadIdx.x;
   const int cpr = ld / 8;
   if (t >= (long long)rows * cpr) return;
   const int r = (int)(t / cpr), c = (int)(t % cpr) * 8;
@@ -563,11 +661,11 @@ __global__ __launch_bounds__(256) void k_pad_rows(const uint16_t *src, int rows,
 constexpr int kDzCols = 256, kDzRows = 8;
 
 template <int DT>
-__global__ __launch_bounds__(256) void k_lin_dz(LinDz a) {
+__device__ __forceinline__ void lin_dz(const LinDz &a, int bx, int by) {
   __shared__ float red[kDzRows][kDzCols];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
-  const int j = blockIdx.x * kDzCols + 8 * cx, n = a.N - j;
-  const int m0 = (int)((long long)blockIdx.y * a.M / a.slices), m1 = (int)((long long)(blockIdx.y + 1) * a.M / a.slices);
+  const int j = bx * kDzCols + 8 * cx, n = a.N - j;
+  const int m0 = (int)((long long)by * a.M / a.slices), m1 = (int)((long long)(by + 1) * a.M / a.slices);
   float s[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) s[e] = 0.0f;
@@ -618,27 +716,69 @@ __global__ __launch_bounds__(256) void k_lin_dz(LinDz a) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) red[ry][8 * cx + e] = s[e];
   __syncthreads();
-  const int col = blockIdx.x * kDzCols + threadIdx.x;
+  const int col = bx * kDzCols + threadIdx.x;
   if (col >= a.N) return;
   float v = 0.0f;
 #pragma unroll
   for (int r = 0; r < kDzRows; ++r) v += red[r][threadIdx.x];
-  a.part[(size_t)blockIdx.y * a.N + col] = v;
+  a.part[(size_t)by * a.N + col] = v;
 }
+
+// Everything the products read that is not there yet, in one launch: padded X,
+// padded W, dZ with its column sums.
+template <int DT>
+__global__ __launch_bounds__(256) void k_lin_prep(LinPrep p) {
+  int b = blockIdx.x;
+  if (b < p.x_blocks) return pad_rows(p.X, p.x_rows, p.x_cols, p.Xp, p.x_ld, b);
+  b -= p.x_blocks;
+  if (b < p.w_blocks) return pad_rows(p.W, p.w_rows, p.w_cols, p.Wp, p.w_ld, b);
+  b -= p.w_blocks;
+  const int cols = (p.dz.np + kDzCols - 1) / kDzCols;
+  lin_dz<DT>(p.dz, b % cols, b / cols);
+}
+
 
 // ---------------------------------------------------------------- planning
-using Big = Cfg<256, 128, 2, 2, 32, 3, 2>;     // 72 KB of LDS: two workgroups per CU
-using Small = Cfg<128, 128, 2, 2, 32, 3, 2>;   // few tiles
+constexpr int kCus = 256;
 
-bool big_tiles(int I, int J) {
-  return (long long)ceil_div(I, Big::TI) * ceil_div(J, Big::TJ) >= 256;
+int quarters(int I, int J) { return ceil_div(I, 128) * ceil_div(J, 128); }
+
+// Splits of the reduction: for so few 128 x 128 tiles that one round leaves
+// half of the CUs idle, at least 256 of the reduction each.
+int gemm_splits(int I, int J, int R) {
+  return std::max(1, std::min({kCus / quarters(I, J), R / 256, 16}));
 }
 
-int gemm_splits(int I, int J, int R) {
-  const long long tiles = big_tiles(I, J) ? (long long)ceil_div(I, Big::TI) * ceil_div(J, Big::TJ)
-                                          : (long long)ceil_div(I, Small::TI) * ceil_div(J, Small::TJ);
-  if (tiles >= 256) return 1;
-  return (int)std::max(1LL, std::min({512 / tiles, (long long)R / 512, 16LL}));
+// How the last tiles are cut.  `rem` tiles remain after whole rounds of one
+// 256 x 256 tile per CU; a round of halves costs 0.62 of a round of whole
+// tiles, one of quarters 0.38.
+int best_cut(int rem) {
+  const float full = 1.0f, half = 0.62f * ceil_div(2 * rem, kCus), quarter = 0.38f * ceil_div(4 * rem, kCus);
+  return full <= half && full <= quarter ? 1 : half <= quarter ? 2 : 4;
+}
+
+// Sets the units of the jobs of one launch; the last tiles are the last job's.
+void plan_units(LinGemm *job, int n) {
+  int tiles = 0;
+  for (int i = 0; i < n; ++i) {
+    LinGemm &a = job[i];
+    a.nbi = ceil_div(a.I, 256);
+    a.nbj = ceil_div(a.J, 256);
+    if (a.splits <= 1) tiles += a.nbi * a.nbj;
+  }
+  int rem = tiles % kCus;
+  const int cut = best_cut(rem);
+  for (int i = n - 1; i >= 0; --i) {
+    LinGemm &a = job[i];
+    const int t = a.nbi * a.nbj;
+    if (a.splits > 1) {
+      a.full = 0; a.cut = 4; a.parts = 4 * t * a.splits;
+      continue;
+    }
+    const int last = cut == 1 ? 0 : std::min(t, rem);
+    rem -= last;
+    a.full = t - last; a.cut = cut; a.parts = last * cut;
+  }
 }
 
 int skinny_splits(int J, int K) {
@@ -647,21 +787,6 @@ int skinny_splits(int J, int K) {
 
 size_t part_bytes(int I, int J, int splits) {
   return splits > 1 ? (size_t)splits * I * part_ld(J) * sizeof(float) : 0;
-}
-
-template <class C, int DT, bool AS, bool BS>
-hipError_t run_tiles(const LinGemm &a, hipStream_t s) {
-  const unsigned tiles = (unsigned)(ceil_div(a.I, C::TI) * ceil_div(a.J, C::TJ));
-  if (a.splits > 1)
-    hipLaunchKernelGGL((k_lin_gemm<C, DT, AS, BS, true>), dim3(tiles, (unsigned)a.splits), dim3(C::NT), 0, s, a);
-  else
-    hipLaunchKernelGGL((k_lin_gemm<C, DT, AS, BS, false>), dim3(tiles), dim3(C::NT), 0, s, a);
-  return hipGetLastError();
-}
-
-template <int DT, bool AS, bool BS>
-hipError_t pick_tiles(const LinGemm &a, hipStream_t s) {
-  return big_tiles(a.I, a.J) ? run_tiles<Big, DT, AS, BS>(a, s) : run_tiles<Small, DT, AS, BS>(a, s);
 }
 
 template <int DT, int MT>
@@ -675,21 +800,41 @@ hipError_t run_skinny(const LinGemm &a, hipStream_t s) {
 }
 
 template <int DT>
-hipError_t run_linear(const LinGemm &a, bool skinny, hipStream_t s) {
+hipError_t run_reduce(const LinGemm &a, const LinGemm &b, hipStream_t s) {
+  long long items = a.splits > 1 ? (long long)a.I * ceil_div(a.J, 8) : 0;
+  const bool two = b.splits > 1;
+  if (two) items = std::max(items, (long long)b.I * ceil_div(b.J, 8));
+  if (items == 0) return hipSuccess;
+  const LinGemm &first = a.splits > 1 ? a : b;
+  hipLaunchKernelGGL(k_lin_reduce<DT>, dim3((unsigned)((items + 255) / 256), a.splits > 1 && two ? 2u : 1u), dim3(256), 0,
+                     s, first, b);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t run_forward(LinGemm a, bool skinny, hipStream_t s) {
   hipError_t e;
   if (skinny) {
     const int mt = ceil_div(a.I, 16);
     e = mt == 1 ? run_skinny<DT, 1>(a, s) : mt == 2 ? run_skinny<DT, 2>(a, s)
         : mt == 3 ? run_skinny<DT, 3>(a, s) : run_skinny<DT, 4>(a, s);
-  } else if (a.b_rows) {
-    e = a.a_rows ? pick_tiles<DT, true, true>(a, s) : pick_tiles<DT, false, true>(a, s);
   } else {
-    e = pick_tiles<DT, false, false>(a, s);
+    plan_units(&a, 1);
+    hipLaunchKernelGGL(k_lin_fwd<DT>, dim3((unsigned)(a.full + a.parts)), dim3(512), 0, s, a);
+    e = hipGetLastError();
   }
-  if (e != hipSuccess || a.splits <= 1) return e;
-  const long long items = (long long)a.I * ceil_div(a.J, 8);
-  hipLaunchKernelGGL(k_lin_reduce<DT>, dim3((unsigned)((items + 255) / 256)), dim3(256), 0, s, a);
-  return hipGetLastError();
+  return e != hipSuccess ? e : run_reduce<DT>(a, LinGemm{}, s);
+}
+
+template <int DT>
+hipError_t run_backward(const LinGemm &x, const LinGemm &w, hipStream_t s) {
+  LinGemm job[2] = {x, w};
+  const bool has_x = x.out != nullptr, has_w = w.out != nullptr;
+  plan_units(has_x ? job : job + 1, has_x && has_w ? 2 : 1);
+  hipLaunchKernelGGL(k_lin_bwd<DT>, dim3((unsigned)(job[0].full + job[0].parts + job[1].full + job[1].parts)), dim3(512),
+                     0, s, job[0], job[1]);
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess ? e : run_reduce<DT>(has_x ? job[0] : LinGemm{}, has_w ? job[1] : LinGemm{}, s);
 }
 
 }  // namespace
@@ -733,28 +878,36 @@ LinPlan plan_linear_backward(int M, int K, int N) {
   p.db_off = off;
   off = align_up(off + (size_t)p.slices * N * sizeof(float), 256);
   p.part_off = off;
-  off = align_up(off + std::max(part_bytes(M, K, p.splits_dx), part_bytes(K, N, p.splits_dw)), 256);
+  off = align_up(off + part_bytes(M, K, p.splits_dx), 256);
+  p.part_w_off = off;
+  off = align_up(off + part_bytes(K, N, p.splits_dw), 256);
   p.total = off;
   return p;
 }
 
 hipError_t launch_linear(const LinGemm &a, bool skinny, hipStream_t s) {
-  return a.dtype == kBf16 ? run_linear<kBf16>(a, skinny, s) : run_linear<kF16>(a, skinny, s);
+  return a.dtype == kBf16 ? run_forward<kBf16>(a, skinny, s) : run_forward<kF16>(a, skinny, s);
 }
 
-hipError_t launch_pad_rows(const uint16_t *src, int rows, int cols, uint16_t *dst, int ld, hipStream_t s) {
-  const long long items = (long long)rows * (ld / 8);
-  hipLaunchKernelGGL(k_pad_rows, dim3((unsigned)((items + 255) / 256)), dim3(256), 0, s, src, rows, cols, dst, ld);
-  return hipGetLastError();
+hipError_t launch_linear_backward(const LinGemm &x, const LinGemm &w, hipStream_t s) {
+  const int dtype = x.out ? x.dtype : w.dtype;
+  return dtype == kBf16 ? run_backward<kBf16>(x, w, s) : run_backward<kF16>(x, w, s);
 }
 
-hipError_t launch_linear_dz(const LinDz &a, hipStream_t s) {
-  const dim3 grid((unsigned)ceil_div(a.np, kDzCols), (unsigned)a.slices);
-  if (a.dtype == kBf16) hipLaunchKernelGGL(k_lin_dz<kBf16>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(k_lin_dz<kF16>, grid, dim3(256), 0, s, a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !a.db) return e;
-  return launch_sum_parts(a.part, (size_t)a.N, a.slices, 1, a.N, a.db, a.dtype, s);
+hipError_t launch_linear_prep(LinPrep p, int dtype, hipStream_t s) {
+  auto blocks = [](const uint16_t *src, int rows, int ld) {
+    return src ? (int)(((long long)rows * (ld / 8) + 255) / 256) : 0;
+  };
+  p.x_blocks = blocks(p.X, p.x_rows, p.x_ld);
+  p.w_blocks = blocks(p.W, p.w_rows, p.w_ld);
+  const bool dz = p.dz.dY != nullptr;
+  const int n = p.x_blocks + p.w_blocks + (dz ? ceil_div(p.dz.np, kDzCols) * p.dz.slices : 0);
+  if (n == 0) return hipSuccess;
+  if (dtype == kBf16) hipLaunchKernelGGL(k_lin_prep<kBf16>, dim3((unsigned)n), dim3(256), 0, s, p);
+  else hipLaunchKernelGGL(k_lin_prep<kF16>, dim3((unsigned)n), dim3(256), 0, s, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !dz || !p.dz.db) return e;
+  return launch_sum_parts(SumArgs{p.dz.part, (size_t)p.dz.N, p.dz.slices, p.dz.N, p.dz.db, nullptr, dtype}, 1, s);
 }
 
 }  // namespace hsq
