@@ -315,8 +315,9 @@ struct LinGemm {
   float *part;             // split partial sums (workspace)
   int splits;
   // units of the launch (set there): nbi x nbj tiles of 256 x 256, of which
-  // `full` whole, the others in `cut` parts, `parts` units in all
-  int nbi, nbj, full, cut, parts;
+  // `full` whole (workgroups full0 ..), the others in `cut` parts, `parts` units
+  // in all (workgroups parts0 ..)
+  int nbi, nbj, full, cut, parts, full0, parts0;
 };
 
 struct LinPlan {
@@ -328,7 +329,7 @@ struct LinPlan {
   size_t x_off = 0, w_off = 0, dz_off = 0, part_off = 0, part_w_off = 0, db_off = 0, total = 0;
 };
 
-constexpr int kLinSkinnyMaxM = 64;
+constexpr int kLinSkinnyMaxM = 48;   // rows of the weight-streaming kernel (three row tiles)
 
 LinPlan plan_linear(int M, int K, int N);
 LinPlan plan_linear_backward(int M, int K, int N);

@@ -196,20 +196,18 @@ __global__ __launch_bounds__(norm_threads<W>()) void k_layer_norm(NormArgs a) {
   }
 }
 
-// Backward: workgroup p of group gi takes rows p, p + parts, ... of the
-// group (RPB at a time where a row is one wave's), keeps its columns' sums of
-// dy xh and dy in registers and writes them as one partial row; the partial
-// rows are summed by k_sum_parts.  The next row is loaded while this one is
+// Backward: workgroup p of group gi takes RPB rows at a time of the group (a
+// row to one wave, four or eight), keeps its columns' sums of dy xh and dy in
+// registers and writes them as one partial row; the partial rows are summed
+// by k_sum_parts.  The next row is loaded while this one is
 // worked on, where the registers allow it (NV < 4).
-constexpr int kBwdThreads = 512;
-template <int W>
-constexpr int bwd_rows() { return W > 1 ? 1 : kBwdThreads / 64; }
+constexpr int kBwdWaves = 8;
 
 template <int TX, int TY, int W, int NV>
-__global__ __launch_bounds__(64 * W * bwd_rows<W>()) void k_layer_norm_bwd(NormArgs a) {
-  constexpr int RPB = bwd_rows<W>();
-  __shared__ float red[4][W > 1 ? W : 1];
-  __shared__ float comb[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? 512 * 2 : 1];
+__global__ __launch_bounds__(64 * kBwdWaves) void k_layer_norm_bwd(NormArgs a) {
+  constexpr int RPB = kBwdWaves / W;
+  __shared__ float red[4][RPB][W];
+  __shared__ float comb[RPB > 1 ? RPB - 1 : 1][RPB > 1 ? 1024 * W : 1];
   const int t = threadIdx.x % (64 * W), wave = t >> 6, sub = threadIdx.x / (64 * W);
   const int gi = blockIdx.y;
   const size_t g = (size_t)gi * a.C;
@@ -229,22 +227,24 @@ __global__ __launch_bounds__(64 * W * bwd_rows<W>()) void k_layer_norm_bwd(NormA
   Run<TX> nx[NV];
   Run<TY> ny[NV];
   float nmean = 0.0f, nrstd = 0.0f;
-  auto fetch = [&](int r) __attribute__((always_inline)) {
-    const size_t row = (size_t)gi * a.rows + r, base = row * a.C;
+  auto fetch = [&](int r) __attribute__((always_inline)) {   // rows past the group's: zeros
+    const bool has = r < a.rows;
+    const size_t row = (size_t)gi * a.rows + (has ? r : 0), base = row * a.C;
     nmean = a.mean[row];
     nrstd = a.rstd[row];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = 8 * (t + v * 64 * W);
-      nx[v] = load_run<TX>(a.X, base + c, a.C - c);
-      ny[v] = load_run<TY>(a.dY, base + c, a.C - c);
+      const int c = 8 * (t + v * 64 * W), n = has ? a.C - c : 0;
+      nx[v] = load_run<TX>(a.X, base + c, n);
+      ny[v] = load_run<TY>(a.dY, base + c, n);
     }
   };
   const int stride = gridDim.x * RPB;
   int turn = 0;
-  int r = blockIdx.x * RPB + sub;
-  if (kAhead && r < a.rows) fetch(r);
-  for (; r < a.rows; r += stride, turn ^= 2) {
+  if (kAhead) fetch(blockIdx.x * RPB + sub);
+  for (int r0 = blockIdx.x * RPB; r0 < a.rows; r0 += stride, turn ^= 2) {
+    const int r = r0 + sub;
+    const bool has = r < a.rows;
     if (!kAhead) fetch(r);
     const size_t base = ((size_t)gi * a.rows + r) * a.C;
     const float mean = nmean, rstd = nrstd;
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(64 * W * bwd_rows<W>()) void k_layer_norm_bwd(NormA
       const int c = 8 * (t + v * 64 * W);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float h = c + e < a.C ? (value<TX>(nx[v], e) - mean) * rstd : 0.0f;
+        const float h = has && c + e < a.C ? (value<TX>(nx[v], e) - mean) * rstd : 0.0f;
         const float dy = value<TY>(ny[v], e);
         dw[v][e] = fmaf(dy, h, dw[v][e]);
         db[v][e] += dy;
@@ -265,14 +265,14 @@ __global__ __launch_bounds__(64 * W * bwd_rows<W>()) void k_layer_norm_bwd(NormA
         s2 = fmaf(gr[v][e], h, s2);
       }
     }
-    if (kAhead && r + stride < a.rows) fetch(r + stride);
+    if (kAhead && r0 + stride < a.rows) fetch(r + stride);
     if (a.dX) {
-      const float c1 = row_sum<W>(s1, red[turn], wave) / (float)a.C;
-      const float c2 = row_sum<W>(s2, red[turn + 1], wave) / (float)a.C;
+      const float c1 = row_sum<W>(s1, red[turn][sub], wave) / (float)a.C;
+      const float c2 = row_sum<W>(s2, red[turn + 1][sub], wave) / (float)a.C;
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int c = 8 * (t + v * 64 * W);
-        if (a.C - c <= 0) continue;
+        if (!has || a.C - c <= 0) continue;
         float d[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) d[e] = rstd * (gr[v][e] - c1 - xh[v][e] * c2);
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(64 * W * bwd_rows<W>()) void k_layer_norm_bwd(NormA
     }
   }
   if (!a.part) return;
-  // the workgroup's rows in order of its waves (one wave to a row), 512 columns at a time
+  // the rows' shares in order, 512 W columns at a time
   float *out = a.part + ((size_t)gi * a.parts + blockIdx.x) * 2 * a.C;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
@@ -291,16 +291,16 @@ __global__ __launch_bounds__(64 * W * bwd_rows<W>()) void k_layer_norm_bwd(NormA
       if (sub > 0)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          comb[sub - 1][e * 64 + t] = dw[v][e];
-          comb[sub - 1][512 + e * 64 + t] = db[v][e];
+          comb[sub - 1][e * 64 * W + t] = dw[v][e];
+          comb[sub - 1][512 * W + e * 64 * W + t] = db[v][e];
         }
       __syncthreads();
       if (sub == 0)
         for (int k = 0; k < RPB - 1; ++k)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            dw[v][e] += comb[k][e * 64 + t];
-            db[v][e] += comb[k][512 + e * 64 + t];
+            dw[v][e] += comb[k][e * 64 * W + t];
+            db[v][e] += comb[k][512 * W + e * 64 * W + t];
           }
     }
     if (sub == 0 && n > 0) {
@@ -349,7 +349,7 @@ hipError_t run_norm(const NormArgs &a, bool backward, hipStream_t s) {
   constexpr int RPB = norm_threads<W>() / (64 * W);
   if (backward)
     hipLaunchKernelGGL((k_layer_norm_bwd<TX, TY, W, NV>), dim3((unsigned)a.parts, (unsigned)a.groups),
-                       dim3(64 * W * bwd_rows<W>()), 0, s, a);
+                       dim3(64 * kBwdWaves), 0, s, a);
   else
     hipLaunchKernelGGL((k_layer_norm<TX, TY, W, NV>), dim3((unsigned)ceil_div(a.M, RPB)), dim3(norm_threads<W>()), 0,
                        s, a);
@@ -377,13 +377,12 @@ hipError_t pick_types(const NormArgs &a, bool backward, hipStream_t s) {
 
 }  // namespace
 
-// Workgroups per group of the backward pass: the rows of one workgroup are
-// summed in registers, so fewer workgroups write fewer partial rows, and
-// more keep more rows in flight.  One workgroup of eight rows per CU, four
-// of one row.
+// Workgroups per group of the backward pass: one per CU over all groups (each
+// keeps its rows' sums in registers and writes one partial row), fewer where
+// a workgroup would not get two turns of rows.
 int norm_backward_parts(int M, int C, int groups) {
-  const int rows = M / groups, rpb = C <= 1536 ? 8 : 1, wgs = C <= 1536 ? 256 : 1024;
-  return std::max(1, std::min(ceil_div(rows, 2 * rpb), std::max(1, wgs / groups)));
+  const int rows = M / groups, rpb = C <= 1536 ? 8 : C <= 4096 ? 2 : 1;
+  return std::max(1, std::min(ceil_div(rows, 2 * rpb), std::max(1, 256 / groups)));
 }
 
 hipError_t launch_layer_norm(const NormArgs &a, hipStream_t s) { return pick_types(a, false, s); }

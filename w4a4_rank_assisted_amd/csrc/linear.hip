@@ -9,7 +9,7 @@
 // contiguous (X in X W, both operands of dZ W^T) or with r as its rows (W in
 // X W, both operands of X^T dZ).  Both kinds travel to LDS unchanged by
 // direct-to-LDS loads; the second kind is transposed on the way into the
-// registers by the transposing LDS read.  Few rows (M <= 64) of the forward
+// registers by the transposing LDS read.  Few rows (M <= 48) of the forward
 // product stream the weights instead (k_lin_skinny).
 #include "hsq_internal.h"
 
@@ -22,8 +22,9 @@ namespace {
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
-struct __attribute__((packed, aligned(2))) U16 { uint32_t d[4]; };   // 16 bytes at any element
-struct __attribute__((packed, aligned(4))) F32x4 { float f[4]; };
+// 16 bytes at any element: global memory takes them as they come
+typedef uint32_t U16 __attribute__((ext_vector_type(4), aligned(2)));
+typedef float F32x4 __attribute__((ext_vector_type(4), aligned(4)));
 
 template <int DT>
 __device__ __forceinline__ v4f mfma(v4u a, v4u b, v4f c) {
@@ -101,7 +102,7 @@ __device__ __forceinline__ void finish(const LinGemm &a, int i, int j, const flo
         U16 t;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          t.d[e] = f32_to_half<DT>(v[8 * c + 2 * e]) | (f32_to_half<DT>(v[8 * c + 2 * e + 1]) << 16);
+          t[e] = f32_to_half<DT>(v[8 * c + 2 * e]) | (f32_to_half<DT>(v[8 * c + 2 * e + 1]) << 16);
         *reinterpret_cast<U16 *>(p + o + 8 * c) = t;
       }
     } else {
@@ -131,10 +132,10 @@ __device__ __forceinline__ void finish(const LinGemm &a, int i, int j, const flo
         if (r) {
           t = *reinterpret_cast<const F32x4 *>(r + o + 4 * c);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * c + e] += t.f[e];
+          for (int e = 0; e < 4; ++e) v[4 * c + e] += t[e];
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) t.f[e] = v[4 * c + e];
+        for (int e = 0; e < 4; ++e) t[e] = v[4 * c + e];
         *reinterpret_cast<F32x4 *>(y + o + 4 * c) = t;
       }
     } else {
@@ -151,7 +152,7 @@ __device__ __forceinline__ void finish(const LinGemm &a, int i, int j, const flo
       for (int c = 0; c < NV / 8; ++c) {
         const U16 t = *reinterpret_cast<const U16 *>(r + o + 8 * c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[8 * c + e] += half_to_f32<DT>((t.d[e / 2] >> (16 * (e & 1))) & 0xFFFFu);
+        for (int e = 0; e < 8; ++e) v[8 * c + e] += half_to_f32<DT>((t[e / 2] >> (16 * (e & 1))) & 0xFFFFu);
       }
     } else {
 #pragma unroll
@@ -477,13 +478,12 @@ __global__ __launch_bounds__(512, 2) void k_lin_fwd(LinGemm a) {
 template <int DT>
 __global__ __launch_bounds__(512, 2) void k_lin_bwd(LinGemm x, LinGemm w) {
   __shared__ __attribute__((aligned(16))) char lds[kLinLds];
-  int u = blockIdx.x;
-  if (u < x.full) return lin_full<DT, false, false>(x, lds, u);
-  u -= x.full;
-  if (u < w.full) return lin_full<DT, true, true>(w, lds, u);
-  u -= w.full;
-  if (u < x.parts) return lin_part<DT, false, false>(x, lds, u);
-  lin_part<DT, true, true>(w, lds, u - x.parts);
+  const int u = blockIdx.x;
+  auto in = [&](int first, int count) { return u >= first && u < first + count; };
+  if (in(x.full0, x.full)) lin_full<DT, false, false>(x, lds, u - x.full0);
+  else if (in(w.full0, w.full)) lin_full<DT, true, true>(w, lds, u - w.full0);
+  else if (in(x.parts0, x.parts)) lin_part<DT, false, false>(x, lds, u - x.parts0);
+  else lin_part<DT, true, true>(w, lds, u - w.parts0);
 }
 
 // Sums the splits' partial sums in split order and finishes eight columns per thread.
@@ -499,13 +499,24 @@ __global__ __launch_bounds__(256) void k_lin_reduce(LinGemm first, LinGemm secon
   float v[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-  for (int z = 0; z < a.splits; ++z, p += (size_t)a.I * ld) {
-    const v4f lo = *reinterpret_cast<const v4f *>(p), hi = *reinterpret_cast<const v4f *>(p + 4);
+  const size_t next = (size_t)a.I * ld;
+  for (int z = 0; z < a.splits; z += 4, p += 4 * next) {   // four splits in flight
+    v4f lo[4], hi[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] += lo[e];
-      v[4 + e] += hi[e];
+    for (int k = 0; k < 4; ++k) {
+      const float *pk = p + (z + k < a.splits ? k : 0) * next;
+      lo[k] = *reinterpret_cast<const v4f *>(pk);
+      hi[k] = *reinterpret_cast<const v4f *>(pk + 4);
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (z + k < a.splits) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] += lo[k][e];
+          v[4 + e] += hi[k][e];
+        }
+      }
   }
   float bias[8];
   load_bias<DT, 8>(a, j, bias);
@@ -513,7 +524,7 @@ __global__ __launch_bounds__(256) void k_lin_reduce(LinGemm first, LinGemm secon
 }
 
 // ---------------------------------------------------------------- few rows
-// Y of up to 16 MT rows, bound by the one read of W.  A workgroup owns 128
+// Y of up to 48 rows (16 MT), bound by the one read of W.  A workgroup owns 128
 // columns and a share of K; its four waves split that share in runs of 32.
 // Lane l loads, for its 8 rows k = 8 (l / 16) .. + 7 of a run, the 8
 // columns 8 (l % 16) .. + 7 (16 bytes each, a row's 128 columns are 256
@@ -524,7 +535,7 @@ __global__ __launch_bounds__(256) void k_lin_reduce(LinGemm first, LinGemm secon
 constexpr int kSkCols = 128, kSkWaves = 4;
 
 template <int DT, int MT, bool PART>
-__global__ __launch_bounds__(64 * kSkWaves) void k_lin_skinny(LinGemm a) {
+__global__ __launch_bounds__(64 * kSkWaves, 5 - MT) void k_lin_skinny(LinGemm a) {
   __shared__ float red[kSkWaves][16][kSkCols + 4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
@@ -538,20 +549,26 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_lin_skinny(LinGemm a) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[m][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 
-  const bool whole = jc + 8 <= a.J;
+  // whole runs of whole strips load without a test
+  const bool strip = j0 + kSkCols <= a.J;
   auto load = [&](int run, U16 (&w)[8]) __attribute__((always_inline)) {
     const int k = 32 * run + 8 * g;
+    const uint16_t *p = a.B + (size_t)k * a.ldb + jc;
+    if (strip && 32 * run + 32 <= a.R) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const U16 *>(p + (size_t)e * a.ldb);
+      return;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      w[e] = U16{{0u, 0u, 0u, 0u}};
-      const uint16_t *p = a.B + (size_t)(k + e) * a.ldb + jc;
+      w[e] = (U16){0u, 0u, 0u, 0u};
       if (k + e < a.R) {
-        if (whole) {
-          w[e] = *reinterpret_cast<const U16 *>(p);
+        if (jc + 8 <= a.J) {
+          w[e] = *reinterpret_cast<const U16 *>(p + (size_t)e * a.ldb);
         } else {
 #pragma unroll
           for (int h = 0; h < 8; ++h)
-            if (jc + h < a.J) w[e].d[h / 2] |= (uint32_t)p[h] << (16 * (h & 1));
+            if (jc + h < a.J) w[e][h / 2] |= (uint32_t)p[(size_t)e * a.ldb + h] << (16 * (h & 1));
         }
       }
     }
@@ -566,8 +583,7 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_lin_skinny(LinGemm a) {
       if (row < a.I) {
         const uint16_t *p = a.A + (size_t)row * a.lda + k;
         if (k + 8 <= a.R) {
-          const U16 t = *reinterpret_cast<const U16 *>(p);
-          x[m] = (v4u){t.d[0], t.d[1], t.d[2], t.d[3]};
+          x[m] = *reinterpret_cast<const U16 *>(p);
         } else {
 #pragma unroll
           for (int h = 0; h < 8; ++h)
@@ -580,22 +596,16 @@ __global__ __launch_bounds__(64 * kSkWaves) void k_lin_skinny(LinGemm a) {
       v4u b;   // column 8 c + j, k .. k + 7
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        b[e] = __builtin_amdgcn_perm(w[2 * e + 1].d[j / 2], w[2 * e].d[j / 2], (j & 1) ? 0x07060302u : 0x05040100u);
+        b[e] = __builtin_amdgcn_perm(w[2 * e + 1][j / 2], w[2 * e][j / 2], (j & 1) ? 0x07060302u : 0x05040100u);
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[m][j] = mfma<DT>(b, x[m], acc[m][j]);
     }
   };
-  U16 w0[8], w1[8];
-  int run = r0 + wave;
-  if (run < r1) load(run, w0);
-  while (run < r1) {
-    if (run + kSkWaves < r1) load(run + kSkWaves, w1);
-    step(run, w0);
-    run += kSkWaves;
-    if (run >= r1) break;
-    if (run + kSkWaves < r1) load(run + kSkWaves, w0);
-    step(run, w1);
-    run += kSkWaves;
+  // one run in flight per wave: sixteen waves per CU keep 128 KB on the way
+  for (int run = r0 + wave; run < r1; run += kSkWaves) {
+    U16 w[8];
+    load(run, w);
+    step(run, w);
   }
 
   // waves summed in order, 16 rows at a time: thread t finishes row t / 16, columns 8 (t % 16) .. + 7
@@ -643,15 +653,15 @@ __device__ __forceinline__ void pad_rows(const uint16_t *src, int rows, int cols
   if (t >= (long long)rows * cpr) return;
   const int r = (int)(t / cpr), c = (int)(t % cpr) * 8;
   const uint16_t *p = src + (size_t)r * cols + c;
-  U16 v = U16{{0u, 0u, 0u, 0u}};
+  v4u v = {0u, 0u, 0u, 0u};
   if (c + 8 <= cols) {
     v = *reinterpret_cast<const U16 *>(p);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (c + e < cols) v.d[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+      if (c + e < cols) v[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
   }
-  *reinterpret_cast<v4u *>(dst + (size_t)r * ld + c) = (v4u){v.d[0], v.d[1], v.d[2], v.d[3]};
+  *reinterpret_cast<v4u *>(dst + (size_t)r * ld + c) = v;
 }
 
 // dZ = dY act'(Z), rounded to the operand type of the two products, and the
@@ -673,45 +683,67 @@ __device__ __forceinline__ void lin_dz(const LinDz &a, int bx, int by) {
     if (n >= 8) {
       const U16 t = *reinterpret_cast<const U16 *>(p);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = half_to_f32<DT>((t.d[e / 2] >> (16 * (e & 1))) & 0xFFFFu);
+      for (int e = 0; e < 8; ++e) v[e] = half_to_f32<DT>((t[e / 2] >> (16 * (e & 1))) & 0xFFFFu);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = e < n ? half_to_f32<DT>(p[e]) : 0.0f;
     }
   };
-  if (n > 0)
-    for (int m = m0 + ry; m < m1; m += kDzRows) {
-      const size_t o = (size_t)m * a.N + j;
-      float d[8], z[8];
-      if (a.dy_f32) {
-        const float *p = static_cast<const float *>(a.dY) + o;
+  auto load = [&](int m, float *d, float *z) __attribute__((always_inline)) {
+    const size_t o = (size_t)m * a.N + j;
+    if (a.dy_f32) {
+      const float *p = static_cast<const float *>(a.dY) + o;
+      if (n >= 8) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const F32x4 t = *reinterpret_cast<const F32x4 *>(p + 4 * c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[4 * c + e] = t[e];
+        }
+      } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) d[e] = e < n ? p[e] : 0.0f;
-      } else {
-        half8(static_cast<const uint16_t *>(a.dY) + o, d);
       }
-      if (a.act != kActIdentity) {
-        half8(a.Z + o, z);
-        if (a.act == kActGeluTanh) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] *= act_grad(z[e], kActGeluTanh);
-        } else if (a.act == kActGelu) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] *= act_grad(z[e], kActGelu);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] *= act_grad(z[e], kActSilu);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] += d[e];
-      if (a.dZ) {
-        v4u t;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] = f32_to_half<DT>(d[2 * e]) | (f32_to_half<DT>(d[2 * e + 1]) << 16);
-        *reinterpret_cast<v4u *>(a.dZ + (size_t)m * a.np + j) = t;
-      }
+    } else {
+      half8(static_cast<const uint16_t *>(a.dY) + o, d);
     }
+    if (a.act != kActIdentity) half8(a.Z + o, z);
+  };
+  auto work = [&](int m, float *d, const float *z) __attribute__((always_inline)) {
+    if (a.act == kActGeluTanh) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] *= act_grad(z[e], kActGeluTanh);
+    } else if (a.act == kActGelu) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] *= act_grad(z[e], kActGelu);
+    } else if (a.act == kActSilu) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] *= act_grad(z[e], kActSilu);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += d[e];
+    if (a.dZ) {
+      v4u t;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[e] = f32_to_half<DT>(d[2 * e]) | (f32_to_half<DT>(d[2 * e + 1]) << 16);
+      *reinterpret_cast<v4u *>(a.dZ + (size_t)m * a.np + j) = t;
+    }
+  };
+  if (n > 0) {
+    int m = m0 + ry;
+    for (; m + kDzRows < m1; m += 2 * kDzRows) {   // two rows in flight
+      float d0[8], z0[8], d1[8], z1[8];
+      load(m, d0, z0);
+      load(m + kDzRows, d1, z1);
+      work(m, d0, z0);
+      work(m + kDzRows, d1, z1);
+    }
+    if (m < m1) {
+      float d[8], z[8];
+      load(m, d, z);
+      work(m, d, z);
+    }
+  }
   if (!a.db) return;
 #pragma unroll
   for (int e = 0; e < 8; ++e) red[ry][8 * cx + e] = s[e];
@@ -743,46 +775,73 @@ constexpr int kCus = 256;
 
 int quarters(int I, int J) { return ceil_div(I, 128) * ceil_div(J, 128); }
 
-// Splits of the reduction: for so few 128 x 128 tiles that one round leaves
-// half of the CUs idle, at least 256 of the reduction each.
+// Splits of the reduction: towards 128 workgroups of 128 x 128 tiles, at least
+// 256 of the reduction each.  64 x 12288 x 4096 (32 tiles): 4 splits 39 us, 8
+// 44, 2 64, none 112; 64 x 4096 x 12288 (96 tiles): none 44 us, 2 49.
 int gemm_splits(int I, int J, int R) {
-  return std::max(1, std::min({kCus / quarters(I, J), R / 256, 16}));
+  return std::max(1, std::min({kCus / 2 / quarters(I, J), R / 256, 16}));
 }
 
-// How the last tiles are cut.  `rem` tiles remain after whole rounds of one
-// 256 x 256 tile per CU; a round of halves costs 0.62 of a round of whole
-// tiles, one of quarters 0.38.
+// How the last `rem` of the tiles, after whole rounds of one 256 x 256 tile
+// per CU, are cut: in 1, 2 or 4.  The cost of a round relative to a full one
+// of whole tiles (115 us at a reduction of 4096): 0.55 for halves, 0.34 for
+// quarters, and a round that fills only the share f of the CUs costs 0.35 +
+// 0.65 f of that (the chip is power-limited: idle CUs speed up the others).
+// Measured, us: 1.5 rounds whole 192, halves 176, quarters 193; 0.66 rounds 76,
+// 90, 88; 1.125 rounds 76, 62, 56.
 int best_cut(int rem) {
-  const float full = 1.0f, half = 0.62f * ceil_div(2 * rem, kCus), quarter = 0.38f * ceil_div(4 * rem, kCus);
+  auto cost = [](int units, float round) {
+    const int part = units % kCus;
+    return round * (units / kCus + (part ? 0.35f + 0.65f * part / kCus : 0.0f));
+  };
+  const float full = cost(rem, 1.0f), half = cost(2 * rem, 0.55f), quarter = cost(4 * rem, 0.34f);
   return full <= half && full <= quarter ? 1 : half <= quarter ? 2 : 4;
 }
 
-// Sets the units of the jobs of one launch; the last tiles are the last job's.
-void plan_units(LinGemm *job, int n) {
-  int tiles = 0;
-  for (int i = 0; i < n; ++i) {
-    LinGemm &a = job[i];
-    a.nbi = ceil_div(a.I, 256);
-    a.nbj = ceil_div(a.J, 256);
-    if (a.splits <= 1) tiles += a.nbi * a.nbj;
+// Sets the units of the jobs of one launch.  The job with the longer reduction
+// runs first; the tiles left over from whole rounds, counted in tiles of the
+// second, are the second's last.
+void plan_units(LinGemm &a, LinGemm &b) {
+  LinGemm *order[2] = {&a, &b};
+  if (b.R > a.R) std::swap(order[0], order[1]);
+  double work = 0.0;
+  for (LinGemm *j : order) {
+    j->nbi = ceil_div(j->I, 256);
+    j->nbj = ceil_div(j->J, 256);
+    if (j->splits <= 1) work += (double)j->nbi * j->nbj * j->R;
   }
-  int rem = tiles % kCus;
-  const int cut = best_cut(rem);
-  for (int i = n - 1; i >= 0; --i) {
-    LinGemm &a = job[i];
-    const int t = a.nbi * a.nbj;
-    if (a.splits > 1) {
-      a.full = 0; a.cut = 4; a.parts = 4 * t * a.splits;
-      continue;
+  LinGemm *last = order[1]->nbi * order[1]->nbj > 0 && order[1]->splits <= 1 ? order[1] : order[0];
+  const int rem = last->R > 0 ? (int)(work / last->R) % kCus : 0, cut = best_cut(rem);
+  int base = 0;
+  for (LinGemm *j : order) {
+    const int t = j->nbi * j->nbj;
+    j->cut = cut;
+    j->full = t;
+    j->parts = 0;
+    if (j->splits > 1) {
+      j->full = 0; j->cut = 4; j->parts = 4 * t * j->splits;
+    } else if (j == last && cut > 1) {
+      j->full = std::max(0, t - rem);
+      j->parts = (t - j->full) * cut;
     }
-    const int last = cut == 1 ? 0 : std::min(t, rem);
-    rem -= last;
-    a.full = t - last; a.cut = cut; a.parts = last * cut;
+    j->full0 = base;
+    base += j->full;
+  }
+  for (LinGemm *j : order) {
+    j->parts0 = base;
+    base += j->parts;
   }
 }
 
+// Splits of K of the weight-streaming kernel: the fewest whose workgroups
+// fill nine tenths of whole rounds over the CUs, at least 256 of K each.
+// 1 x 4096 x 12288 (96 strips): 5 splits 22.1 us, 4 and 8 22.4, 3 25.8; 16 x
+// 12288 x 4096 (32 strips): 8 splits 23.6 us, 16 24.9, 12 26.8.
 int skinny_splits(int J, int K) {
-  return std::max(1, std::min({512 / ceil_div(J, kSkCols), K / 256, 16}));
+  const int strips = ceil_div(J, kSkCols), most = std::max(1, std::min(K / 256, 16));
+  for (int s = 1; s < most; ++s)
+    if (10 * strips * s >= 9 * kCus * ceil_div(strips * s, kCus)) return s;
+  return most;
 }
 
 size_t part_bytes(int I, int J, int splits) {
@@ -816,10 +875,10 @@ hipError_t run_forward(LinGemm a, bool skinny, hipStream_t s) {
   hipError_t e;
   if (skinny) {
     const int mt = ceil_div(a.I, 16);
-    e = mt == 1 ? run_skinny<DT, 1>(a, s) : mt == 2 ? run_skinny<DT, 2>(a, s)
-        : mt == 3 ? run_skinny<DT, 3>(a, s) : run_skinny<DT, 4>(a, s);
+    e = mt == 1 ? run_skinny<DT, 1>(a, s) : mt == 2 ? run_skinny<DT, 2>(a, s) : run_skinny<DT, 3>(a, s);
   } else {
-    plan_units(&a, 1);
+    LinGemm none{};
+    plan_units(a, none);
     hipLaunchKernelGGL(k_lin_fwd<DT>, dim3((unsigned)(a.full + a.parts)), dim3(512), 0, s, a);
     e = hipGetLastError();
   }
@@ -830,7 +889,7 @@ template <int DT>
 hipError_t run_backward(const LinGemm &x, const LinGemm &w, hipStream_t s) {
   LinGemm job[2] = {x, w};
   const bool has_x = x.out != nullptr, has_w = w.out != nullptr;
-  plan_units(has_x ? job : job + 1, has_x && has_w ? 2 : 1);
+  plan_units(job[0], job[1]);
   hipLaunchKernelGGL(k_lin_bwd<DT>, dim3((unsigned)(job[0].full + job[0].parts + job[1].full + job[1].parts)), dim3(512),
                      0, s, job[0], job[1]);
   const hipError_t e = hipGetLastError();
@@ -866,8 +925,9 @@ LinPlan plan_linear_backward(int M, int K, int N) {
   p.pad_w = p.np != N;
   p.splits_dx = gemm_splits(M, K, N);
   p.splits_dw = gemm_splits(K, N, M);
-  // row slices of the dZ pass: about 1024 workgroups, at least 32 rows each
-  p.slices = std::max(1, std::min(1024 / ceil_div(p.np, kDzCols), ceil_div(M, 32)));
+  // row slices of the dZ pass: about 1024 workgroups, at least one row per
+  // thread
+  p.slices = std::max(1, std::min(1024 / ceil_div(p.np, kDzCols), ceil_div(M, kDzRows)));
   size_t off = 0;
   p.x_off = off;
   if (p.pad_x) off = align_up(off + (size_t)M * p.kp * 2, 256);
