@@ -443,7 +443,7 @@ int hsq_closed_form_l2(const float *HL1, const double *Cinv, int K, int N, int r
  *
  * with 16-bit operands, fp32 sums and an fp32 epilogue, rounded once at each
  * store.  Any M, K, N >= 1 with M * K, K * N, M * N < 2^30 (K and N
- * rounded up to 8 where they are row lengths).
+ * rounded up to 8 where they are row lengths) and K, N <= 2^24.
  *   X         in : M x K of `dtype` (HSQ_BF16 or HSQ_F16)
  *   W         in : K x N of `dtype` (input channel x output channel)
  *   bias      in : N of `dtype`, or NULL
@@ -505,7 +505,8 @@ int hsq_linear_backward(const void *dY, int y_dtype, const uint16_t *X, int M, i
  *   rstd     out: M fp32 each, or NULL: as the backward pass takes them
  * y_dtype is x_dtype, or any of the three where x_dtype is HSQ_F32; p_dtype
  * is HSQ_F32 or y_dtype.  1 <= C <= 16384, groups divides M (HSQ_E_SHAPE)
- * and is at most 65535, M * C < 2^31; eps is finite and not negative.
+ * and is at most 65535, M <= 2^25, M * C < 2^31; eps is finite and not
+ * negative.
  * Arithmetic is fp32, the variance taken around the finished mean.
  * Errors: HSQ_E_INVAL, HSQ_E_SHAPE, HSQ_E_ALIGN, HSQ_E_HIP. */
 int hsq_layer_norm(const void *X, int x_dtype, int M, int C, int groups, const void *weight,

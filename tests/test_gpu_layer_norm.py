@@ -235,6 +235,41 @@ def test_replay_streams_and_repeats():
             assert all(torch.equal(a, c) for a, c in zip(o, ref))
 
 
+@pytest.mark.parametrize("M,C", [(131071, 16384), (1 << 25, 61)])
+def test_largest_sizes(M, C):
+    # rows sampled over the whole range; the parameter gradients of all rows
+    say(f"[norm large] {M} {C}")
+    g = torch.Generator(device=DEV).manual_seed(6)
+    X = torch.empty(M, C, device=DEV, dtype=BF).normal_(generator=g)
+    dY = torch.empty(M, C, device=DEV, dtype=BF).normal_(generator=g)
+    w, b = torch.rand(C, generator=g, device=DEV) + 0.5, torch.rand(C, generator=g, device=DEV)
+    rows = torch.cat([torch.arange(0, M, M // 60, device=DEV), torch.tensor([M - 1], device=DEV)])
+    y, mean, rstd = hsq.layer_norm(X, w, b, return_stats=True)
+    ry, rm, rr = layer_norm64(X[rows], w, b, 1e-5)
+    close(y[rows], ry, forward_bound(X[rows], w, b, ry, rm, rr, 1e-5)[0], BF, "Y")
+    del y
+    dX, dw, db = hsq.layer_norm_backward(dY, X, mean, rstd, w)
+    x, dy, r = X[rows].double(), dY[rows].double(), rstd[rows].double()[:, None]
+    rX = layer_norm_backward64(dy, x, mean[rows], rstd[rows], w)[0]
+    xh, gr = ((x - mean[rows].double()[:, None]) * r).abs(), dy.abs() * w.double()
+    close(dX[rows], rX, (DEPTH + 12) * U32 * r * (gr + gr.mean(1, keepdim=True) + xh * (gr * xh).mean(1, keepdim=True)),
+          BF, "dX")
+    del dX
+    # a workgroup adds its share of the rows one by one, 256 shares (8 rows side by side in short rows)
+    for c in (0, C // 2, C - 1):
+        col, wx = dY[:, c].double(), (X[:, c].double() - mean.double()) * rstd.double()
+        n = M // 256 + 300
+        assert abs(db[c] - col.sum()) <= n * U32 * col.abs().sum() + U32 * db[c].abs()
+        assert abs(dw[c] - (col * wx).sum()) <= (n + 12) * U32 * (col * wx).abs().sum() + U32 * dw[c].abs()
+
+
+def test_more_rows_than_a_launch_has_threads_for_are_refused():
+    X = torch.zeros((1 << 26) - 1, 1, device=DEV, dtype=BF)
+    with pytest.raises(hsq.HsqError) as e:
+        hsq.layer_norm(X)
+    assert e.value.status == hsq.E_INVAL
+
+
 def rel(a, b):
     return ((a.double() - b).norm() / b.norm()).item()
 

@@ -249,6 +249,16 @@ def test_activations_at_the_ends(act):
     assert Y[20].isnan() and dX[20].isnan()
 
 
+@pytest.mark.parametrize("act", ["gelu_tanh", "gelu", "silu"])
+def test_slope_at_a_stored_infinity(act):
+    # a Z beyond fp16 is stored as an infinity: its slope is 1 or 0, not NaN
+    X = torch.tensor([[float("inf")], [float("-inf")]], device=DEV, dtype=F16)
+    W, dY = torch.ones(1, 1, dtype=F16, device=DEV), torch.ones(2, 1, dtype=F16, device=DEV)
+    dX = hsq.linear_backward(dY, X, W, X, act=act, need_weight=False, need_bias=False)[0]
+    # below -64 the slope is at most 65 e^-64 < 1e-25, below fp16's smallest value (6e-8) by far
+    assert dX[0] == 1 and dX[1] == 0
+
+
 @pytest.mark.parametrize("M,K,N", [(8, 512, 384), (100, 512, 384), (333, 130, 257)])
 def test_gradient_against_differences(M, K, N):
     # L = sum(dY * Y): the library's gradient along a direction v against the
@@ -320,3 +330,79 @@ def test_replay_streams_and_repeats():
         torch.cuda.synchronize()
         for g in got:
             assert all(torch.equal(a, c) for a, c in zip(g, ref))
+
+
+LARGE = [
+    # each of the three matrices in turn close to 2^30 elements
+    (262143, 4088, 72),
+    (3, 4088, 262136),
+    (70, 4088, 262136),
+    (262143, 16, 4088),
+]
+
+
+@pytest.mark.parametrize("M,K,N", LARGE)
+def test_largest_sizes(M, K, N):
+    # rows and columns sampled over the whole range, the last ones among them
+    say(f"[linear large] {M} {K} {N}")
+    g = torch.Generator(device=DEV).manual_seed(9)
+    X = torch.empty(M, K, device=DEV, dtype=BF).normal_(generator=g)
+    W = torch.empty(K, N, device=DEV, dtype=BF).normal_(generator=g)
+    rows = torch.cat([torch.arange(0, M, max(1, M // 50), device=DEV), torch.tensor([M - 1], device=DEV)])
+    cols = torch.cat([torch.arange(0, N, max(1, N // 50), device=DEV), torch.tensor([N - 1], device=DEV)])
+    Y = hsq.linear(X, W, y_dtype="f32")
+    Xs, Ws = X[rows], W[:, cols].contiguous()
+    y, _, ty, _ = linear64(Xs, Ws, None, None, "identity")
+    close(Y[rows][:, cols], y, ty, F32, "Y")
+    del Y
+    dY = torch.empty(M, N, device=DEV, dtype=BF).normal_(generator=g)
+    dX, dW, db = hsq.linear_backward(dY, X, W)
+    kc = torch.cat([torch.arange(0, K, max(1, K // 20), device=DEV), torch.tensor([K - 1], device=DEV)])
+    d = dY[rows].double()
+    w = W[kc].double()
+    close(dX[rows][:, kc], d @ w.t(), 2 * N * 2.0 ** -24 * (d.abs() @ w.abs().t()), BF, "dX")
+    x, d = X[:, kc].double(), dY[:, cols].double()
+    xt = x.t().contiguous()
+    close(dW[kc][:, cols], xt @ d, 2 * M * 2.0 ** -24 * (xt.abs() @ d.abs()), BF, "dW")
+    close(db[cols], d.sum(0), 2 * M * 2.0 ** -24 * d.abs().sum(0), BF, "db")
+
+
+def test_wide_rows():
+    # the widest N and K, one token
+    say("[linear wide]")
+    for K, N in ((3, 1 << 24), (1 << 24, 3)):
+        X, W, b, rnd = make(13, 1, K, N, BF)
+        y, _, ty, _ = linear64(X, W, b, None, "identity")
+        close(hsq.linear(X, W, b, y_dtype="f32"), y, ty, F32, "Y")
+        dY = rnd(1, N).to(BF)
+        (rX, rW, rb), (tX, tW, tb) = linear_backward64(dY, X, W, None, "identity")
+        dX, dW, db = hsq.linear_backward(dY, X, W)
+        close(dX, rX, tX, BF, "dX")
+        close(dW, rW, tW, BF, "dW")
+        close(db, rb, tb, BF, "db")
+
+
+def test_host_threads():
+    """Calls from several host threads at once, a stream and buffers each."""
+    import threading
+
+    say("[linear threads]")
+    M, K, N = 150, 700, 333
+    X, W, b, rnd = make(19, M, K, N, F16)
+    dY = rnd(M, N).to(F16)
+    ref = hsq.linear_backward(dY, X, W) + (hsq.linear(X, W, b),)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got = hsq.linear_backward(dY, X, W) + (hsq.linear(X, W, b),)
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(a, c) for a, c in zip(got, ref)):
+                    bad.append(1)
+
+    ts = [threading.Thread(target=work) for _ in range(4)]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    assert not bad

@@ -33,6 +33,7 @@ def _linear(**kw):
     (dict(M=1 << 18, K=1 << 12), hsq.E_INVAL),             # M * K = 2^30
     (dict(K=1 << 15, N=1 << 15, M=1), hsq.E_INVAL),        # K * N = 2^30
     (dict(M=1 << 27, K=1, N=1), hsq.E_INVAL),              # rows of 1 rounded up to 8: 2^30
+    (dict(M=1, K=1, N=(1 << 24) + 1), hsq.E_INVAL), (dict(M=1, K=(1 << 24) + 1, N=1), hsq.E_INVAL),
     (dict(M=333, K=1001, N=777, wsb=0), hsq.E_WORKSPACE),  # ragged rows are staged
     (dict(M=333, K=1001, N=777, ws=None, wsb=1 << 30), hsq.E_WORKSPACE),
 ])
@@ -70,6 +71,7 @@ def _norm(**kw):
 SIZES = [
     (dict(M=0), hsq.E_INVAL), (dict(C=0), hsq.E_INVAL), (dict(C=16385), hsq.E_INVAL), (dict(G=0), hsq.E_INVAL),
     (dict(G=65536, M=65536), hsq.E_INVAL), (dict(G=5), hsq.E_SHAPE), (dict(M=1 << 20, C=1 << 11), hsq.E_INVAL),
+    (dict(M=(1 << 25) + 1, C=2), hsq.E_INVAL),
     (dict(xdt=3), hsq.E_INVAL), (dict(ydt=hsq.F32), hsq.E_INVAL), (dict(ydt=hsq.F16), hsq.E_INVAL),
     (dict(pdt=hsq.F16), hsq.E_INVAL), (dict(xdt=hsq.F32, ydt=hsq.F32, pdt=hsq.BF16), hsq.E_INVAL),
     (dict(X=None), hsq.E_INVAL), (dict(X=A + 2), hsq.E_ALIGN), (dict(w=A + 4), hsq.E_ALIGN),

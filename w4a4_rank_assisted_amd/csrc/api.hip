@@ -114,9 +114,14 @@ int calib_sizes(int K) {
 // 16-bit linear: every matrix, its row length rounded up to 8, stays below
 // 2^31 bytes (32-bit buffer offsets).
 constexpr long long kLinMaxElems = 1LL << 30;
+// Widths stay where every launch has fewer than 2^32 threads a dimension (the
+// sum of partial rows runs 32 threads per column); likewise the norm's rows,
+// of which the shortest take a wave each.
+constexpr int kLinMaxWidth = 1 << 24;
+constexpr int kNormMaxRows = 1 << 25;
 
 int lin_sizes(int M, int K, int N) {
-  if (M < 1 || K < 1 || N < 1) return HSQ_E_INVAL;
+  if (M < 1 || K < 1 || N < 1 || K > kLinMaxWidth || N > kLinMaxWidth) return HSQ_E_INVAL;
   const long long kp = ((long long)K + 7) / 8 * 8, np = ((long long)N + 7) / 8 * 8;
   if (M * kp >= kLinMaxElems || K * np >= kLinMaxElems || M * np >= kLinMaxElems) return HSQ_E_INVAL;
   return HSQ_OK;
@@ -132,7 +137,7 @@ int norm_check(int M, int C, int groups, int x_dtype, int y_dtype, int p_dtype) 
   auto known = [](int t) { return t == HSQ_F32 || t == HSQ_BF16 || t == HSQ_F16; };
   if (!known(x_dtype) || !known(y_dtype) || !known(p_dtype)) return HSQ_E_INVAL;
   if ((y_dtype != x_dtype && x_dtype != HSQ_F32) || (p_dtype != HSQ_F32 && p_dtype != y_dtype)) return HSQ_E_INVAL;
-  if (M < 1 || C < 1 || C > kNormMaxC || (long long)M * C >= INT_MAX || groups < 1 || groups > 65535)
+  if (M < 1 || M > kNormMaxRows || C < 1 || C > kNormMaxC || (long long)M * C >= INT_MAX || groups < 1 || groups > 65535)
     return HSQ_E_INVAL;
   return M % groups == 0 ? HSQ_OK : HSQ_E_SHAPE;
 }

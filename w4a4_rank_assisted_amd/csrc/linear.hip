@@ -72,8 +72,10 @@ __device__ __forceinline__ float act_grad(float z, int act) {
     const float z2 = z * z, e = exp_neg(z * fmaf(kG1, z2, kG0)), p = __builtin_amdgcn_rcpf(1.0f + e);
     return fmaf(z * fmaf(3.0f * kG1, z2, kG0), e * p * p, p);
   }
-  if (act == kActGelu)
+  if (act == kActGelu) {                 // an infinite Z has slope 0 or 1 too
+    z = limited(z, 16.0f);
     return fmaf(z * 0.39894228f, __builtin_amdgcn_exp2f(z * z * -0.72134752f), 0.5f * (1.0f + erff(z * 0.70710678f)));
+  }
   if (act == kActSilu) {
     z = limited(z, 64.0f);
     const float e = exp_neg(z), p = __builtin_amdgcn_rcpf(1.0f + e);
