@@ -131,24 +131,6 @@ def test_constants_match_header():
     assert consts["HSQ_ACT_SILU"] == hsq.ACT_SILU
 
 
-class _Fake:
-    """Stands for a device tensor where the binding looks before it calls."""
-
-    @staticmethod
-    def patch(monkeypatch):
-        monkeypatch.setattr(hsq, "_dev_tensor", lambda t, name, dtypes, shape=None: _Fake.check(t, name, dtypes, shape))
-
-    @staticmethod
-    def check(t, name, dtypes, shape):
-        if dtypes and t.dtype not in dtypes:
-            raise TypeError(name)
-        if not t.is_contiguous():
-            raise ValueError(name)
-        if shape is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(name)
-        return t
-
-
 def test_binding_refuses_host_tensors():
     x = torch.zeros(4, 8, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="HIP device"):
@@ -162,7 +144,8 @@ def test_binding_refuses_host_tensors():
 
 
 def test_binding_refuses_shapes_and_types(monkeypatch):
-    _Fake.patch(monkeypatch)
+    # host tensors stand for device tensors up to the call: both are on "device" -1
+    monkeypatch.setattr(hsq, "_device", lambda t, name: -1)
     bf, f16, f32 = torch.bfloat16, torch.float16, torch.float32
     x, w = torch.zeros(4, 8, dtype=bf), torch.zeros(8, 16, dtype=bf)
     for bad in (torch.zeros(7, 16, dtype=bf), torch.zeros(8, dtype=bf)):
@@ -206,14 +189,21 @@ def test_binding_refuses_shapes_and_types(monkeypatch):
 
 
 def test_binding_refuses_another_device(monkeypatch):
-    class T:
-        def __init__(self, i):
-            self.device = torch.device("cuda", i)
+    class T(torch.Tensor):
+        def get_device(self):
+            return 1
 
+    other = torch.zeros(4, 8, dtype=torch.bfloat16).as_subclass(T)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    hsq._on_current_device(T(0), None)
     with pytest.raises(ValueError, match="current device"):
-        hsq._on_current_device(T(0), T(1))
+        hsq.layer_norm(other)
+    with pytest.raises(ValueError, match="current device"):
+        hsq.linear(other, other)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="HIP device 1"):      # X there, W on the host
+        hsq.linear(other, torch.zeros(8, 8, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="HIP device 1"):
+        hsq.layer_norm(other, torch.zeros(8, dtype=torch.bfloat16))
 
 
 # ------------------------------------------------------- the definitions

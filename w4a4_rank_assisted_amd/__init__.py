@@ -116,10 +116,16 @@ def header_functions():
 
 
 # --------------------------------------------------------------- marshalling
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -561,14 +567,45 @@ def _half16():
     return (torch.bfloat16, torch.float16)
 
 
-def _on_current_device(*tensors):
-    """The kernels run on the current stream of the current device: every
-    tensor has to live there."""
+def _norm_types():
     torch = _torch()
+    return (torch.float32, torch.bfloat16, torch.float16)
+
+
+def _device(t, name) -> int:
+    """Index of the device the kernels run on: the current one, on whose
+    current stream they are enqueued.  Every tensor has to live there."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be on a HIP device")
     cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{cur}")
+    if dev != cur:
+        raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{cur}")
+    return dev
+
+
+def _arg(t, name, dev: int, dtypes, shape=None) -> int:
+    """Checks one operand and returns its device pointer (one pass over the
+    tensor's properties: these calls are short)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on HIP device {dev}, the current device and that of the other operands")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _raw_stream(dev: int) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(dev)
 
 
 def _y_type(y_dtype, x_dtype, allowed):
@@ -583,15 +620,26 @@ def _y_type(y_dtype, x_dtype, allowed):
     return t
 
 
-def _scratch(workspace, need: int, device):
+def _scratch(workspace, need, X, dev):
+    """(workspace, pointer, bytes): the caller's, or a new one of need() bytes."""
     torch = _torch()
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    return _dev_tensor(workspace, "workspace", (torch.uint8,))
+        n = int(need())
+        if n == 0:
+            return None, None, 0
+        workspace = torch.empty(n, dtype=torch.uint8, device=X.device)
+        return workspace, workspace.data_ptr(), n
+    return workspace, _arg(workspace, "workspace", dev, (torch.uint8,)), workspace.numel()
 
 
 def linear_workspace_bytes(M: int, K: int, N: int) -> int:
     return int(_load().hsq_linear_workspace_bytes(M, K, N))
+
+
+def _columns(W, X, K: int) -> int:
+    if W.dim() != 2 or W.shape[0] != K:
+        raise ValueError(f"W: shape {tuple(W.shape)} does not follow X {tuple(X.shape)}")
+    return W.shape[1]
 
 
 def linear(X, W, bias=None, residual=None, *, act: str = "identity", y_dtype=None, out=None,
@@ -604,37 +652,30 @@ def linear(X, W, bias=None, residual=None, *, act: str = "identity", y_dtype=Non
     (Y, Z)."""
     torch = _torch()
     lib = _load()
-    _dev_tensor(X, "X", _half16())
+    dts = _dtypes()
+    dev = _device(X, "X")
+    px = _arg(X, "X", dev, _half16())
     M, K = X.shape
     dt = X.dtype
-    _dev_tensor(W, "W", (dt,))
-    if W.dim() != 2 or W.shape[0] != K:
-        raise ValueError(f"W: shape {tuple(W.shape)} does not follow X {tuple(X.shape)}")
-    N = int(W.shape[1])
+    half = (dt,)
+    pw = _arg(W, "W", dev, half)
+    N = _columns(W, X, K)
     if act not in _LINEAR_ACTS:
         raise ValueError(f"act {act!r} not in {sorted(_LINEAR_ACTS)}")
-    ydt = _y_type(y_dtype, dt, (torch.float32, dt))
-    if bias is not None:
-        _dev_tensor(bias, "bias", (dt,), (N,))
-    if residual is not None:
-        _dev_tensor(residual, "residual", (ydt,), (M, N))
+    ydt = dt if y_dtype is None else _y_type(y_dtype, dt, (torch.float32, dt))
+    pb = None if bias is None else _arg(bias, "bias", dev, half, (N,))
+    pr = None if residual is None else _arg(residual, "residual", dev, (ydt,), (M, N))
     if out is None:
         out = torch.empty((M, N), dtype=ydt, device=X.device)
+        po = out.data_ptr()
     else:
-        _dev_tensor(out, "out", (ydt,), (M, N))
-    if preact_out is not None:
-        _dev_tensor(preact_out, "preact_out", (dt,), (M, N))
-    elif return_preact:
+        po = _arg(out, "out", dev, (ydt,), (M, N))
+    if preact_out is None and return_preact:
         preact_out = torch.empty((M, N), dtype=dt, device=X.device)
-    if workspace is None:
-        need = int(lib.hsq_linear_workspace_bytes(M, K, N))
-        workspace = _scratch(None, need, X.device) if need else None
-    else:
-        _dev_tensor(workspace, "workspace", (torch.uint8,))
-    _on_current_device(X, W, bias, residual, out, preact_out, workspace)
-    _check(lib.hsq_linear(_ptr(X), M, K, N, _dtypes()[dt], _ptr(W), _ptr(bias), _LINEAR_ACTS[act],
-                          _ptr(residual), _ptr(out), _dtypes()[ydt], _ptr(preact_out), _ptr(workspace),
-                          0 if workspace is None else workspace.numel(), _stream()), "hsq_linear")
+    pz = None if preact_out is None else _arg(preact_out, "preact_out", dev, half, (M, N))
+    workspace, ps, nbytes = _scratch(workspace, lambda: lib.hsq_linear_workspace_bytes(M, K, N), X, dev)
+    _check(lib.hsq_linear(px, M, K, N, dts[dt], pw, pb, _LINEAR_ACTS[act], pr, po, dts[ydt], pz, ps, nbytes,
+                          _raw_stream(dev)), "hsq_linear")
     return (out, preact_out) if return_preact else out
 
 
@@ -650,39 +691,33 @@ def linear_backward(dY, X, W, preact=None, *, act: str = "identity", need_input:
     the residual's gradient is dY itself."""
     torch = _torch()
     lib = _load()
-    _dev_tensor(X, "X", _half16())
+    dts = _dtypes()
+    dev = _device(X, "X")
+    px = _arg(X, "X", dev, _half16())
     M, K = X.shape
     dt = X.dtype
-    _dev_tensor(W, "W", (dt,))
-    if W.dim() != 2 or W.shape[0] != K:
-        raise ValueError(f"W: shape {tuple(W.shape)} does not follow X {tuple(X.shape)}")
-    N = int(W.shape[1])
+    pw = _arg(W, "W", dev, (dt,))
+    N = _columns(W, X, K)
     if act not in _LINEAR_ACTS:
         raise ValueError(f"act {act!r} not in {sorted(_LINEAR_ACTS)}")
-    _dev_tensor(dY, "dY", (dt, torch.float32), (M, N))
-    if act != "identity":
-        _dev_tensor(preact, "preact", (dt,), (M, N))
-    else:
-        preact = None
+    py = _arg(dY, "dY", dev, (dt, torch.float32), (M, N))
+    pz = None if act == "identity" else _arg(preact, "preact", dev, (dt,), (M, N))
     dX = torch.empty((M, K), dtype=dt, device=X.device) if need_input else None
     dW = torch.empty((K, N), dtype=dt, device=X.device) if need_weight else None
     db = torch.empty((N,), dtype=dt, device=X.device) if need_bias else None
-    workspace = _scratch(workspace, 0 if workspace is not None else
-                         int(lib.hsq_linear_backward_workspace_bytes(M, K, N)), X.device)
-    _on_current_device(dY, X, W, preact, workspace)
-    _check(lib.hsq_linear_backward(_ptr(dY), _dtypes()[dY.dtype], _ptr(X), M, K, N, _dtypes()[dt], _ptr(W),
-                                   _ptr(preact), _LINEAR_ACTS[act], _ptr(dX), _ptr(dW), _ptr(db),
-                                   _ptr(workspace), workspace.numel(), _stream()), "hsq_linear_backward")
+    workspace, ps, nbytes = _scratch(workspace, lambda: lib.hsq_linear_backward_workspace_bytes(M, K, N), X, dev)
+    _check(lib.hsq_linear_backward(py, dts[dY.dtype], px, M, K, N, dts[dt], pw, pz, _LINEAR_ACTS[act], _ptr(dX),
+                                   _ptr(dW), _ptr(db), ps, nbytes, _raw_stream(dev)), "hsq_linear_backward")
     return dX, dW, db
 
 
-def _norm_param(p, name, ydt, C):
-    """weight / bias (C,) or (groups, C), fp32 or of Y's type -> groups."""
+def _norm_param(p, name, dev, ydt, C):
+    """weight / bias (C,) or (groups, C), fp32 or of Y's type -> (pointer, groups)."""
     torch = _torch()
-    _dev_tensor(p, name, (torch.float32, ydt))
+    ptr = _arg(p, name, dev, (torch.float32, ydt))
     if p.dim() not in (1, 2) or p.shape[-1] != C:
         raise ValueError(f"{name}: shape {tuple(p.shape)} is neither ({C},) nor (groups, {C})")
-    return 1 if p.dim() == 1 else int(p.shape[0])
+    return ptr, 1 if p.dim() == 1 else p.shape[0]
 
 
 def layer_norm(X, weight=None, bias=None, *, eps: float = 1e-5, y_dtype=None, out=None,
@@ -696,27 +731,31 @@ def layer_norm(X, weight=None, bias=None, *, eps: float = 1e-5, y_dtype=None, ou
     torch = _torch()
     lib = _load()
     dts = _dtypes()
-    _dev_tensor(X, "X", (torch.float32, torch.bfloat16, torch.float16))
+    dev = _device(X, "X")
+    px = _arg(X, "X", dev, _norm_types())
     M, C = X.shape
-    ydt = _y_type(y_dtype, X.dtype, (X.dtype,) if X.dtype != torch.float32 else
-                  (torch.float32, torch.bfloat16, torch.float16))
-    groups, pdt = 1, torch.float32
-    for p, name in ((weight, "weight"), (bias, "bias")):
-        if p is not None:
-            groups, pdt = _norm_param(p, name, ydt, C), p.dtype
-    if weight is not None and bias is not None and (weight.shape != bias.shape or weight.dtype != bias.dtype):
-        raise ValueError("weight and bias differ in shape or type")
+    xdt = X.dtype
+    ydt = xdt if y_dtype is None else _y_type(y_dtype, xdt, _norm_types() if xdt == torch.float32 else (xdt,))
+    groups, pdt, pw, pb = 1, torch.float32, None, None
+    if weight is not None:
+        pw, groups = _norm_param(weight, "weight", dev, ydt, C)
+        pdt = weight.dtype
+    if bias is not None:
+        pb, groups = _norm_param(bias, "bias", dev, ydt, C)
+        pdt = bias.dtype
+        if weight is not None and (weight.shape != bias.shape or weight.dtype != pdt):
+            raise ValueError("weight and bias differ in shape or type")
     if out is None:
         out = torch.empty((M, C), dtype=ydt, device=X.device)
+        po = out.data_ptr()
     else:
-        _dev_tensor(out, "out", (ydt,), (M, C))
+        po = _arg(out, "out", dev, (ydt,), (M, C))
     mean = rstd = None
     if return_stats:
         mean = torch.empty((M,), dtype=torch.float32, device=X.device)
         rstd = torch.empty((M,), dtype=torch.float32, device=X.device)
-    _on_current_device(X, weight, bias, out)
-    _check(lib.hsq_layer_norm(_ptr(X), dts[X.dtype], M, C, groups, _ptr(weight), _ptr(bias), dts[pdt],
-                              eps, _ptr(out), dts[ydt], _ptr(mean), _ptr(rstd), _stream()), "hsq_layer_norm")
+    _check(lib.hsq_layer_norm(px, dts[xdt], M, C, groups, pw, pb, dts[pdt], eps, po, dts[ydt], _ptr(mean), _ptr(rstd),
+                              _raw_stream(dev)), "hsq_layer_norm")
     return (out, mean, rstd) if return_stats else out
 
 
@@ -733,27 +772,27 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, *, groups: int = 1, need
     torch = _torch()
     lib = _load()
     dts = _dtypes()
-    _dev_tensor(X, "X", (torch.float32, torch.bfloat16, torch.float16))
+    dev = _device(X, "X")
+    px = _arg(X, "X", dev, _norm_types())
     M, C = X.shape
-    _dev_tensor(dY, "dY", (X.dtype,) if X.dtype != torch.float32 else
-                (torch.float32, torch.bfloat16, torch.float16), (M, C))
-    _dev_tensor(mean, "mean", (torch.float32,), (M,))
-    _dev_tensor(rstd, "rstd", (torch.float32,), (M,))
-    shape, pdt = (groups, C), torch.float32
+    xdt = X.dtype
+    py = _arg(dY, "dY", dev, _norm_types() if xdt == torch.float32 else (xdt,), (M, C))
+    f32 = (torch.float32,)
+    pm, pr = _arg(mean, "mean", dev, f32, (M,)), _arg(rstd, "rstd", dev, f32, (M,))
+    shape, pdt, pw = (groups, C), torch.float32, None
     if weight is not None:
-        if groups not in (1, wg := _norm_param(weight, "weight", dY.dtype, C)):
+        pw, wg = _norm_param(weight, "weight", dev, dY.dtype, C)
+        if groups not in (1, wg):
             raise ValueError(f"groups {groups} does not go with weight {tuple(weight.shape)}")
         groups, shape, pdt = wg, weight.shape, weight.dtype
-    dX = torch.empty((M, C), dtype=X.dtype, device=X.device) if need_input else None
-    dw = db = None
+    dX = torch.empty((M, C), dtype=xdt, device=X.device) if need_input else None
+    dw = db = ps = None
+    nbytes = 0
     if need_params:
         dw = torch.empty(shape, dtype=pdt, device=X.device)
         db = torch.empty(shape, dtype=pdt, device=X.device)
-        workspace = _scratch(workspace, 0 if workspace is not None else
-                             int(lib.hsq_layer_norm_backward_workspace_bytes(M, C, groups)), X.device)
-    _on_current_device(dY, X, mean, rstd, weight, workspace)
-    _check(lib.hsq_layer_norm_backward(_ptr(dY), dts[dY.dtype], _ptr(X), dts[X.dtype], M, C, groups, _ptr(mean),
-                                       _ptr(rstd), _ptr(weight), dts[pdt], _ptr(dX), _ptr(dw), _ptr(db),
-                                       _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                       _stream()), "hsq_layer_norm_backward")
+        workspace, ps, nbytes = _scratch(
+            workspace, lambda: lib.hsq_layer_norm_backward_workspace_bytes(M, C, groups), X, dev)
+    _check(lib.hsq_layer_norm_backward(py, dts[dY.dtype], px, dts[xdt], M, C, groups, pm, pr, pw, dts[pdt], _ptr(dX),
+                                       _ptr(dw), _ptr(db), ps, nbytes, _raw_stream(dev)), "hsq_layer_norm_backward")
     return dX, dw, db

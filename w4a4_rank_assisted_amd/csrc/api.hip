@@ -858,12 +858,12 @@ int hsq_linear_backward(const void *dY, int y_dtype, const uint16_t *X, int M, i
     d.dY = dY; d.dy_f32 = y_dtype == HSQ_F32;
     d.Z = act == HSQ_ACT_IDENTITY ? nullptr : Z;
     d.dZ = same || (!dX && !dW) ? nullptr : (uint16_t *)(ws + L.dz_off);
-    d.db = dbias;
-    d.part = (float *)(ws + L.db_off);
+    d.part = dbias ? (float *)(ws + L.db_off) : nullptr;
     d.M = M; d.N = N; d.np = L.np; d.act = act; d.dtype = dtype; d.slices = L.slices;
   }
   hipError_t e = launch_linear_prep(p, dtype, s);
-  if (e == hipSuccess && (dX || dW)) e = launch_linear_backward(x, w, s);
+  const SumArgs db{p.dz.part, (size_t)N, L.slices, N, dbias, nullptr, dtype};
+  if (e == hipSuccess) e = launch_linear_backward(x, w, db, dtype, s);
   return debug_check(hip_status(e), stream);
 }
 

@@ -297,6 +297,18 @@ hipError_t launch_l2(const L2Args &a, hipStream_t s);
 constexpr int kF32 = 0, kBf16 = 1, kF16 = 2;
 constexpr int kActGelu = 2, kActSilu = 3;   // after kActIdentity, kActGeluTanh
 
+// Sums of fp32 partial rows of stride ld, `parts` of them per group, columns 0
+// .. C - 1 into dst and columns C .. 2 C - 1 into dst2 (either null: not
+// wanted), groups x C of dtype.
+struct SumArgs {
+  const float *src;
+  size_t ld;
+  int parts, C;
+  void *dst, *dst2;
+  int dtype;
+};
+hipError_t launch_sum_parts(const SumArgs &a, int groups, hipStream_t s);
+
 // One product out(i, j) = sum_r A(i, r) B(r, j) with its epilogue.  An
 // operand is stored either with r contiguous (A: I x lda, B: J x ldb) or
 // with r as its rows (A: R x lda, B: R x ldb); strides are multiples of 8
@@ -336,22 +348,22 @@ LinPlan plan_linear_backward(int M, int K, int N);
 // Forward: A = X with r contiguous, B = W with r as rows.
 hipError_t launch_linear(const LinGemm &a, bool skinny, hipStream_t s);
 // Backward, each with out == nullptr where not wanted: dX = dZ W^T (both
-// operands r-contiguous) and dW = X^T dZ (both with r as rows).
-hipError_t launch_linear_backward(const LinGemm &dx, const LinGemm &dw, hipStream_t s);
+// operands r-contiguous) and dW = X^T dZ (both with r as rows), and the bias
+// gradient from the partial rows of the preparing launch (at least one).
+hipError_t launch_linear_backward(const LinGemm &dx, const LinGemm &dw, const SumArgs &db, int dtype, hipStream_t s);
 
 struct LinDz {
   const void *dY;          // M x N, fp32 or dtype
   int dy_f32;
   const uint16_t *Z;       // M x N dtype (null for the identity)
   uint16_t *dZ;            // M x np dtype, zeros past N (null: only the column sums)
-  void *db;                // N dtype (null: not wanted)
-  float *part;             // slices x N fp32
+  float *part;             // slices x N fp32 partial rows of the bias gradient (null: not wanted)
   int M, N, np, act, dtype, slices;
 };
 
 // What the products read that is not there yet: X and W with rows of a
-// multiple of 8 (src null: not needed), dZ and the bias gradient (dY null: not
-// needed).
+// multiple of 8 (src null: not needed), dZ and the partial rows of the bias
+// gradient (dY null: not needed).
 struct LinPrep {
   const uint16_t *X, *W;
   uint16_t *Xp, *Wp;
@@ -360,18 +372,6 @@ struct LinPrep {
   int x_blocks, w_blocks;  // set by the launch
 };
 hipError_t launch_linear_prep(LinPrep p, int dtype, hipStream_t s);
-
-// Sums of fp32 partial rows of stride ld, `parts` of them per group, columns 0
-// .. C - 1 into dst and columns C .. 2 C - 1 into dst2 (either null: not
-// wanted), groups x C of dtype.
-struct SumArgs {
-  const float *src;
-  size_t ld;
-  int parts, C;
-  void *dst, *dst2;
-  int dtype;
-};
-hipError_t launch_sum_parts(const SumArgs &a, int groups, hipStream_t s);
 
 constexpr int kNormMaxC = 16384;   // a row is held in the registers of one workgroup
 

@@ -477,15 +477,45 @@ __global__ __launch_bounds__(512, 2) void k_lin_fwd(LinGemm a) {
   if (u < a.full) lin_full<DT, false, true>(a, lds, u);
   else lin_part<DT, false, true>(a, lds, u - a.full);
 }
+// The last workgroups sum the bias gradient's partial rows (of the launch
+// before): 32 columns each, 16 shares of the rows, added in order.
+constexpr int kDbCols = 32, kDbShares = 16;
 template <int DT>
-__global__ __launch_bounds__(512, 2) void k_lin_bwd(LinGemm x, LinGemm w) {
+__device__ __forceinline__ void lin_db(const SumArgs &a, char *lds, int block) {
+  float *sh = reinterpret_cast<float *>(lds);
+  const int cx = threadIdx.x % kDbCols, y = threadIdx.x / kDbCols, c = block * kDbCols + cx;
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c < a.C) {
+    const float *src = a.src + c;
+    int p = y;
+    for (; p + 3 * kDbShares < a.parts; p += 4 * kDbShares) {
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = src[(size_t)(p + k * kDbShares) * a.ld];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += v[k];
+    }
+    for (; p < a.parts; p += kDbShares) s[0] += src[(size_t)p * a.ld];
+  }
+  sh[y * (kDbCols + 1) + cx] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (y != 0 || c >= a.C) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kDbShares; ++k) v += sh[k * (kDbCols + 1) + cx];
+  static_cast<uint16_t *>(a.dst)[c] = (uint16_t)f32_to_half<DT>(v);
+}
+
+template <int DT>
+__global__ __launch_bounds__(512, 2) void k_lin_bwd(LinGemm x, LinGemm w, SumArgs db, int db0) {
   __shared__ __attribute__((aligned(16))) char lds[kLinLds];
   const int u = blockIdx.x;
   auto in = [&](int first, int count) { return u >= first && u < first + count; };
   if (in(x.full0, x.full)) lin_full<DT, false, false>(x, lds, u - x.full0);
   else if (in(w.full0, w.full)) lin_full<DT, true, true>(w, lds, u - w.full0);
   else if (in(x.parts0, x.parts)) lin_part<DT, false, false>(x, lds, u - x.parts0);
-  else lin_part<DT, true, true>(w, lds, u - w.parts0);
+  else if (in(w.parts0, w.parts)) lin_part<DT, true, true>(w, lds, u - w.parts0);
+  else lin_db<DT>(db, lds, u - db0);
 }
 
 // Sums the splits' partial sums in split order and finishes eight columns per thread.
@@ -746,7 +776,7 @@ __device__ __forceinline__ void lin_dz(const LinDz &a, int bx, int by) {
       work(m, d, z);
     }
   }
-  if (!a.db) return;
+  if (!a.part) return;
 #pragma unroll
   for (int e = 0; e < 8; ++e) red[ry][8 * cx + e] = s[e];
   __syncthreads();
@@ -888,12 +918,13 @@ hipError_t run_forward(LinGemm a, bool skinny, hipStream_t s) {
 }
 
 template <int DT>
-hipError_t run_backward(const LinGemm &x, const LinGemm &w, hipStream_t s) {
+hipError_t run_backward(const LinGemm &x, const LinGemm &w, const SumArgs &db, hipStream_t s) {
   LinGemm job[2] = {x, w};
   const bool has_x = x.out != nullptr, has_w = w.out != nullptr;
   plan_units(job[0], job[1]);
-  hipLaunchKernelGGL(k_lin_bwd<DT>, dim3((unsigned)(job[0].full + job[0].parts + job[1].full + job[1].parts)), dim3(512),
-                     0, s, job[0], job[1]);
+  const int units = job[0].full + job[0].parts + job[1].full + job[1].parts;
+  hipLaunchKernelGGL(k_lin_bwd<DT>, dim3((unsigned)(units + (db.dst ? ceil_div(db.C, kDbCols) : 0))), dim3(512), 0, s,
+                     job[0], job[1], db, units);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess ? e : run_reduce<DT>(has_x ? job[0] : LinGemm{}, has_w ? job[1] : LinGemm{}, s);
 }
@@ -951,9 +982,8 @@ hipError_t launch_linear(const LinGemm &a, bool skinny, hipStream_t s) {
   return a.dtype == kBf16 ? run_forward<kBf16>(a, skinny, s) : run_forward<kF16>(a, skinny, s);
 }
 
-hipError_t launch_linear_backward(const LinGemm &x, const LinGemm &w, hipStream_t s) {
-  const int dtype = x.out ? x.dtype : w.dtype;
-  return dtype == kBf16 ? run_backward<kBf16>(x, w, s) : run_backward<kF16>(x, w, s);
+hipError_t launch_linear_backward(const LinGemm &x, const LinGemm &w, const SumArgs &db, int dtype, hipStream_t s) {
+  return dtype == kBf16 ? run_backward<kBf16>(x, w, db, s) : run_backward<kF16>(x, w, db, s);
 }
 
 hipError_t launch_linear_prep(LinPrep p, int dtype, hipStream_t s) {
@@ -967,9 +997,7 @@ hipError_t launch_linear_prep(LinPrep p, int dtype, hipStream_t s) {
   if (n == 0) return hipSuccess;
   if (dtype == kBf16) hipLaunchKernelGGL(k_lin_prep<kBf16>, dim3((unsigned)n), dim3(256), 0, s, p);
   else hipLaunchKernelGGL(k_lin_prep<kF16>, dim3((unsigned)n), dim3(256), 0, s, p);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !dz || !p.dz.db) return e;
-  return launch_sum_parts(SumArgs{p.dz.part, (size_t)p.dz.N, p.dz.slices, p.dz.N, p.dz.db, nullptr, dtype}, 1, s);
+  return hipGetLastError();
 }
 
 }  // namespace hsq
