@@ -475,7 +475,7 @@ __global__ __launch_bounds__(512, 2) void k_lin_fwd(LinGemm a) {
   __shared__ __attribute__((aligned(16))) char lds[kLinLds];
   const int u = blockIdx.x;
   if (u < a.full) lin_full<DT, false, true>(a, lds, u);
-  else lin_part<DT, false, true>(a, lds, u - a.full);
+  else lin_part<DT, false, true>(a, lds, u - a.parts0);
 }
 // The last workgroups sum the bias gradient's partial rows (of the launch
 // before): 32 columns each, 16 shares of the rows, added in order.
@@ -807,11 +807,22 @@ constexpr int kCus = 256;
 
 int quarters(int I, int J) { return ceil_div(I, 128) * ceil_div(J, 128); }
 
-// Splits of the reduction: towards 128 workgroups of 128 x 128 tiles, at least
-// 256 of the reduction each.  64 x 12288 x 4096 (32 tiles): 4 splits 39 us, 8
-// 44, 2 64, none 112; 64 x 4096 x 12288 (96 tiles): none 44 us, 2 49.
+// Splits of the reduction, each of at least 256, for fewer 128 x 128 tiles
+// than CUs: towards 128 workgroups, or 256 where few rows stream a long
+// operand (64 x 12288 x 4096, 32 tiles: 4 splits 39 us, 8 44, 2 64, none 112).
+// Of these the cheapest: a stage of 32 takes 0.3 us, the second launch 3 us,
+// and the partial sums go out and back at 2.5 TB/s (1000 x 1024 x 1024: none
+// 13.6 us, 2 19.8; 256 x 8192 x 256: none 65 us, 16 16.7).
 int gemm_splits(int I, int J, int R) {
-  return std::max(1, std::min({kCus / 2 / quarters(I, J), R / 256, 16}));
+  const int tiles = quarters(I, J), cap = std::min(kCus / tiles, std::max(kCus / 2 / tiles, R / 64 / I));
+  const int most = std::min({cap, R / 256, 16});
+  int best = 1;
+  float least = 0.0f;
+  for (int s = 1; s <= most; ++s) {
+    const float us = 0.3f / 32 * R / s + (s > 1 ? 3.0f + 3.2e-6f * s * I * J : 0.0f);
+    if (s == 1 || us < least) least = us, best = s;
+  }
+  return best;
 }
 
 // How the last `rem` of the tiles, after whole rounds of one 256 x 256 tile
@@ -844,7 +855,13 @@ void plan_units(LinGemm &a, LinGemm &b) {
   }
   LinGemm *last = order[1]->nbi * order[1]->nbj > 0 && order[1]->splits <= 1 ? order[1] : order[0];
   const int rem = last->R > 0 ? (int)(work / last->R) % kCus : 0, cut = best_cut(rem);
+  // split tiles have the longest way to go for their size: they start first
   int base = 0;
+  for (LinGemm *j : order)
+    if (j->splits > 1) {
+      j->parts0 = base;
+      base += 4 * j->nbi * j->nbj * j->splits;
+    }
   for (LinGemm *j : order) {
     const int t = j->nbi * j->nbj;
     j->cut = cut;
@@ -859,10 +876,11 @@ void plan_units(LinGemm &a, LinGemm &b) {
     j->full0 = base;
     base += j->full;
   }
-  for (LinGemm *j : order) {
-    j->parts0 = base;
-    base += j->parts;
-  }
+  for (LinGemm *j : order)
+    if (j->splits <= 1) {
+      j->parts0 = base;
+      base += j->parts;
+    }
 }
 
 // Splits of K of the weight-streaming kernel: the fewest whose workgroups
