@@ -83,7 +83,15 @@ FORWARD = [
     (2048, 1152, 4608, BF, "gelu_tanh", True, False, True),
     (4096, 8, 8200, F16, "identity", True, True, True),
     (1000, 1, 999, BF, "gelu", True, True, True),
-]
+    # few rows at the ends of X and W: loads there move back by up to seven elements
+    (5, 3867, 119, BF, "gelu", False, False, False),
+    (48, 33, 9, F16, "silu", True, True, True),
+    (2, 4, 2, BF, "identity", True, False, True),
+    (1, 8, 1, BF, "identity", False, False, True),
+    (1, 7, 1, BF, "identity", False, False, True),
+    (7, 1, 7, F16, "gelu_tanh", True, False, True),
+    (49, 300, 131, BF, "identity", True, False, True),
+] + [(3, 31 + i, 121 + i, BF, "identity", False, False, True) for i in range(8)]
 
 
 @pytest.mark.parametrize("M,K,N,dt,act,bias,res,y32", FORWARD)

@@ -566,6 +566,24 @@ __global__ __launch_bounds__(256) void k_lin_reduce(LinGemm first, LinGemm secon
 // l % 16 and 32 consecutive columns.
 constexpr int kSkCols = 128, kSkWaves = 4;
 
+// Eight elements from i on of an array of `end` >= 8; those past the end are
+// anything.
+__device__ __forceinline__ v4u load_within(const uint16_t *p, long long i, long long end) {
+  const long long at = i < end - 8 ? i : end - 8;
+  const int d = (int)(i - at), s = d >> 1;
+  const v4u t = *reinterpret_cast<const U16 *>(p + at);
+  v4u u;   // t shifted down by s dwords, then by the odd element
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    u[h] = t[h];
+#pragma unroll
+    for (int k = 1; h + k < 4; ++k) u[h] = s == k ? t[h + k] : u[h];
+  }
+#pragma unroll
+  for (int h = 0; h < 4; ++h) u[h] = __builtin_amdgcn_alignbit(h < 3 ? u[h + 1] : 0u, u[h], (uint32_t)(d & 1) * 16u);
+  return u;
+}
+
 template <int DT, int MT, bool PART>
 __global__ __launch_bounds__(64 * kSkWaves, 5 - MT) void k_lin_skinny(LinGemm a) {
   __shared__ float red[kSkWaves][16][kSkCols + 4];
@@ -581,46 +599,39 @@ __global__ __launch_bounds__(64 * kSkWaves, 5 - MT) void k_lin_skinny(LinGemm a)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[m][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 
-  // whole runs of whole strips load without a test
-  const bool strip = j0 + kSkCols <= a.J;
-  auto load = [&](int run, U16 (&w)[8]) __attribute__((always_inline)) {
+  // Columns past J only reach outputs that are not stored, so a run may read
+  // on into the next row wherever that stays inside W; at the end of W the
+  // loads are moved back and shifted, and the rows past K are zeros.
+  const long long w_end = (long long)a.R * a.ldb, x_end = (long long)a.I * a.lda;
+  auto load = [&](int run, v4u (&w)[8]) __attribute__((always_inline)) {
     const int k = 32 * run + 8 * g;
-    const uint16_t *p = a.B + (size_t)k * a.ldb + jc;
-    if (strip && 32 * run + 32 <= a.R) {
+    if ((long long)(32 * run + 31) * a.ldb + j0 + kSkCols <= w_end) {
+      const uint16_t *p = a.B + (size_t)k * a.ldb + jc;
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const U16 *>(p + (size_t)e * a.ldb);
       return;
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      w[e] = (U16){0u, 0u, 0u, 0u};
-      if (k + e < a.R) {
-        if (jc + 8 <= a.J) {
-          w[e] = *reinterpret_cast<const U16 *>(p + (size_t)e * a.ldb);
-        } else {
+      const v4u t = load_within(a.B, (long long)min(k + e, a.R - 1) * a.ldb + jc, w_end);
 #pragma unroll
-          for (int h = 0; h < 8; ++h)
-            if (jc + h < a.J) w[e][h / 2] |= (uint32_t)p[(size_t)e * a.ldb + h] << (16 * (h & 1));
-        }
-      }
+      for (int h = 0; h < 4; ++h) w[e][h] = k + e < a.R ? t[h] : 0u;
     }
   };
-  auto step = [&](int run, const U16 (&w)[8]) __attribute__((always_inline)) {
+  auto step = [&](int run, const v4u (&w)[8]) __attribute__((always_inline)) {
     const int k = 32 * run + 8 * g;
     v4u x[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      x[m] = (v4u){0u, 0u, 0u, 0u};
       const int row = 16 * m + c;
-      if (row < a.I) {
-        const uint16_t *p = a.A + (size_t)row * a.lda + k;
-        if (k + 8 <= a.R) {
-          x[m] = *reinterpret_cast<const U16 *>(p);
-        } else {
+      if (32 * run + 32 <= a.R) {
+        x[m] = (v4u){0u, 0u, 0u, 0u};
+        if (row < a.I) x[m] = *reinterpret_cast<const U16 *>(a.A + (size_t)row * a.lda + k);
+      } else {
+        const v4u t = load_within(a.A, (long long)min(row, a.I - 1) * a.lda + min(k, a.R - 1), x_end);
+        const int n = row < a.I ? a.R - k : 0;      // elements of this row
 #pragma unroll
-          for (int h = 0; h < 8; ++h)
-            if (k + h < a.R) x[m][h / 2] |= (uint32_t)p[h] << (16 * (h & 1));
-        }
+        for (int h = 0; h < 4; ++h) x[m][h] = n >= 2 * h + 2 ? t[h] : n == 2 * h + 1 ? t[h] & 0xFFFFu : 0u;
       }
     }
 #pragma unroll
@@ -635,7 +646,7 @@ __global__ __launch_bounds__(64 * kSkWaves, 5 - MT) void k_lin_skinny(LinGemm a)
   };
   // one run in flight per wave: sixteen waves per CU keep 128 KB on the way
   for (int run = r0 + wave; run < r1; run += kSkWaves) {
-    U16 w[8];
+    v4u w[8];
     load(run, w);
     step(run, w);
   }
@@ -953,7 +964,8 @@ LinPlan plan_linear(int M, int K, int N) {
   LinPlan p;
   p.kp = ceil_div(K, 8) * 8;
   p.np = ceil_div(N, 8) * 8;
-  p.skinny = M <= kLinSkinnyMaxM;
+  // (its loads at the end of X and W are moved back inside them: 8 elements at least)
+  p.skinny = M <= kLinSkinnyMaxM && (long long)M * K >= 8 && (long long)K * N >= 8;
   p.splits = p.skinny ? skinny_splits(N, K) : gemm_splits(M, N, K);
   p.pad_x = !p.skinny && p.kp != K;
   p.pad_w = !p.skinny && p.np != N;
