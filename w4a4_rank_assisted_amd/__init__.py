@@ -702,8 +702,8 @@ def linear_backward(dY, X, W, preact=None, *, act: str = "identity", need_input:
         raise ValueError(f"act {act!r} not in {sorted(_LINEAR_ACTS)}")
     py = _arg(dY, "dY", dev, (dt, torch.float32), (M, N))
     pz = None if act == "identity" else _arg(preact, "preact", dev, (dt,), (M, N))
-    dX = torch.empty((M, K), dtype=dt, device=X.device) if need_input else None
-    dW = torch.empty((K, N), dtype=dt, device=X.device) if need_weight else None
+    dX = torch.empty_like(X) if need_input else None
+    dW = torch.empty_like(W) if need_weight else None
     db = torch.empty((N,), dtype=dt, device=X.device) if need_bias else None
     workspace, ps, nbytes = _scratch(workspace, lambda: lib.hsq_linear_backward_workspace_bytes(M, K, N), X, dev)
     _check(lib.hsq_linear_backward(py, dts[dY.dtype], px, M, K, N, dts[dt], pw, pz, _LINEAR_ACTS[act], _ptr(dX),
@@ -746,14 +746,14 @@ def layer_norm(X, weight=None, bias=None, *, eps: float = 1e-5, y_dtype=None, ou
         if weight is not None and (weight.shape != bias.shape or weight.dtype != pdt):
             raise ValueError("weight and bias differ in shape or type")
     if out is None:
-        out = torch.empty((M, C), dtype=ydt, device=X.device)
+        out = torch.empty_like(X) if ydt == xdt else torch.empty((M, C), dtype=ydt, device=X.device)
         po = out.data_ptr()
     else:
         po = _arg(out, "out", dev, (ydt,), (M, C))
     mean = rstd = None
     if return_stats:
         mean = torch.empty((M,), dtype=torch.float32, device=X.device)
-        rstd = torch.empty((M,), dtype=torch.float32, device=X.device)
+        rstd = torch.empty_like(mean)
     _check(lib.hsq_layer_norm(px, dts[xdt], M, C, groups, pw, pb, dts[pdt], eps, po, dts[ydt], _ptr(mean), _ptr(rstd),
                               _raw_stream(dev)), "hsq_layer_norm")
     return (out, mean, rstd) if return_stats else out
@@ -779,18 +779,18 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, *, groups: int = 1, need
     py = _arg(dY, "dY", dev, _norm_types() if xdt == torch.float32 else (xdt,), (M, C))
     f32 = (torch.float32,)
     pm, pr = _arg(mean, "mean", dev, f32, (M,)), _arg(rstd, "rstd", dev, f32, (M,))
-    shape, pdt, pw = (groups, C), torch.float32, None
+    pdt, pw = torch.float32, None
     if weight is not None:
         pw, wg = _norm_param(weight, "weight", dev, dY.dtype, C)
         if groups not in (1, wg):
             raise ValueError(f"groups {groups} does not go with weight {tuple(weight.shape)}")
-        groups, shape, pdt = wg, weight.shape, weight.dtype
-    dX = torch.empty((M, C), dtype=xdt, device=X.device) if need_input else None
+        groups, pdt = wg, weight.dtype
+    dX = torch.empty_like(X) if need_input else None
     dw = db = ps = None
     nbytes = 0
     if need_params:
-        dw = torch.empty(shape, dtype=pdt, device=X.device)
-        db = torch.empty(shape, dtype=pdt, device=X.device)
+        dw = torch.empty((groups, C), dtype=pdt, device=X.device) if weight is None else torch.empty_like(weight)
+        db = torch.empty_like(dw)
         workspace, ps, nbytes = _scratch(
             workspace, lambda: lib.hsq_layer_norm_backward_workspace_bytes(M, C, groups), X, dev)
     _check(lib.hsq_layer_norm_backward(py, dts[dY.dtype], px, dts[xdt], M, C, groups, pm, pr, pw, dts[pdt], _ptr(dX),
