@@ -91,6 +91,11 @@ FORWARD = [
     (1, 7, 1, BF, "identity", False, False, True),
     (7, 1, 7, F16, "gelu_tanh", True, False, True),
     (49, 300, 131, BF, "identity", True, False, True),
+    # ragged rows read as they are (short reductions, few tiles) and from padded copies
+    (130, 8, 3, BF, "identity", True, False, True),
+    (1000, 4001, 201, BF, "silu", True, True, False),
+    (900, 2500, 1201, F16, "identity", False, False, True),
+] + [(150 + i, 95 + i, 241 + 3 * i, BF, "identity", False, False, True) for i in range(8)
 ] + [(3, 31 + i, 121 + i, BF, "identity", False, False, True) for i in range(8)]
 
 
@@ -132,6 +137,10 @@ BACKWARD = [
     (1000, 999, 31, BF, "gelu", True, False),
     (40, 2049, 4104, BF, "identity", True, False),           # many tiles of dW, a short reduction
     (2049, 4100, 72, F16, "silu", True, False),              # many tiles of dX
+    (1500, 1023, 1401, BF, "identity", True, False),         # ragged rows read as they are
+    (700, 1503, 5001, F16, "gelu", False, False),            # W padded for dX, X too
+    (2, 2240, 4001, BF, "gelu_tanh", True, False),           # few rows against a long, split reduction
+    (9, 1, 9, BF, "identity", True, False),
     (4096, 256, 300, BF, "gelu_tanh", True, False),          # a long reduction into few tiles of dW
 ]
 

@@ -34,8 +34,8 @@ def _linear(**kw):
     (dict(K=1 << 15, N=1 << 15, M=1), hsq.E_INVAL),        # K * N = 2^30
     (dict(M=1 << 27, K=1, N=1), hsq.E_INVAL),              # rows of 1 rounded up to 8: 2^30
     (dict(M=1, K=1, N=(1 << 24) + 1), hsq.E_INVAL), (dict(M=1, K=(1 << 24) + 1, N=1), hsq.E_INVAL),
-    (dict(M=333, K=1001, N=777, wsb=0), hsq.E_WORKSPACE),  # ragged rows are staged
-    (dict(M=333, K=1001, N=777, ws=None, wsb=1 << 30), hsq.E_WORKSPACE),
+    (dict(M=4333, K=1001, N=4777, wsb=0), hsq.E_WORKSPACE),  # many ragged rows are staged
+    (dict(M=4333, K=1001, N=4777, ws=None, wsb=1 << 30), hsq.E_WORKSPACE),
 ])
 def test_linear_refusals(kw, code):
     assert _linear(**kw) == code
@@ -110,8 +110,8 @@ def test_workspace_sizes():
                lib.hsq_layer_norm_backward_workspace_bytes)
     assert f(0, 64, 64) == 0 and b(64, 0, 64) == 0 and n(0, 64, 1) == 0 and n(6, 64, 4) == 0
     assert f(4096, 1152, 4608) == 0                       # whole rows, enough tiles: nothing to stage
-    assert f(333, 1001, 777) >= 2 * (333 * 1008 + 1001 * 784)
-    assert b(333, 1001, 777) >= 2 * (333 * 1008 + 1001 * 784 + 333 * 784)
+    assert f(4333, 1001, 4777) >= 2 * (4333 * 1008 + 1001 * 4784)
+    assert b(4333, 4001, 4777) >= 2 * (4333 * 4008 + 4001 * 4784 + 4333 * 4784)
     assert n(8192, 1152, 2) % (2 * 2 * 1152 * 4) == 0 and n(8192, 1152, 2) > 0
     for M, K, N in [(1, 1, 1), (1, 4096, 12288), (64, 12288, 4096), (65, 7, 9), (8192, 12288, 4096)]:
         assert f(M, K, N) < 1 << 31 and 0 < b(M, K, N) < 1 << 33

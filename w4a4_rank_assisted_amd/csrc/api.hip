@@ -785,6 +785,7 @@ int hsq_linear(const uint16_t *X, int M, int K, int N, int dtype, const uint16_t
   a.bias = bias; a.res = residual; a.out = Y; a.out_f32 = y_dtype == HSQ_F32; a.Z = Z; a.act = act;
   a.part = (float *)(ws + L.part_off);
   a.splits = L.splits;
+  a.ragged = L.ragged_x;
   LinPrep p{};
   if (L.pad_x) {
     p.X = X; p.x_rows = M; p.x_cols = K; p.x_ld = L.kp;
@@ -830,7 +831,7 @@ int hsq_linear_backward(const void *dY, int y_dtype, const uint16_t *X, int M, i
   if (dX) {
     x.dtype = dtype;
     x.A = dz; x.lda = L.np;
-    x.B = W; x.ldb = N;
+    x.B = W; x.ldb = N; x.ragged = L.ragged_w;
     if (L.pad_w) {
       p.W = W; p.w_rows = K; p.w_cols = N; p.w_ld = L.np;
       p.Wp = (uint16_t *)(ws + L.w_off);
@@ -842,7 +843,7 @@ int hsq_linear_backward(const void *dY, int y_dtype, const uint16_t *X, int M, i
   }
   if (dW) {
     w.dtype = dtype;
-    w.A = X; w.lda = K;
+    w.A = X; w.lda = K; w.ragged = L.ragged_x;
     if (L.pad_x) {
       p.X = X; p.x_rows = M; p.x_cols = K; p.x_ld = L.kp;
       p.Xp = (uint16_t *)(ws + L.x_off);

@@ -311,8 +311,9 @@ hipError_t launch_sum_parts(const SumArgs &a, int groups, hipStream_t s);
 
 // One product out(i, j) = sum_r A(i, r) B(r, j) with its epilogue.  An
 // operand is stored either with r contiguous (A: I x lda, B: J x ldb) or
-// with r as its rows (A: R x lda, B: R x ldb); strides are multiples of 8
-// elements and the elements past R of an r-contiguous row are zero.
+// with r as its rows (A: R x lda, B: R x ldb); unless `ragged`, strides are
+// multiples of 8 elements and the elements past R of an r-contiguous row are
+// zero.
 struct LinGemm {
   const uint16_t *A, *B;
   int I, J, R, lda, ldb;
@@ -326,6 +327,7 @@ struct LinGemm {
   int act;
   float *part;             // split partial sums (workspace)
   int splits;
+  int ragged;              // 1: row lengths of any kind; A and B hold 8 elements at least
   // units of the launch (set there): nbi x nbj tiles of 256 x 256, of which
   // `full` whole (workgroups full0 ..), the others in `cut` parts, `parts` units
   // in all (workgroups parts0 ..)
@@ -337,7 +339,8 @@ struct LinPlan {
   int splits = 1;          // splits of the reduction (forward)
   int splits_dx = 1, splits_dw = 1, slices = 1;   // backward: splits, row slices of the bias gradient
   int kp = 0, np = 0;      // K and N rounded up to 8
-  bool pad_x = false, pad_w = false;
+  bool pad_x = false, pad_w = false;        // X, W copied to rows of kp, np
+  bool ragged_x = false, ragged_w = false;  // X, W read as they are (backward: by dW, dX; forward: both)
   size_t x_off = 0, w_off = 0, dz_off = 0, part_off = 0, part_w_off = 0, db_off = 0, total = 0;
 };
 

@@ -259,14 +259,71 @@ struct Stager {
   }
 };
 
+// Eight elements from i on of an array of `end` >= 8; those past the end are
+// anything.
+__device__ __forceinline__ v4u load_within(const uint16_t *p, long long i, long long end) {
+  const long long at = i < end - 8 ? i : end - 8;
+  const int d = (int)(i - at), s = d >> 1;
+  const v4u t = *reinterpret_cast<const U16 *>(p + at);
+  v4u u;   // t shifted down by s dwords, then by the odd element
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    u[h] = t[h];
+#pragma unroll
+    for (int k = 1; h + k < 4; ++k) u[h] = s == k ? t[h + k] : u[h];
+  }
+#pragma unroll
+  for (int h = 0; h < 4; ++h) u[h] = __builtin_amdgcn_alignbit(h < 3 ? u[h + 1] : 0u, u[h], (uint32_t)(d & 1) * 16u);
+  return u;
+}
+
+// The same staging through registers, for rows of any length: this thread's one
+// 16-byte chunk of a stage, loaded at any element, zero past R.  Chunks of
+// rows or columns past the matrix hold anything that lies inside it.
+template <int T, bool STRIDED, bool ISB>
+struct RaggedStager {
+  const uint16_t *p;
+  long long base, end;
+  int ld, R, x0, off;
+  static constexpr int CPR = STRIDED ? T / 8 : BK / 8;
+  static_assert(T * BK / 8 == 512, "one chunk per thread");
+
+  __device__ __forceinline__ void init(const uint16_t *p_, int n, int x0_, int R_, int ld_, int w, int l) {
+    p = p_; ld = ld_; R = R_; x0 = x0_;
+    end = (long long)(STRIDED ? R : n) * ld;
+    const int row = w * (64 / CPR) + l / CPR;
+    if constexpr (STRIDED) {
+      off = row;
+      base = (long long)row * ld + x0 + 8 * (l % CPR ^ swz_strided<ISB>(row));
+    } else {
+      off = 8 * (l % CPR ^ swz_cont<ISB>(row));
+      base = (long long)min(x0 + row, n - 1) * ld + off;
+    }
+  }
+  __device__ __forceinline__ v4u load(int r0) const {
+    const long long i = base + (STRIDED ? (long long)r0 * ld : r0);
+    const bool inside = r0 + BK <= R && (!STRIDED || (long long)(r0 + BK - 1) * ld + x0 + T <= end);
+    if (inside) return *reinterpret_cast<const U16 *>(p + i);
+    const int n = R - r0 - off;            // elements (rows) left from here
+    v4u t = load_within(p, n > 0 ? i : 0, end);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      if constexpr (STRIDED) t[h] = n > 0 ? t[h] : 0u;
+      else t[h] = n >= 2 * h + 2 ? t[h] : n == 2 * h + 1 ? t[h] & 0xFFFFu : 0u;
+    }
+    return t;
+  }
+};
+
 template <int N>
 __device__ __forceinline__ void stage_wait() {   // all but this wave's N newest loads, its LDS reads, the workgroup
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // One tile of a job: rows i0 .. + TI, columns j0 .. + TJ, split z of the
-// reduction (PART: the sum goes to the split's partial matrix).
-template <class C, int DT, bool ASTR, bool BSTR, bool PART>
+// reduction (PART: the sum goes to the split's partial matrix).  RAGGED: rows
+// of any length, staged through registers.
+template <class C, int DT, bool ASTR, bool BSTR, bool PART, bool RAGGED = false>
 __device__ __forceinline__ void lin_tile(const LinGemm &a, char *lds, int i0, int j0, int z) {
   struct alignas(16) Stage { char a[C::kA]; char b[C::kB]; };
   static_assert(sizeof(Stage) * C::NS <= kLinLds, "stage buffers");
@@ -276,11 +333,6 @@ __device__ __forceinline__ void lin_tile(const LinGemm &a, char *lds, int i0, in
   const int nst = (a.R + BK - 1) / BK;
   const int s0 = PART ? __builtin_amdgcn_readfirstlane((int)((long long)z * nst / a.splits)) : 0;
   const int s1 = PART ? __builtin_amdgcn_readfirstlane((int)((long long)(z + 1) * nst / a.splits)) : nst;
-
-  Stager<C::TI, C::PA, ASTR, false> la;
-  Stager<C::TJ, C::PB, BSTR, true> lb;
-  la.init(a.A, a.I, i0, a.R, a.lda, wave, lane);
-  lb.init(a.B, a.J, j0, a.R, a.ldb, wave, lane);
 
   // Operand reads.  MFMA operand lane l holds row l % 16 and r = 8 (l / 16) ..
   // + 7 of the 32.  The product is formed transposed: the MFMA's row operand
@@ -342,63 +394,104 @@ __device__ __forceinline__ void lin_tile(const LinGemm &a, char *lds, int i0, in
   for (int i = 0; i < C::NI; ++i)
 #pragma unroll
     for (int j = 0; j < C::NJ; ++j) acc[i][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr int P = C::PA + C::PB;       // this wave's loads of a stage
-  auto issue = [&](int u, int s, int buf) __attribute__((always_inline)) {
-    if (u < C::PA) la.issue(u, s * BK, lds_addr(sm[buf].a));
-    else lb.issue(u - C::PA, s * BK, lds_addr(sm[buf].b));
-  };
-
-  // The operands of stage s are in registers when stage s is multiplied: they
-  // are read from LDS between the MFMAs of stage s - 1, and their buffer takes
-  // the loads of stage s + NS.  One barrier per stage: behind it every wave
-  // has its operands of stage s (its buffer is free) and its loads of stage s +
-  // 1 (they may be read).  A stage's work is dealt into P parts of one load, a
-  // share of the next operands' reads and a share of the MFMAs, so that
-  // neither the loads of eight waves nor their reads meet in one burst.
-  // Stages past s1 are loaded and read, not multiplied.
-#pragma unroll
-  for (int p = 0; p < C::NS; ++p)
-#pragma unroll
-    for (int u = 0; u < P; ++u) issue(u, s0 + p, p);
-  int buf = 0;               // of the stage in registers
-  auto step = [&](int s, const Frags &cur, Frags &nxt) __attribute__((always_inline)) {
-    stage_wait<(C::NS - 2) * P>();
-    const int next = buf + 1 == C::NS ? 0 : buf + 1;
-#pragma unroll
-    for (int u = 0; u < P; ++u) {
-      issue(u, s + C::NS, buf);
-#pragma unroll
-      for (int x = u * (C::NJ + C::NI) / P; x < (u + 1) * (C::NJ + C::NI) / P; ++x) {
-        if (x < C::NJ) read_b(next, x, nxt);
-        else read_a(next, x - C::NJ, nxt);
+  if constexpr (RAGGED) {
+    // Four stages on their way in registers, two in LDS: a wave writes stage s
+    // + 1 while others may still read stage s, and reaches the barrier of stage
+    // s + 1 only behind its reads of stage s.
+    RaggedStager<C::TI, ASTR, false> la;
+    RaggedStager<C::TJ, BSTR, true> lb;
+    la.init(a.A, a.I, i0, a.R, a.lda, wave, lane);
+    lb.init(a.B, a.J, j0, a.R, a.ldb, wave, lane);
+    v4u ra[4], rb[4];
+    auto fetch = [&](int d, int s) __attribute__((always_inline)) {
+      if (s < s1) {
+        ra[d] = la.load(s * BK);
+        rb[d] = lb.load(s * BK);
       }
+    };
 #pragma unroll
-      for (int i = u * C::NI / P; i < (u + 1) * C::NI / P; ++i)
+    for (int d = 0; d < 4; ++d) fetch(d, s0 + d);
+    for (int s = s0; s < s1; s += 4)
 #pragma unroll
-        for (int j = 0; j < C::NJ; ++j) acc[i][j] = mfma<DT>(cur.b[j], cur.a[i], acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int d = 0; d < 4; ++d)
+        if (s + d < s1) {
+          *reinterpret_cast<v4u *>(sm[d & 1].a + wave * 1024 + lane * 16) = ra[d];
+          *reinterpret_cast<v4u *>(sm[d & 1].b + wave * 1024 + lane * 16) = rb[d];
+          fetch(d, s + d + 4);
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          Frags f;
+#pragma unroll
+          for (int j = 0; j < C::NJ; ++j) read_b(d & 1, j, f);
+#pragma unroll
+          for (int i = 0; i < C::NI; ++i) read_a(d & 1, i, f);
+#pragma unroll
+          for (int i = 0; i < C::NI; ++i)
+#pragma unroll
+            for (int j = 0; j < C::NJ; ++j) acc[i][j] = mfma<DT>(f.b[j], f.a[i], acc[i][j]);
+        }
+  } else {
+    Stager<C::TI, C::PA, ASTR, false> la;
+    Stager<C::TJ, C::PB, BSTR, true> lb;
+    la.init(a.A, a.I, i0, a.R, a.lda, wave, lane);
+    lb.init(a.B, a.J, j0, a.R, a.ldb, wave, lane);
+    constexpr int P = C::PA + C::PB;       // this wave's loads of a stage
+    auto issue = [&](int u, int s, int buf) __attribute__((always_inline)) {
+      if (u < C::PA) la.issue(u, s * BK, lds_addr(sm[buf].a));
+      else lb.issue(u - C::PA, s * BK, lds_addr(sm[buf].b));
+    };
+
+    // The operands of stage s are in registers when stage s is multiplied: they
+    // are read from LDS between the MFMAs of stage s - 1, and their buffer takes
+    // the loads of stage s + NS.  One barrier per stage: behind it every wave
+    // has its operands of stage s (its buffer is free) and its loads of stage s +
+    // 1 (they may be read).  A stage's work is dealt into P parts of one load, a
+    // share of the next operands' reads and a share of the MFMAs, so that
+    // neither the loads of eight waves nor their reads meet in one burst.
+    // Stages past s1 are loaded and read, not multiplied.
+#pragma unroll
+    for (int p = 0; p < C::NS; ++p)
+#pragma unroll
+      for (int u = 0; u < P; ++u) issue(u, s0 + p, p);
+    int buf = 0;               // of the stage in registers
+    auto step = [&](int s, const Frags &cur, Frags &nxt) __attribute__((always_inline)) {
+      stage_wait<(C::NS - 2) * P>();
+      const int next = buf + 1 == C::NS ? 0 : buf + 1;
+#pragma unroll
+      for (int u = 0; u < P; ++u) {
+        issue(u, s + C::NS, buf);
+#pragma unroll
+        for (int x = u * (C::NJ + C::NI) / P; x < (u + 1) * (C::NJ + C::NI) / P; ++x) {
+          if (x < C::NJ) read_b(next, x, nxt);
+          else read_a(next, x - C::NJ, nxt);
+        }
+#pragma unroll
+        for (int i = u * C::NI / P; i < (u + 1) * C::NI / P; ++i)
+#pragma unroll
+          for (int j = 0; j < C::NJ; ++j) acc[i][j] = mfma<DT>(cur.b[j], cur.a[i], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      buf = next;
+    };
+    Frags f0, f1;
+    stage_wait<(C::NS - 1) * P>();
+#pragma unroll
+    for (int j = 0; j < C::NJ; ++j) read_b(0, j, f0);
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i) read_a(0, i, f0);
+    int s = s0;
+    for (; s + 1 < s1; s += 2) {
+      step(s, f0, f1);
+      step(s + 1, f1, f0);
     }
-    buf = next;
-  };
-  Frags f0, f1;
-  stage_wait<(C::NS - 1) * P>();
+    if (s < s1) {
 #pragma unroll
-  for (int j = 0; j < C::NJ; ++j) read_b(0, j, f0);
+      for (int i = 0; i < C::NI; ++i)
 #pragma unroll
-  for (int i = 0; i < C::NI; ++i) read_a(0, i, f0);
-  int s = s0;
-  for (; s + 1 < s1; s += 2) {
-    step(s, f0, f1);
-    step(s + 1, f1, f0);
+        for (int j = 0; j < C::NJ; ++j) acc[i][j] = mfma<DT>(f0.b[j], f0.a[i], acc[i][j]);
+    }
+    // no load may land in LDS that the next workgroup owns
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   }
-  if (s < s1) {
-#pragma unroll
-    for (int i = 0; i < C::NI; ++i)
-#pragma unroll
-      for (int j = 0; j < C::NJ; ++j) acc[i][j] = mfma<DT>(f0.b[j], f0.a[i], acc[i][j]);
-  }
-  // no load may land in LDS that the next workgroup owns
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   const int j = j0 + wj * 64 + 16 * g;
   if constexpr (PART) {
@@ -463,7 +556,10 @@ __device__ __forceinline__ void lin_part(const LinGemm &a, char *lds, int u) {
   lin_unit(a, u % count, a.full, count, a.cut, bi, bj, part);
   const int i0 = bi * 256 + (a.cut == 4 ? part >> 1 : 0) * 128, j0 = bj * 256 + (part & 1) * 128;
   if (i0 >= a.I || j0 >= a.J) return;
-  if (a.splits > 1) lin_tile<Quarter, DT, AS, BS, true>(a, lds, i0, j0, z);
+  if (a.ragged) {
+    if (a.splits > 1) lin_tile<Quarter, DT, AS, BS, true, true>(a, lds, i0, j0, z);
+    else lin_tile<Quarter, DT, AS, BS, false, true>(a, lds, i0, j0, 0);
+  } else if (a.splits > 1) lin_tile<Quarter, DT, AS, BS, true>(a, lds, i0, j0, z);
   else if (a.cut == 4) lin_tile<Quarter, DT, AS, BS, false>(a, lds, i0, j0, 0);
   else lin_tile<Half, DT, AS, BS, false>(a, lds, i0, j0, 0);
 }
@@ -565,24 +661,6 @@ __global__ __launch_bounds__(256) void k_lin_reduce(LinGemm first, LinGemm secon
 // columns 8 c + j.  W never passes through LDS.  The result lane holds row
 // l % 16 and 32 consecutive columns.
 constexpr int kSkCols = 128, kSkWaves = 4;
-
-// Eight elements from i on of an array of `end` >= 8; those past the end are
-// anything.
-__device__ __forceinline__ v4u load_within(const uint16_t *p, long long i, long long end) {
-  const long long at = i < end - 8 ? i : end - 8;
-  const int d = (int)(i - at), s = d >> 1;
-  const v4u t = *reinterpret_cast<const U16 *>(p + at);
-  v4u u;   // t shifted down by s dwords, then by the odd element
-#pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    u[h] = t[h];
-#pragma unroll
-    for (int k = 1; h + k < 4; ++k) u[h] = s == k ? t[h + k] : u[h];
-  }
-#pragma unroll
-  for (int h = 0; h < 4; ++h) u[h] = __builtin_amdgcn_alignbit(h < 3 ? u[h + 1] : 0u, u[h], (uint32_t)(d & 1) * 16u);
-  return u;
-}
 
 template <int DT, int MT, bool PART>
 __global__ __launch_bounds__(64 * kSkWaves, 5 - MT) void k_lin_skinny(LinGemm a) {
@@ -836,6 +914,16 @@ int gemm_splits(int I, int J, int R) {
   return best;
 }
 
+// Whether a product with rows that are no multiple of 8 reads them as they are
+// (128 x 128 tiles staged through registers, 0.45 us a stage) instead of from
+// padded copies (a launch more, 0.3 us a stage).  As they are / padded, us:
+// 202 x 1502 x 359 13.6 / 16.6, 333 x 1001 x 777 14.8 / 17.7, gradients of
+// 1500 x 1023 x 1401 37 / 55; a long reduction, 1000 x 4001 x 1201, 63 / 55; many
+// tiles, 4000 x 999 x 3999, 81 / 55.
+bool reads_ragged(int I, int J, int R) {
+  return quarters(I, J) <= kCus / 2 && R / gemm_splits(I, J, R) <= 2048;
+}
+
 // How the last `rem` of the tiles, after whole rounds of one 256 x 256 tile
 // per CU, are cut: in 1, 2 or 4.  The cost of a round relative to a full one
 // of whole tiles (115 us at a reduction of 4096): 0.55 for halves, 0.34 for
@@ -862,24 +950,25 @@ void plan_units(LinGemm &a, LinGemm &b) {
   for (LinGemm *j : order) {
     j->nbi = ceil_div(j->I, 256);
     j->nbj = ceil_div(j->J, 256);
-    if (j->splits <= 1) work += (double)j->nbi * j->nbj * j->R;
+    if (j->splits <= 1 && !j->ragged) work += (double)j->nbi * j->nbj * j->R;
   }
-  LinGemm *last = order[1]->nbi * order[1]->nbj > 0 && order[1]->splits <= 1 ? order[1] : order[0];
+  auto apart = [](const LinGemm *j) { return j->splits > 1 || j->ragged; };   // all in quarters
+  LinGemm *last = order[1]->nbi * order[1]->nbj > 0 && !apart(order[1]) ? order[1] : order[0];
   const int rem = last->R > 0 ? (int)(work / last->R) % kCus : 0, cut = best_cut(rem);
   // split tiles have the longest way to go for their size: they start first
   int base = 0;
   for (LinGemm *j : order)
-    if (j->splits > 1) {
+    if (apart(j)) {
       j->parts0 = base;
-      base += 4 * j->nbi * j->nbj * j->splits;
+      base += 4 * j->nbi * j->nbj * std::max(1, j->splits);
     }
   for (LinGemm *j : order) {
     const int t = j->nbi * j->nbj;
     j->cut = cut;
     j->full = t;
     j->parts = 0;
-    if (j->splits > 1) {
-      j->full = 0; j->cut = 4; j->parts = 4 * t * j->splits;
+    if (apart(j)) {
+      j->full = 0; j->cut = 4; j->parts = 4 * t * std::max(1, j->splits);
     } else if (j == last && cut > 1) {
       j->full = std::max(0, t - rem);
       j->parts = (t - j->full) * cut;
@@ -888,7 +977,7 @@ void plan_units(LinGemm &a, LinGemm &b) {
     base += j->full;
   }
   for (LinGemm *j : order)
-    if (j->splits <= 1) {
+    if (!apart(j)) {
       j->parts0 = base;
       base += j->parts;
     }
@@ -967,8 +1056,10 @@ LinPlan plan_linear(int M, int K, int N) {
   // (its loads at the end of X and W are moved back inside them: 8 elements at least)
   p.skinny = M <= kLinSkinnyMaxM && (long long)M * K >= 8 && (long long)K * N >= 8;
   p.splits = p.skinny ? skinny_splits(N, K) : gemm_splits(M, N, K);
-  p.pad_x = !p.skinny && p.kp != K;
-  p.pad_w = !p.skinny && p.np != N;
+  const bool odd = p.kp != K || p.np != N, whole = (long long)M * K >= 8 && (long long)K * N >= 8;
+  p.ragged_x = p.ragged_w = !p.skinny && odd && whole && reads_ragged(M, N, K);
+  p.pad_x = !p.skinny && !p.ragged_x && p.kp != K;
+  p.pad_w = !p.skinny && !p.ragged_x && p.np != N;
   size_t off = 0;
   p.x_off = off;
   if (p.pad_x) off = align_up(off + (size_t)M * p.kp * 2, 256);
@@ -984,8 +1075,11 @@ LinPlan plan_linear_backward(int M, int K, int N) {
   LinPlan p;
   p.kp = ceil_div(K, 8) * 8;
   p.np = ceil_div(N, 8) * 8;
-  p.pad_x = p.kp != K;
-  p.pad_w = p.np != N;
+  // dZ always has whole rows; W is read for dX, X for dW
+  p.ragged_w = p.np != N && (long long)K * N >= 8 && reads_ragged(M, K, N);
+  p.ragged_x = p.kp != K && (long long)M * K >= 8 && reads_ragged(K, N, M);
+  p.pad_x = p.kp != K && !p.ragged_x;
+  p.pad_w = p.np != N && !p.ragged_w;
   p.splits_dx = gemm_splits(M, K, N);
   p.splits_dw = gemm_splits(K, N, M);
   // row slices of the dZ pass: about 1024 workgroups, at least one row per
