@@ -12,6 +12,11 @@
 // large common offset costs no precision) and written once.  A row belongs
 // to one wave, four waves or eight, the fewest whose registers hold it.
 // Statistics and parameter sums are fp32.
+//
+// Measured on an MI355X (a large copy: 4.92 TB/s): 8192 x 1152 bf16 with
+// parameters per half of the rows, forward 12 us (38 MB, 3.1 TB/s, of which 3
+// us are what one row takes), backward 18.6 us (57 MB: 18 us, its partial
+// rows 4 us, overlapping); 1537 x 2241 fp32 backward 16 us (35 MB).
 #include "hsq_internal.h"
 
 #include <algorithm>
