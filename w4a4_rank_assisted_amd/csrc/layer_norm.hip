@@ -369,6 +369,7 @@ hipError_t pick_width(const NormArgs &a, bool backward, hipStream_t s) {
   if (a.C <= 2048) return run_norm<TX, TY, 4, 1>(a, backward, s);
   if (a.C <= 4096) return run_norm<TX, TY, 4, 2>(a, backward, s);
   if (a.C <= 8192) return run_norm<TX, TY, 8, 2>(a, backward, s);
+  if (a.C <= 12288) return run_norm<TX, TY, 8, 3>(a, backward, s);
   return run_norm<TX, TY, 8, 4>(a, backward, s);
 }
 

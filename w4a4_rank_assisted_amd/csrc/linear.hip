@@ -909,18 +909,18 @@ constexpr int kCus = 256;
 int quarters(int I, int J) { return ceil_div(I, 128) * ceil_div(J, 128); }
 
 // Splits of the reduction, each of at least 256, for fewer 128 x 128 tiles
-// than CUs: towards 128 workgroups, or 256 where few rows stream a long
-// operand (64 x 12288 x 4096, 32 tiles: 4 splits 39 us, 8 44, 2 64, none 112).
-// Of these the cheapest: a stage of 32 takes 0.3 us, the second launch 3 us,
-// and the partial sums go out and back at 2.5 TB/s (1000 x 1024 x 1024: none
-// 13.6 us, 2 19.8; 256 x 8192 x 256: none 65 us, 16 16.7).
+// than CUs: the cheapest by what was measured.  A stage of 32 takes 0.3 us, a
+// streamed operand arrives at 3 TB/s, the second launch takes 3 us, and the
+// partial sums go out and back at 2.5 TB/s.  64 x 12288 x 4096 (32 tiles): 4
+// splits 39 us, 8 44, 2 64, none 112; 64 x 4096 x 12288 (96): none 44, 2 49; 1000 x
+// 1024 x 1024 (64): none 13.6, 2 19.8; 256 x 8192 x 256 (4): 16 16.7, none 65.
 int gemm_splits(int I, int J, int R) {
-  const int tiles = quarters(I, J), cap = std::min(kCus / tiles, std::max(kCus / 2 / tiles, R / 64 / I));
-  const int most = std::min({cap, R / 256, 16});
+  const int most = std::min({kCus / quarters(I, J), R / 256, 16});
+  const float stream = 2.0f / 3e6f * ((float)I + J) * R;
   int best = 1;
   float least = 0.0f;
   for (int s = 1; s <= most; ++s) {
-    const float us = 0.3f / 32 * R / s + (s > 1 ? 3.0f + 3.2e-6f * s * I * J : 0.0f);
+    const float us = std::max(0.3f / 32 * R / s, stream) + (s > 1 ? 3.0f + 3.2e-6f * s * I * J : 0.0f);
     if (s == 1 || us < least) least = us, best = s;
   }
   return best;
@@ -936,55 +936,85 @@ bool reads_ragged(int I, int J, int R) {
   return quarters(I, J) <= kCus / 2 && R / gemm_splits(I, J, R) <= 2048;
 }
 
-// How the last `rem` of the tiles, after whole rounds of one 256 x 256 tile
-// per CU, are cut: in 1, 2 or 4.  The cost of a round relative to a full one
-// of whole tiles (115 us at a reduction of 4096): 0.55 for halves, 0.34 for
-// quarters, and a round that fills only the share f of the CUs costs 0.35 +
-// 0.65 f of that (the chip is power-limited: idle CUs speed up the others).
-// Measured, us: 1.5 rounds whole 192, halves 176, quarters 193; 0.66 rounds 76,
-// 90, 88; 1.125 rounds 76, 62, 56.
-int best_cut(int rem) {
-  auto cost = [](int units, float round) {
-    const int part = units % kCus;
-    return round * (units / kCus + (part ? 0.35f + 0.65f * part / kCus : 0.0f));
-  };
-  const float full = cost(rem, 1.0f), half = cost(2 * rem, 0.55f), quarter = cost(4 * rem, 0.34f);
-  return full <= half && full <= quarter ? 1 : half <= quarter ? 2 : 4;
+// Units of a job whose tiles are all cut in 1, 2 or 4 (empty parts left out),
+// and the time of one relative to a stage of a whole tile.
+int units_of(const LinGemm &a, int cut) {
+  return cut == 1 ? a.nbi * a.nbj : cut == 2 ? a.nbi * ceil_div(a.J, 128) : quarters(a.I, a.J);
 }
+float unit_time(const LinGemm &a, int cut) { return (cut == 1 ? 1.0f : cut == 2 ? 0.6f : 0.4f) * a.R; }
 
-// Sets the units of the jobs of one launch.  The job with the longer reduction
-// runs first; the tiles left over from whole rounds, counted in tiles of the
-// second, are the second's last.
+// Sets the units of the jobs of one launch: which tiles are cut.  Either the
+// last of the second job are, those left over from whole rounds of one tile
+// per CU, or all tiles of a job.  Estimated: one round takes its longest unit
+// (shorter where CUs idle: the chip is power-limited), more rounds the work
+// over the CUs and half of a last unit.  Measured, us: 1.5 rounds whole 192,
+// last cut in halves 176, in quarters 193; 1.125 rounds 76, 62, 56; 0.66 rounds
+// whole 76, all in halves 90, in quarters 88; 18 tiles of 144 stages beside 162 of
+// 14 whole 116.
+// The job with the longer reduction runs first; jobs with a split reduction
+// or ragged rows are all quarters and start before the others.
 void plan_units(LinGemm &a, LinGemm &b) {
   LinGemm *order[2] = {&a, &b};
   if (b.R > a.R) std::swap(order[0], order[1]);
-  double work = 0.0;
-  for (LinGemm *j : order) {
+  auto apart = [](const LinGemm *j) { return j->splits > 1 || j->ragged; };
+  int base = 0, t[2] = {0, 0};
+  for (int i = 0; i < 2; ++i) {
+    LinGemm *j = order[i];
     j->nbi = ceil_div(j->I, 256);
     j->nbj = ceil_div(j->J, 256);
-    if (j->splits <= 1 && !j->ragged) work += (double)j->nbi * j->nbj * j->R;
-  }
-  auto apart = [](const LinGemm *j) { return j->splits > 1 || j->ragged; };   // all in quarters
-  LinGemm *last = order[1]->nbi * order[1]->nbj > 0 && !apart(order[1]) ? order[1] : order[0];
-  const int rem = last->R > 0 ? (int)(work / last->R) % kCus : 0, cut = best_cut(rem);
-  // split tiles have the longest way to go for their size: they start first
-  int base = 0;
-  for (LinGemm *j : order)
+    j->full = j->parts = j->full0 = j->parts0 = 0;
+    j->cut = 1;
     if (apart(j)) {
+      j->cut = 4;
+      j->parts = 4 * j->nbi * j->nbj * std::max(1, j->splits);
       j->parts0 = base;
-      base += 4 * j->nbi * j->nbj * std::max(1, j->splits);
+      base += j->parts;
+    } else {
+      t[i] = j->nbi * j->nbj;
     }
+  }
+  if (t[0] + t[1] > 0) {
+    LinGemm *last = t[1] > 0 ? order[1] : order[0];
+    const int tl = t[1] > 0 ? t[1] : t[0];
+    const double whole = ((double)t[0] * order[0]->R + (double)t[1] * order[1]->R) / last->R;
+    const int rem = std::min(tl, (int)whole % kCus);
+    auto estimate = [&](double units, double work, double longest, double end) {
+      return units <= kCus ? longest * (0.5 + 0.5 * units / kCus) : std::max(longest, work / kCus + 0.5 * end);
+    };
+    const double others = t[0] + t[1] - tl, first = t[1] > 0 && t[0] > 0 ? order[0]->R : 0.0;
+    double least = 0.0;
+    int tail = 1, cuts[2] = {1, 1};
+    for (int c : {1, 2, 4}) {           // the last job's last tiles
+      const double u = unit_time(*last, c), work = others * first + (double)(tl - rem) * last->R + (double)rem * c * u;
+      const double e = estimate(others + tl - rem + (double)rem * c, work, std::max(first, tl > rem ? (double)last->R : u), u);
+      if (c == 1 || e < least) least = e, tail = c;
+    }
+    bool all = false;
+    for (int c0 : {1, 2, 4})            // all tiles of either job
+      for (int c1 : {1, 2, 4}) {
+        if ((t[0] == 0 && c0 > 1) || (t[1] == 0 && c1 > 1)) continue;
+        double units = 0.0, work = 0.0, longest = 0.0, end = 0.0;
+        const int c[2] = {c0, c1};
+        for (int i = 0; i < 2; ++i)
+          if (t[i] > 0) {
+            end = unit_time(*order[i], c[i]);
+            longest = std::max(longest, end);
+            units += units_of(*order[i], c[i]);
+            work += units_of(*order[i], c[i]) * end;
+          }
+        const double e = estimate(units, work, longest, end);
+        if (e < least) least = e, all = true, cuts[0] = c0, cuts[1] = c1;
+      }
+    for (int i = 0; i < 2; ++i)
+      if (t[i] > 0) {
+        LinGemm *j = order[i];
+        const int cut = all ? cuts[i] : j == last ? tail : 1, n = cut == 1 ? 0 : all ? t[i] : rem;
+        j->cut = cut;
+        j->full = t[i] - n;
+        j->parts = n * cut;
+      }
+  }
   for (LinGemm *j : order) {
-    const int t = j->nbi * j->nbj;
-    j->cut = cut;
-    j->full = t;
-    j->parts = 0;
-    if (apart(j)) {
-      j->full = 0; j->cut = 4; j->parts = 4 * t * std::max(1, j->splits);
-    } else if (j == last && cut > 1) {
-      j->full = std::max(0, t - rem);
-      j->parts = (t - j->full) * cut;
-    }
     j->full0 = base;
     base += j->full;
   }
