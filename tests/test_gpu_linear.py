@@ -176,7 +176,7 @@ def test_outputs_stay_inside_their_buffers(M, K, N, dt):
     say(f"[linear buffers] M={M} K={K} N={N} {dt}")
     X, W, b, rnd = make(5, M, K, N, dt)
     dY = rnd(M, N).to(dt)
-    lib, P, code = hsq._load(), hsq._ptr, hsq._dtypes()[dt]
+    lib, P, code = hsq._load(), hsq._ptr, hsq._t().code[dt]
     outs = [guarded(s, dt) for s in ((M, K), (K, N), (N,))]
     need = hsq.linear_backward_workspace_bytes(M, K, N)
     ws = torch.full((need + 256,), 90, dtype=torch.uint8, device=DEV)

@@ -145,7 +145,7 @@ def test_binding_refuses_host_tensors():
 
 def test_binding_refuses_shapes_and_types(monkeypatch):
     # host tensors stand for device tensors up to the call: both are on "device" -1
-    monkeypatch.setattr(hsq, "_device", lambda t, name: -1)
+    monkeypatch.setattr(hsq, "_device", lambda T, t, name: -1)
     bf, f16, f32 = torch.bfloat16, torch.float16, torch.float32
     x, w = torch.zeros(4, 8, dtype=bf), torch.zeros(8, 16, dtype=bf)
     for bad in (torch.zeros(7, 16, dtype=bf), torch.zeros(8, dtype=bf)):
@@ -194,12 +194,12 @@ def test_binding_refuses_another_device(monkeypatch):
             return 1
 
     other = torch.zeros(4, 8, dtype=torch.bfloat16).as_subclass(T)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(hsq._t(), "current_device", lambda: 0)
     with pytest.raises(ValueError, match="current device"):
         hsq.layer_norm(other)
     with pytest.raises(ValueError, match="current device"):
         hsq.linear(other, other)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(hsq._t(), "current_device", lambda: 1)
     with pytest.raises(ValueError, match="HIP device 1"):      # X there, W on the host
         hsq.linear(other, torch.zeros(8, 8, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="HIP device 1"):

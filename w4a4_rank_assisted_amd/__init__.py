@@ -548,50 +548,49 @@ def closed_form_l2(HL1, Cinv, W, packed_w, sw, group: int = 64, out=None, worksp
 
 
 # ------------------------------------------- 16-bit linear, layer normalisation
-_DTYPES = {}
+class _Torch:
+    """What the calls below need of torch, looked up once: a norm of one token
+    is 3 us of GPU work and as much of launch, so the lookups show."""
 
-
-def _dtypes():
-    """torch dtype -> HSQ_* code, and its name -> torch dtype."""
-    if not _DTYPES:
+    def __init__(self):
         torch = _torch()
-        for name, code in (("f32", F32), ("bf16", BF16), ("f16", F16)):
-            t = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[name]
-            _DTYPES[t] = code
-            _DTYPES[name] = t
-    return _DTYPES
+        self.Tensor, self.empty, self.empty_like = torch.Tensor, torch.empty, torch.empty_like
+        self.f32, self.u8 = torch.float32, torch.uint8
+        self.named = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+        self.code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+        self.half = (torch.bfloat16, torch.float16)
+        self.any = (torch.float32, torch.bfloat16, torch.float16)
+        self.current_device = torch._C._cuda_getDevice
+        self.stream = torch._C._cuda_getCurrentRawStream   # see _stream
 
 
-def _half16():
-    torch = _torch()
-    return (torch.bfloat16, torch.float16)
+_cached = None
 
 
-def _norm_types():
-    torch = _torch()
-    return (torch.float32, torch.bfloat16, torch.float16)
+def _t() -> _Torch:
+    global _cached
+    if _cached is None:
+        _cached = _Torch()
+    return _cached
 
 
-def _device(t, name) -> int:
+def _device(T, t, name) -> int:
     """Index of the device the kernels run on: the current one, on whose
     current stream they are enqueued.  Every tensor has to live there."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, T.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     dev = t.get_device()
     if dev < 0:
         raise ValueError(f"{name} must be on a HIP device")
-    cur = torch.cuda.current_device()
+    cur = T.current_device()
     if dev != cur:
         raise ValueError(f"{name} is on cuda:{dev}, but the current device is cuda:{cur}")
     return dev
 
 
-def _arg(t, name, dev: int, dtypes, shape=None) -> int:
-    """Checks one operand and returns its device pointer (one pass over the
-    tensor's properties: these calls are short)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+def _arg(T, t, name, dev: int, dtypes, shape=None) -> int:
+    """Checks one operand and returns its device pointer."""
+    if not isinstance(t, T.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.get_device() != dev:
         raise ValueError(f"{name} must be on HIP device {dev}, the current device and that of the other operands")
@@ -604,32 +603,24 @@ def _arg(t, name, dev: int, dtypes, shape=None) -> int:
     return t.data_ptr()
 
 
-def _raw_stream(dev: int) -> int:
-    return _torch()._C._cuda_getCurrentRawStream(dev)
-
-
-def _y_type(y_dtype, x_dtype, allowed):
-    torch = _torch()
-    if y_dtype is None:
-        return x_dtype
-    if y_dtype not in ("f32", "bf16", "f16"):
+def _y_type(T, y_dtype, x_dtype, allowed):
+    if y_dtype not in T.named:
         raise ValueError(f"y_dtype {y_dtype!r} is not 'f32', 'bf16' or 'f16'")
-    t = _dtypes()[y_dtype]
+    t = T.named[y_dtype]
     if t not in allowed:
         raise TypeError(f"y_dtype {y_dtype} does not go with {x_dtype} inputs")
     return t
 
 
-def _scratch(workspace, need, X, dev):
+def _scratch(T, workspace, need, X, dev):
     """(workspace, pointer, bytes): the caller's, or a new one of need() bytes."""
-    torch = _torch()
     if workspace is None:
         n = int(need())
         if n == 0:
             return None, None, 0
-        workspace = torch.empty(n, dtype=torch.uint8, device=X.device)
+        workspace = T.empty(n, dtype=T.u8, device=X.device)
         return workspace, workspace.data_ptr(), n
-    return workspace, _arg(workspace, "workspace", dev, (torch.uint8,)), workspace.numel()
+    return workspace, _arg(T, workspace, "workspace", dev, (T.u8,)), workspace.numel()
 
 
 def linear_workspace_bytes(M: int, K: int, N: int) -> int:
@@ -650,32 +641,32 @@ def linear(X, W, bias=None, residual=None, *, act: str = "identity", y_dtype=Non
     preact_out or return_preact the values before the activation are written
     in X's type, as linear_backward takes them; return_preact returns
     (Y, Z)."""
-    torch = _torch()
+    T = _t()
     lib = _load()
-    dts = _dtypes()
-    dev = _device(X, "X")
-    px = _arg(X, "X", dev, _half16())
+    dts = T.code
+    dev = _device(T, X, "X")
+    px = _arg(T, X, "X", dev, T.half)
     M, K = X.shape
     dt = X.dtype
     half = (dt,)
-    pw = _arg(W, "W", dev, half)
+    pw = _arg(T, W, "W", dev, half)
     N = _columns(W, X, K)
     if act not in _LINEAR_ACTS:
         raise ValueError(f"act {act!r} not in {sorted(_LINEAR_ACTS)}")
-    ydt = dt if y_dtype is None else _y_type(y_dtype, dt, (torch.float32, dt))
-    pb = None if bias is None else _arg(bias, "bias", dev, half, (N,))
-    pr = None if residual is None else _arg(residual, "residual", dev, (ydt,), (M, N))
+    ydt = dt if y_dtype is None else _y_type(T, y_dtype, dt, (T.f32, dt))
+    pb = None if bias is None else _arg(T, bias, "bias", dev, half, (N,))
+    pr = None if residual is None else _arg(T, residual, "residual", dev, (ydt,), (M, N))
     if out is None:
-        out = torch.empty((M, N), dtype=ydt, device=X.device)
+        out = T.empty((M, N), dtype=ydt, device=X.device)
         po = out.data_ptr()
     else:
-        po = _arg(out, "out", dev, (ydt,), (M, N))
+        po = _arg(T, out, "out", dev, (ydt,), (M, N))
     if preact_out is None and return_preact:
-        preact_out = torch.empty((M, N), dtype=dt, device=X.device)
-    pz = None if preact_out is None else _arg(preact_out, "preact_out", dev, half, (M, N))
-    workspace, ps, nbytes = _scratch(workspace, lambda: lib.hsq_linear_workspace_bytes(M, K, N), X, dev)
+        preact_out = T.empty((M, N), dtype=dt, device=X.device)
+    pz = None if preact_out is None else _arg(T, preact_out, "preact_out", dev, half, (M, N))
+    workspace, ps, nbytes = _scratch(T, workspace, lambda: lib.hsq_linear_workspace_bytes(M, K, N), X, dev)
     _check(lib.hsq_linear(px, M, K, N, dts[dt], pw, pb, _LINEAR_ACTS[act], pr, po, dts[ydt], pz, ps, nbytes,
-                          _raw_stream(dev)), "hsq_linear")
+                          T.stream(dev)), "hsq_linear")
     return (out, preact_out) if return_preact else out
 
 
@@ -689,32 +680,31 @@ def linear_backward(dY, X, W, preact=None, *, act: str = "identity", need_input:
     (K, N), preact (M, N) as ``linear`` returned it (not needed for the
     identity).  Returns (dX, dW, dbias) in X's type, None where not needed;
     the residual's gradient is dY itself."""
-    torch = _torch()
+    T = _t()
     lib = _load()
-    dts = _dtypes()
-    dev = _device(X, "X")
-    px = _arg(X, "X", dev, _half16())
+    dts = T.code
+    dev = _device(T, X, "X")
+    px = _arg(T, X, "X", dev, T.half)
     M, K = X.shape
     dt = X.dtype
-    pw = _arg(W, "W", dev, (dt,))
+    pw = _arg(T, W, "W", dev, (dt,))
     N = _columns(W, X, K)
     if act not in _LINEAR_ACTS:
         raise ValueError(f"act {act!r} not in {sorted(_LINEAR_ACTS)}")
-    py = _arg(dY, "dY", dev, (dt, torch.float32), (M, N))
-    pz = None if act == "identity" else _arg(preact, "preact", dev, (dt,), (M, N))
-    dX = torch.empty_like(X) if need_input else None
-    dW = torch.empty_like(W) if need_weight else None
-    db = torch.empty((N,), dtype=dt, device=X.device) if need_bias else None
-    workspace, ps, nbytes = _scratch(workspace, lambda: lib.hsq_linear_backward_workspace_bytes(M, K, N), X, dev)
+    py = _arg(T, dY, "dY", dev, (dt, T.f32), (M, N))
+    pz = None if act == "identity" else _arg(T, preact, "preact", dev, (dt,), (M, N))
+    dX = T.empty_like(X) if need_input else None
+    dW = T.empty_like(W) if need_weight else None
+    db = T.empty((N,), dtype=dt, device=X.device) if need_bias else None
+    workspace, ps, nbytes = _scratch(T, workspace, lambda: lib.hsq_linear_backward_workspace_bytes(M, K, N), X, dev)
     _check(lib.hsq_linear_backward(py, dts[dY.dtype], px, M, K, N, dts[dt], pw, pz, _LINEAR_ACTS[act], _ptr(dX),
-                                   _ptr(dW), _ptr(db), ps, nbytes, _raw_stream(dev)), "hsq_linear_backward")
+                                   _ptr(dW), _ptr(db), ps, nbytes, T.stream(dev)), "hsq_linear_backward")
     return dX, dW, db
 
 
-def _norm_param(p, name, dev, ydt, C):
+def _norm_param(T, p, name, dev, ydt, C):
     """weight / bias (C,) or (groups, C), fp32 or of Y's type -> (pointer, groups)."""
-    torch = _torch()
-    ptr = _arg(p, name, dev, (torch.float32, ydt))
+    ptr = _arg(T, p, name, dev, (T.f32, ydt))
     if p.dim() not in (1, 2) or p.shape[-1] != C:
         raise ValueError(f"{name}: shape {tuple(p.shape)} is neither ({C},) nor (groups, {C})")
     return ptr, 1 if p.dim() == 1 else p.shape[0]
@@ -728,34 +718,34 @@ def layer_norm(X, weight=None, bias=None, *, eps: float = 1e-5, y_dtype=None, ou
     image); both of one type, fp32 or Y's.  Y is of X's type, or for fp32 X
     of y_dtype.  ``out`` may be X where the types are equal.  return_stats:
     (Y, mean, rstd), fp32 (M,), for layer_norm_backward."""
-    torch = _torch()
+    T = _t()
     lib = _load()
-    dts = _dtypes()
-    dev = _device(X, "X")
-    px = _arg(X, "X", dev, _norm_types())
+    dts = T.code
+    dev = _device(T, X, "X")
+    px = _arg(T, X, "X", dev, T.any)
     M, C = X.shape
     xdt = X.dtype
-    ydt = xdt if y_dtype is None else _y_type(y_dtype, xdt, _norm_types() if xdt == torch.float32 else (xdt,))
-    groups, pdt, pw, pb = 1, torch.float32, None, None
+    ydt = xdt if y_dtype is None else _y_type(T, y_dtype, xdt, T.any if xdt == T.f32 else (xdt,))
+    groups, pdt, pw, pb = 1, T.f32, None, None
     if weight is not None:
-        pw, groups = _norm_param(weight, "weight", dev, ydt, C)
+        pw, groups = _norm_param(T, weight, "weight", dev, ydt, C)
         pdt = weight.dtype
     if bias is not None:
-        pb, groups = _norm_param(bias, "bias", dev, ydt, C)
+        pb, groups = _norm_param(T, bias, "bias", dev, ydt, C)
         pdt = bias.dtype
         if weight is not None and (weight.shape != bias.shape or weight.dtype != pdt):
             raise ValueError("weight and bias differ in shape or type")
     if out is None:
-        out = torch.empty_like(X) if ydt == xdt else torch.empty((M, C), dtype=ydt, device=X.device)
+        out = T.empty_like(X) if ydt == xdt else T.empty((M, C), dtype=ydt, device=X.device)
         po = out.data_ptr()
     else:
-        po = _arg(out, "out", dev, (ydt,), (M, C))
+        po = _arg(T, out, "out", dev, (ydt,), (M, C))
     mean = rstd = None
     if return_stats:
-        mean = torch.empty((M,), dtype=torch.float32, device=X.device)
-        rstd = torch.empty_like(mean)
+        mean = T.empty((M,), dtype=T.f32, device=X.device)
+        rstd = T.empty_like(mean)
     _check(lib.hsq_layer_norm(px, dts[xdt], M, C, groups, pw, pb, dts[pdt], eps, po, dts[ydt], _ptr(mean), _ptr(rstd),
-                              _raw_stream(dev)), "hsq_layer_norm")
+                              T.stream(dev)), "hsq_layer_norm")
     return (out, mean, rstd) if return_stats else out
 
 
@@ -769,30 +759,30 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, *, groups: int = 1, need
     rstd it returned -> (dX of X's type, dweight, dbias).  The parameter
     gradients have weight's shape and type; without a weight they are
     (groups, C) fp32.  None where not needed."""
-    torch = _torch()
+    T = _t()
     lib = _load()
-    dts = _dtypes()
-    dev = _device(X, "X")
-    px = _arg(X, "X", dev, _norm_types())
+    dts = T.code
+    dev = _device(T, X, "X")
+    px = _arg(T, X, "X", dev, T.any)
     M, C = X.shape
     xdt = X.dtype
-    py = _arg(dY, "dY", dev, _norm_types() if xdt == torch.float32 else (xdt,), (M, C))
-    f32 = (torch.float32,)
-    pm, pr = _arg(mean, "mean", dev, f32, (M,)), _arg(rstd, "rstd", dev, f32, (M,))
-    pdt, pw = torch.float32, None
+    py = _arg(T, dY, "dY", dev, T.any if xdt == T.f32 else (xdt,), (M, C))
+    f32 = (T.f32,)
+    pm, pr = _arg(T, mean, "mean", dev, f32, (M,)), _arg(T, rstd, "rstd", dev, f32, (M,))
+    pdt, pw = T.f32, None
     if weight is not None:
-        pw, wg = _norm_param(weight, "weight", dev, dY.dtype, C)
+        pw, wg = _norm_param(T, weight, "weight", dev, dY.dtype, C)
         if groups not in (1, wg):
             raise ValueError(f"groups {groups} does not go with weight {tuple(weight.shape)}")
         groups, pdt = wg, weight.dtype
-    dX = torch.empty_like(X) if need_input else None
+    dX = T.empty_like(X) if need_input else None
     dw = db = ps = None
     nbytes = 0
     if need_params:
-        dw = torch.empty((groups, C), dtype=pdt, device=X.device) if weight is None else torch.empty_like(weight)
-        db = torch.empty_like(dw)
+        dw = T.empty((groups, C), dtype=pdt, device=X.device) if weight is None else T.empty_like(weight)
+        db = T.empty_like(dw)
         workspace, ps, nbytes = _scratch(
-            workspace, lambda: lib.hsq_layer_norm_backward_workspace_bytes(M, C, groups), X, dev)
+            T, workspace, lambda: lib.hsq_layer_norm_backward_workspace_bytes(M, C, groups), X, dev)
     _check(lib.hsq_layer_norm_backward(py, dts[dY.dtype], px, dts[xdt], M, C, groups, pm, pr, pw, dts[pdt], _ptr(dX),
-                                       _ptr(dw), _ptr(db), ps, nbytes, _raw_stream(dev)), "hsq_layer_norm_backward")
+                                       _ptr(dw), _ptr(db), ps, nbytes, T.stream(dev)), "hsq_layer_norm_backward")
     return dX, dw, db
