@@ -14,8 +14,8 @@
 // Statistics and parameter sums are fp32.
 //
 // Measured on an MI355X (a large copy: 4.92 TB/s): 8192 x 1152 bf16 with
-// parameters per half of the rows, forward 12 us (38 MB, 3.1 TB/s, of which 3
-// us are what one row takes), backward 18.6 us (57 MB: 18 us, its partial
+// parameters per half of the rows, forward 11 us (38 MB; one row alone takes
+// 3 us), backward 18.6 us (57 MB: 18 us, its partial
 // rows 4 us, overlapping); 1537 x 2241 fp32 backward 16 us (35 MB).
 #include "hsq_internal.h"
 
@@ -137,67 +137,85 @@ constexpr int kRowThreads = 256;   // threads of a workgroup with one or four wa
 template <int W>
 constexpr int norm_threads() { return W > 4 ? W * 64 : kRowThreads; }
 
-// W waves to a row, NV runs of 8 elements to a lane: C <= 512 W NV.
+// W waves to a row, NV runs of 8 elements to a lane: C <= 512 W NV.  Sixteen
+// waves a CU go from row to row with the next one on its way: 8192 x 8192 bf16
+// 47 us (5.8 TB/s) against 60 with a workgroup per row, 4096 x 2240 fp32 16
+// against 19, 16384 x 1152 18 against 21; 32 waves 52, 17 and 19.
 template <int TX, int TY, int W, int NV>
 __global__ __launch_bounds__(norm_threads<W>()) void k_layer_norm(NormArgs a) {
   constexpr int RPB = norm_threads<W>() / (64 * W);     // rows per workgroup
-  __shared__ float red[2][W > 1 ? W : 1];
+  __shared__ float red[4][W > 1 ? W : 1];
   const int t = threadIdx.x % (64 * W), wave = t >> 6;
-  const size_t row = (size_t)blockIdx.x * RPB + threadIdx.x / (64 * W);
-  if (RPB > 1 && row >= (size_t)a.M) return;            // whole waves, and no barrier with W = 1
-  const size_t base = row * a.C;
-  const size_t g = (size_t)((int)row / a.rows) * a.C;
   const bool pf = a.p_dtype == kF32;
-  // the parameters travel with the row, not behind its statistics
-  float x[NV][8], w[NV][8], b[NV][8];
-  float s = 0.0f;
+  // the next row is loaded while this one is worked on; the parameters stay in
+  // registers from row to row of a group
+  Run<TX> nx[NV];
+  auto fetch = [&](int row) __attribute__((always_inline)) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = 8 * (t + v * 64 * W);
-    load8<TX>(a.X, base + c, a.C - c, x[v]);
-  }
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = 8 * (t + v * 64 * W);
-    if (a.w) load8p<TY>(a.w, pf, g + c, a.C - c, w[v]);
-    if (a.b) load8p<TY>(a.b, pf, g + c, a.C - c, b[v]);
-  }
-#pragma unroll
-  for (int v = 0; v < NV; ++v)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s += x[v][e];
-  const float mean = row_sum<W>(s, red[0], wave) / (float)a.C;
-  float q = 0.0f;
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = 8 * (t + v * 64 * W);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float d = c + e < a.C ? x[v][e] - mean : 0.0f;
-      q = fmaf(d, d, q);
+    for (int v = 0; v < NV; ++v) {
+      const int c = 8 * (t + v * 64 * W);
+      nx[v] = load_run<TX>(a.X, (size_t)row * a.C + c, a.C - c);
     }
-  }
-  const float rstd = 1.0f / sqrtf(row_sum<W>(q, red[1], wave) / (float)a.C + a.eps);
-  if (t == 0) {
-    if (a.mean) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = rstd;
-  }
+  };
+  float w[NV][8], b[NV][8];
+  int group = -1, turn = 0;
+  int row = blockIdx.x * RPB + threadIdx.x / (64 * W);
+  if (row < a.M) fetch(row);
+  for (; row < a.M; row += gridDim.x * RPB, turn ^= 2) {   // (no barrier with W = 1, one row at a time with more)
+    if (group != row / a.rows) {
+      group = row / a.rows;
+      const size_t g = (size_t)group * a.C;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = 8 * (t + v * 64 * W), n = a.C - c;
-    if (n <= 0) continue;
-    float y[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = (x[v][e] - mean) * rstd;
-    if (a.w) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= w[v][e];
+      for (int v = 0; v < NV; ++v) {
+        const int c = 8 * (t + v * 64 * W);
+        if (a.w) load8p<TY>(a.w, pf, g + c, a.C - c, w[v]);
+        if (a.b) load8p<TY>(a.b, pf, g + c, a.C - c, b[v]);
+      }
     }
-    if (a.b) {
+    const size_t base = (size_t)row * a.C;
+    float x[NV][8];
+    float s = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] += b[v][e];
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[v][e] = value<TX>(nx[v], e);
+        s += x[v][e];
+      }
+    if (row + (int)gridDim.x * RPB < a.M) fetch(row + gridDim.x * RPB);
+    const float mean = row_sum<W>(s, red[turn], wave) / (float)a.C;
+    float q = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = 8 * (t + v * 64 * W);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = c + e < a.C ? x[v][e] - mean : 0.0f;
+        q = fmaf(d, d, q);
+      }
     }
-    store8<TY>(a.Y, base + c, n, y);
+    const float rstd = 1.0f / sqrtf(row_sum<W>(q, red[turn + 1], wave) / (float)a.C + a.eps);
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = 8 * (t + v * 64 * W), n = a.C - c;
+      if (n <= 0) continue;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = (x[v][e] - mean) * rstd;
+      if (a.w) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= w[v][e];
+      }
+      if (a.b) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] += b[v][e];
+      }
+      store8<TY>(a.Y, base + c, n, y);
+    }
   }
 }
 
@@ -351,13 +369,14 @@ __global__ __launch_bounds__(kSumCols * kSumShares) void k_sum_parts(SumArgs a) 
 
 template <int TX, int TY, int W, int NV>
 hipError_t run_norm(const NormArgs &a, bool backward, hipStream_t s) {
-  constexpr int RPB = norm_threads<W>() / (64 * W);
+  // forward: sixteen waves a CU, each going from row to row
+  constexpr int RPB = norm_threads<W>() / (64 * W), kGrid = 256 * 1024 / norm_threads<W>();
   if (backward)
     hipLaunchKernelGGL((k_layer_norm_bwd<TX, TY, W, NV>), dim3((unsigned)a.parts, (unsigned)a.groups),
                        dim3(64 * kBwdWaves), 0, s, a);
   else
-    hipLaunchKernelGGL((k_layer_norm<TX, TY, W, NV>), dim3((unsigned)ceil_div(a.M, RPB)), dim3(norm_threads<W>()), 0,
-                       s, a);
+    hipLaunchKernelGGL((k_layer_norm<TX, TY, W, NV>), dim3((unsigned)std::min(ceil_div(a.M, RPB), kGrid)),
+                       dim3(norm_threads<W>()), 0, s, a);
   return hipGetLastError();
 }
 
