@@ -14,11 +14,11 @@
 //
 // What bounds them (MI355X; a large copy runs at 4.92 TB/s, a large library
 // product in bf16 at 1230 TFLOP/s, both measured):
-//   - many tokens: the chip's power.  2048 x 4096 x 12288 with silu takes 175-185
-//     us (1110-1180 TFLOP/s), its counters 1.93 GHz and the matrix cores busy
-//     for 58 % of the cycles; the same kernel on zeros runs a quarter faster,
+//   - many tokens: the chip's power.  2048 x 4096 x 12288 with silu takes 175-191
+//     us (1080-1180 TFLOP/s); 4096 x 8192 x 8192, two whole rounds of tiles, runs
+//     at 1.93 GHz with the matrix cores busy for 63 % of the cycles; the same kernel on zeros runs a quarter faster,
 //     and deeper buffers, fewer barriers or staging through registers change
-//     nothing.  The two gradients of 2048 x 12288 x 4096 take 350-360 us (1150-1180).
+//     nothing.  The two gradients of 2048 x 12288 x 4096 take 350-375 us.
 //   - few tokens: the read of W.  1 x 4096 x 12288: 21.3 us, 4.7 TB/s; 16 x 12288 x
 //     4096 with residual: 23.3 us, 4.35 TB/s, the second launch 4 us of it.
 //   - small ones: their launches.  333 x 1001 x 777: 14.8 us in two.
@@ -927,13 +927,13 @@ int gemm_splits(int I, int J, int R) {
 }
 
 // Whether a product with rows that are no multiple of 8 reads them as they are
-// (128 x 128 tiles staged through registers, 0.45 us a stage) instead of from
-// padded copies (a launch more, 0.3 us a stage).  As they are / padded, us:
-// 202 x 1502 x 359 13.6 / 16.6, 333 x 1001 x 777 14.8 / 17.7, gradients of
-// 1500 x 1023 x 1401 37 / 55; a long reduction, 1000 x 4001 x 1201, 63 / 55; many
-// tiles, 4000 x 999 x 3999, 81 / 55.
-bool reads_ragged(int I, int J, int R) {
-  return quarters(I, J) <= kCus / 2 && R / gemm_splits(I, J, R) <= 2048;
+// (128 x 128 tiles staged through registers, 0.45 us a stage instead of 0.3) or
+// from padded copies of `elems` elements (3.5 us and their way out and back at
+// 4.5 TB/s).  As they are / padded, us: 202 x 1502 x 359 13.6 / 16.6, 333 x 1001 x
+// 777 14.8 / 17.7, gradients of 1500 x 1023 x 1401 33 / 55, of 6 x 8768 x 9471 193 /
+// 223; 80 tiles of an unsplit 4001 63 / 55; many tiles, 4000 x 999 x 3999, 81 / 55.
+bool reads_ragged(int I, int J, int R, long long elems) {
+  return quarters(I, J) <= kCus / 2 && 0.15f / 32 * R / gemm_splits(I, J, R) <= 3.5f + 4.0f / 4.5e6f * elems;
 }
 
 // Units of a job whose tiles are all cut in 1, 2 or 4 (empty parts left out),
@@ -1099,7 +1099,8 @@ LinPlan plan_linear(int M, int K, int N) {
   p.skinny = M <= kLinSkinnyMaxM && (long long)M * K >= 8 && (long long)K * N >= 8;
   p.splits = p.skinny ? skinny_splits(N, K) : gemm_splits(M, N, K);
   const bool odd = p.kp != K || p.np != N, whole = (long long)M * K >= 8 && (long long)K * N >= 8;
-  p.ragged_x = p.ragged_w = !p.skinny && odd && whole && reads_ragged(M, N, K);
+  const long long copied = (p.kp != K ? (long long)M * K : 0) + (p.np != N ? (long long)K * N : 0);
+  p.ragged_x = p.ragged_w = !p.skinny && odd && whole && reads_ragged(M, N, K, copied);
   p.pad_x = !p.skinny && !p.ragged_x && p.kp != K;
   p.pad_w = !p.skinny && !p.ragged_x && p.np != N;
   size_t off = 0;
@@ -1118,8 +1119,8 @@ LinPlan plan_linear_backward(int M, int K, int N) {
   p.kp = ceil_div(K, 8) * 8;
   p.np = ceil_div(N, 8) * 8;
   // dZ always has whole rows; W is read for dX, X for dW
-  p.ragged_w = p.np != N && (long long)K * N >= 8 && reads_ragged(M, K, N);
-  p.ragged_x = p.kp != K && (long long)M * K >= 8 && reads_ragged(K, N, M);
+  p.ragged_w = p.np != N && (long long)K * N >= 8 && reads_ragged(M, K, N, (long long)K * N);
+  p.ragged_x = p.kp != K && (long long)M * K >= 8 && reads_ragged(K, N, M, (long long)M * K);
   p.pad_x = p.kp != K && !p.ragged_x;
   p.pad_w = p.np != N && !p.ragged_w;
   p.splits_dx = gemm_splits(M, K, N);
