@@ -454,7 +454,10 @@ int hsq_closed_form_l2(const float *HL1, const double *Cinv, int K, int N, int r
  *   Z         out: M x N of `dtype`, or NULL: the values before the
  *                  activation, as hsq_linear_backward takes them
  *   workspace    : ws_bytes >= hsq_linear_workspace_bytes(M, K, N) device
- *                  bytes (NULL is fine where that is 0)
+ *                  bytes (NULL is fine where that is 0); its contents on
+ *                  entry do not matter and are clobbered, here as in the
+ *                  three functions below: calls in order may share one,
+ *                  calls that overlap in time need one each
  * No output may overlap an input, except Y the residual.  Results do not
  * depend on earlier calls or on timing: sums run in a fixed order.
  * Errors: HSQ_E_INVAL, HSQ_E_ALIGN, HSQ_E_WORKSPACE, HSQ_E_HIP. */

@@ -423,3 +423,38 @@ def test_host_threads():
     [t.start() for t in ts]
     [t.join() for t in ts]
     assert not bad
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured calls of different sizes on one workspace, replayed in turn:
+    neither relies on what it left there."""
+    say("[linear graphs, one workspace]")
+    cases = [(300, 4096, 520), (333, 1001, 4777), (20, 3000, 500), (70, 515, 1023)]
+    ws = stale(max(max(hsq.linear_workspace_bytes(*c), hsq.linear_backward_workspace_bytes(*c)) for c in cases))
+    runs = []
+    for M, K, N in cases:
+        X, W, b, rnd = make(M, M, K, N, BF)
+        dY = rnd(M, N).to(BF)
+
+        def run(X=X, W=W, b=b, dY=dY):
+            return (hsq.linear(X, W, b, act="gelu", workspace=ws),) + hsq.linear_backward(dY, X, W, workspace=ws)
+
+        ref = [t.clone() for t in run()]
+        torch.cuda.synchronize()
+        graph, cap = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        cap.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(cap):
+            with torch.cuda.graph(graph, stream=cap):
+                outs = run()
+        torch.cuda.synchronize()
+        # `run` holds the inputs: a graph reads their memory at every replay, and
+        # the next capture returns the memory of dropped tensors to the device
+        runs.append((graph, outs, ref, run))
+    for rep in range(3):
+        for graph, outs, ref, _ in runs:
+            for o in outs:
+                o.fill_(float("nan"))
+            graph.replay()
+        torch.cuda.synchronize()
+        for graph, outs, ref, _ in runs:
+            assert all(torch.equal(a, c) for a, c in zip(outs, ref)), rep

@@ -16,9 +16,10 @@
 // product in bf16 at 1230 TFLOP/s, both measured):
 //   - many tokens: the chip's power.  2048 x 4096 x 12288 with silu takes 175-191
 //     us (1080-1180 TFLOP/s); 4096 x 8192 x 8192, two whole rounds of tiles, runs
-//     at 1.93 GHz with the matrix cores busy for 63 % of the cycles; the same kernel on zeros runs a quarter faster,
-//     and deeper buffers, fewer barriers or staging through registers change
-//     nothing.  The two gradients of 2048 x 12288 x 4096 take 350-375 us.
+//     at 1.93 GHz with the matrix cores busy for 63 % of the cycles; on zeros it
+//     runs a quarter faster, and deeper buffers, fewer barriers or staging
+//     through registers change nothing.  The two gradients of 2048 x 12288 x
+//     4096 take 350-375 us.
 //   - few tokens: the read of W.  1 x 4096 x 12288: 21.3 us, 4.7 TB/s; 16 x 12288 x
 //     4096 with residual: 23.3 us, 4.35 TB/s, the second launch 4 us of it.
 //   - small ones: their launches.  333 x 1001 x 777: 14.8 us in two.
