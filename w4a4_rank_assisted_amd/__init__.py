@@ -623,8 +623,15 @@ def _scratch(T, workspace, need, X, dev):
     return workspace, _arg(T, workspace, "workspace", dev, (T.u8,)), workspace.numel()
 
 
+def _fit(what, sizes: int):
+    """Refuses sizes that a C int does not hold, given or-ed together: ctypes
+    keeps their low 32 bits, and the call would work on another shape."""
+    if sizes >> 31:
+        raise HsqError(E_INVAL, what)
+
+
 def linear_workspace_bytes(M: int, K: int, N: int) -> int:
-    return int(_load().hsq_linear_workspace_bytes(M, K, N))
+    return 0 if (M | K | N) >> 31 else int(_load().hsq_linear_workspace_bytes(M, K, N))
 
 
 def _columns(W, X, K: int) -> int:
@@ -651,6 +658,7 @@ def linear(X, W, bias=None, residual=None, *, act: str = "identity", y_dtype=Non
     half = (dt,)
     pw = _arg(T, W, "W", dev, half)
     N = _columns(W, X, K)
+    _fit("hsq_linear", M | K | N)
     if act not in _LINEAR_ACTS:
         raise ValueError(f"act {act!r} not in {sorted(_LINEAR_ACTS)}")
     ydt = dt if y_dtype is None else _y_type(T, y_dtype, dt, (T.f32, dt))
@@ -671,7 +679,7 @@ def linear(X, W, bias=None, residual=None, *, act: str = "identity", y_dtype=Non
 
 
 def linear_backward_workspace_bytes(M: int, K: int, N: int) -> int:
-    return int(_load().hsq_linear_backward_workspace_bytes(M, K, N))
+    return 0 if (M | K | N) >> 31 else int(_load().hsq_linear_backward_workspace_bytes(M, K, N))
 
 
 def linear_backward(dY, X, W, preact=None, *, act: str = "identity", need_input: bool = True,
@@ -689,6 +697,7 @@ def linear_backward(dY, X, W, preact=None, *, act: str = "identity", need_input:
     dt = X.dtype
     pw = _arg(T, W, "W", dev, (dt,))
     N = _columns(W, X, K)
+    _fit("hsq_linear_backward", M | K | N)
     if act not in _LINEAR_ACTS:
         raise ValueError(f"act {act!r} not in {sorted(_LINEAR_ACTS)}")
     py = _arg(T, dY, "dY", dev, (dt, T.f32), (M, N))
@@ -735,6 +744,7 @@ def layer_norm(X, weight=None, bias=None, *, eps: float = 1e-5, y_dtype=None, ou
         pdt = bias.dtype
         if weight is not None and (weight.shape != bias.shape or weight.dtype != pdt):
             raise ValueError("weight and bias differ in shape or type")
+    _fit("hsq_layer_norm", M | C | groups)
     if out is None:
         out = T.empty_like(X) if ydt == xdt else T.empty((M, C), dtype=ydt, device=X.device)
         po = out.data_ptr()
@@ -750,7 +760,7 @@ def layer_norm(X, weight=None, bias=None, *, eps: float = 1e-5, y_dtype=None, ou
 
 
 def layer_norm_backward_workspace_bytes(M: int, C: int, groups: int = 1) -> int:
-    return int(_load().hsq_layer_norm_backward_workspace_bytes(M, C, groups))
+    return 0 if (M | C | groups) >> 31 else int(_load().hsq_layer_norm_backward_workspace_bytes(M, C, groups))
 
 
 def layer_norm_backward(dY, X, mean, rstd, weight=None, *, groups: int = 1, need_input: bool = True,
@@ -775,6 +785,7 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, *, groups: int = 1, need
         if groups not in (1, wg):
             raise ValueError(f"groups {groups} does not go with weight {tuple(weight.shape)}")
         groups, pdt = wg, weight.dtype
+    _fit("hsq_layer_norm_backward", M | C | groups)
     dX = T.empty_like(X) if need_input else None
     dw = db = ps = None
     nbytes = 0
