@@ -63,7 +63,8 @@ extern "C" {
 
 /* ---- status codes ---- */
 #define HSQ_OK            0
-#define HSQ_E_INVAL      -1  /* null pointer, size out of range, bad dtype or kernel choice */
+#define HSQ_E_INVAL      -1  /* null pointer, size out of range, bad dtype or kernel choice; the
+                              * 16-bit linear and the norm: an output over another operand */
 #define HSQ_E_SHAPE      -2  /* K not a positive multiple of 64, or a window outside the matrix */
 #define HSQ_E_ALIGN      -3  /* a pointer is not 16-byte aligned */
 #define HSQ_E_WORKSPACE  -4  /* workspace missing or smaller than the size function returns */
@@ -458,7 +459,8 @@ int hsq_closed_form_l2(const float *HL1, const double *Cinv, int K, int N, int r
  *                  entry do not matter and are clobbered, here as in the
  *                  three functions below: calls in order may share one,
  *                  calls that overlap in time need one each
- * No output may overlap an input, except Y the residual.  Results do not
+ * No output (the workspace among them) may overlap another operand, except Y
+ * the residual, all of it: HSQ_E_INVAL.  Results do not
  * depend on earlier calls or on timing: sums run in a fixed order.
  * Errors: HSQ_E_INVAL, HSQ_E_ALIGN, HSQ_E_WORKSPACE, HSQ_E_HIP. */
 #define HSQ_ACT_GELU       2  /* the 16-bit linear only */
@@ -483,7 +485,8 @@ int hsq_linear(const uint16_t *X, int M, int K, int N, int dtype, const uint16_t
  *   dbias   out: N of `dtype`, or NULL: not wanted
  *   workspace  : ws_bytes >= hsq_linear_backward_workspace_bytes(M, K, N)
  * W may be NULL where dX is, X where dW is; one output at least is wanted.
- * No output may overlap an input.
+ * No output (the workspace among them) may overlap another operand that the
+ * call reads or writes: HSQ_E_INVAL.
  * Errors: HSQ_E_INVAL, HSQ_E_ALIGN, HSQ_E_WORKSPACE, HSQ_E_HIP. */
 size_t hsq_linear_backward_workspace_bytes(int M, int K, int N);
 int hsq_linear_backward(const void *dY, int y_dtype, const uint16_t *X, int M, int K, int N,
@@ -510,6 +513,7 @@ int hsq_linear_backward(const void *dY, int y_dtype, const uint16_t *X, int M, i
  * is HSQ_F32 or y_dtype.  1 <= C <= 16384, groups divides M (HSQ_E_SHAPE)
  * and is at most 65535, M <= 2^25, M * C < 2^31; eps is finite and not
  * negative.
+ * No other output may overlap another operand: HSQ_E_INVAL.
  * Arithmetic is fp32, the variance taken around the finished mean.
  * Errors: HSQ_E_INVAL, HSQ_E_SHAPE, HSQ_E_ALIGN, HSQ_E_HIP. */
 int hsq_layer_norm(const void *X, int x_dtype, int M, int C, int groups, const void *weight,
@@ -528,8 +532,8 @@ int hsq_layer_norm(const void *X, int x_dtype, int M, int C, int groups, const v
  *   dbias    out: groups x C of p_dtype, or NULL: not wanted
  *   workspace   : ws_bytes >= hsq_layer_norm_backward_workspace_bytes(M, C,
  *                 groups) (NULL is fine where neither dweight nor dbias is wanted)
- * One output at least is wanted; no output may overlap an input.  Sums run in
- * a fixed order.
+ * One output at least is wanted; no output (the workspace among them) may
+ * overlap another operand: HSQ_E_INVAL.  Sums run in a fixed order.
  * Errors: HSQ_E_INVAL, HSQ_E_SHAPE, HSQ_E_ALIGN, HSQ_E_WORKSPACE, HSQ_E_HIP. */
 size_t hsq_layer_norm_backward_workspace_bytes(int M, int C, int groups);
 int hsq_layer_norm_backward(const void *dY, int y_dtype, const void *X, int x_dtype, int M, int C,

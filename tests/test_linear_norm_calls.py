@@ -1,5 +1,5 @@
 """Calls of the 16-bit linear and the layer normalisation that the interface
-does not allow, on the host: sizes beyond a C int."""
+does not allow, on the host: sizes beyond a C int, outputs over other operands."""
 
 import pytest
 import torch
@@ -65,3 +65,86 @@ def test_calls_of_sizes_beyond_an_int_are_refused(recorder):
     assert recorder.calls == []
     hsq.linear(meta(4, 8), few)
     assert recorder.calls[-1][0] == "hsq_linear" and recorder.calls[-1][1][1:4] == (4, 8, 16)
+
+
+# ------------------------------------------------------- outputs over other operands
+# Where a call is not refused it reaches the launch, which fails without a GPU
+# (E_HIP); with one the fake addresses must not get that far, so only refused
+# calls run there.
+NO_GPU = not torch.cuda.is_available()
+GAP = 1 << 24          # operands of these sizes are below 2^24 bytes
+
+
+def at(i):
+    return 0x10000000 + i * GAP
+
+
+def _status(fn, args, refused):
+    if not refused and not NO_GPU:
+        pytest.skip("a launch on made-up addresses")
+    st = fn(*args)
+    assert st == (hsq.E_INVAL if refused else hsq.E_HIP)
+
+
+def linear_args(dt=hsq.BF16, ydt=hsq.BF16, M=64, K=256, N=256, **kw):
+    a = dict(X=at(0), W=at(1), bias=at(2), res=at(3), Y=at(4), Z=at(5), ws=at(6))
+    a.update(kw)
+    need = lib.hsq_linear_workspace_bytes(M, K, N)
+    return (a["X"], M, K, N, dt, a["W"], a["bias"], 0, a["res"], a["Y"], ydt, a["Z"], a["ws"], need, None)
+
+
+END = 64 * 256 * 2     # bytes of X, Y, Z and the residual in 16 bits
+
+
+@pytest.mark.parametrize("kw,refused", [
+    (dict(), False), (dict(Y=at(3)), False),                            # all apart; added in place
+    (dict(Y=at(0)), True), (dict(Y=at(1)), True), (dict(Y=at(2) - END + 16), True), (dict(Y=at(5)), True),
+    (dict(Y=at(3) + 16), True), (dict(Y=at(3) - 16), True), (dict(Y=at(3) + END), False), (dict(Y=at(3) - END), False),
+    (dict(Z=at(0)), True), (dict(Z=at(1) + 256 * 256 * 2 - 16), True), (dict(Z=at(1) + 256 * 256 * 2), False),
+    (dict(Z=at(3)), True), (dict(Z=at(3), Y=at(3)), True),
+    (dict(ydt=hsq.F32, Y=at(5) - END), True), (dict(ydt=hsq.F32, Y=at(5) - 2 * END), False),
+    (dict(X=at(1)), False), (dict(res=at(1)), False),                   # two inputs may share memory
+    (dict(M=300, K=2048, N=256, ws=at(4)), True), (dict(M=300, K=2048, N=256, ws=at(1)), True),
+])
+def test_linear_outputs_over_operands(kw, refused):
+    _status(lib.hsq_linear, linear_args(**kw), refused)
+
+
+@pytest.mark.parametrize("kw,refused", [
+    (dict(), False), (dict(dX=at(1)), True), (dict(dX=at(0)), True), (dict(dW=at(2)), True), (dict(dW=at(3)), True),
+    (dict(db=at(0) + 16), True), (dict(dX=at(5)), True), (dict(ws=at(4)), True), (dict(ws=at(0)), True),
+    (dict(dX=None, dW=at(2)), False),      # W is not read without dX
+    (dict(dX=at(3), act=0), False),        # nor Z for the identity
+    (dict(X=at(2)), False),
+])
+def test_linear_backward_outputs_over_operands(kw, refused):
+    a = dict(dY=at(0), X=at(1), W=at(2), Z=at(3), act=1, dX=at(4), dW=at(5), db=at(6), ws=at(7))
+    a.update(kw)
+    need = lib.hsq_linear_backward_workspace_bytes(64, 256, 256)
+    _status(lib.hsq_linear_backward, (a["dY"], hsq.BF16, a["X"], 64, 256, 256, hsq.BF16, a["W"], a["Z"], a["act"],
+                                      a["dX"], a["dW"], a["db"], a["ws"], need, None), refused)
+
+
+@pytest.mark.parametrize("kw,refused", [
+    (dict(), False), (dict(Y=at(0)), False), (dict(xdt=hsq.F32, Y=at(0)), True), (dict(Y=at(0) + 512), True),
+    (dict(Y=at(1)), True), (dict(Y=at(2)), True), (dict(mean=at(5)), True), (dict(mean=at(0)), True),
+    (dict(rstd=at(4) + 240), True), (dict(rstd=at(4) + 256), False), (dict(rstd=at(3)), True), (dict(w=at(2)), False),
+])
+def test_layer_norm_outputs_over_operands(kw, refused):
+    a = dict(X=at(0), xdt=hsq.BF16, w=at(1), b=at(2), Y=at(3), mean=at(4), rstd=at(5))
+    a.update(kw)
+    _status(lib.hsq_layer_norm, (a["X"], a["xdt"], 64, 256, 1, a["w"], a["b"], hsq.F32, 1e-5, a["Y"], hsq.BF16,
+                                 a["mean"], a["rstd"], None), refused)
+
+
+@pytest.mark.parametrize("kw,refused", [
+    (dict(), False), (dict(dX=at(0)), True), (dict(dX=at(1)), True), (dict(dw=at(2)), True), (dict(db=at(3)), True),
+    (dict(dw=at(7)), True), (dict(db=at(4)), True), (dict(ws=at(5)), True), (dict(ws=at(1)), True),
+    (dict(dw=None, db=None, ws=at(1)), False),       # the workspace is not used then
+])
+def test_layer_norm_backward_outputs_over_operands(kw, refused):
+    a = dict(dY=at(0), X=at(1), mean=at(2), rstd=at(3), w=at(4), dX=at(5), dw=at(6), db=at(7), ws=at(8))
+    a.update(kw)
+    need = lib.hsq_layer_norm_backward_workspace_bytes(64, 256, 1)
+    _status(lib.hsq_layer_norm_backward, (a["dY"], hsq.BF16, a["X"], hsq.BF16, 64, 256, 1, a["mean"], a["rstd"],
+                                          a["w"], hsq.F32, a["dX"], a["dw"], a["db"], a["ws"], need, None), refused)

@@ -644,10 +644,10 @@ def linear(X, W, bias=None, residual=None, *, act: str = "identity", y_dtype=Non
            preact_out=None, return_preact: bool = False, workspace=None):
     """Y = act(X W + bias) + residual: X (M, K), W (K, N), bias (N,) bf16 or
     fp16, residual (M, N) of Y's type.  Y is of X's type, or fp32 with
-    y_dtype="f32".  ``out`` may be ``residual`` (added in place).  With
-    preact_out or return_preact the values before the activation are written
-    in X's type, as linear_backward takes them; return_preact returns
-    (Y, Z)."""
+    y_dtype="f32".  ``out`` may be ``residual`` (added in place) and overlaps
+    nothing else (refused).  With preact_out or return_preact the values before
+    the activation are written in X's type, as linear_backward takes them;
+    return_preact returns (Y, Z)."""
     T = _t()
     lib = _load()
     dts = T.code
@@ -725,7 +725,8 @@ def layer_norm(X, weight=None, bias=None, *, eps: float = 1e-5, y_dtype=None, ou
     weight and bias are (C,), or (groups, C) for groups of M / groups
     consecutive rows (the modulated norm: weight = 1 + scale, bias = shift per
     image); both of one type, fp32 or Y's.  Y is of X's type, or for fp32 X
-    of y_dtype.  ``out`` may be X where the types are equal.  return_stats:
+    of y_dtype.  ``out`` may be X where the types are equal, and overlaps
+    nothing else (refused).  return_stats:
     (Y, mean, rstd), fp32 (M,), for layer_norm_backward."""
     T = _t()
     lib = _load()

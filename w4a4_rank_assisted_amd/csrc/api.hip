@@ -9,6 +9,7 @@
 #include <climits>
 #include <cstdlib>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 
 namespace hsq {
@@ -141,6 +142,28 @@ int norm_check(int M, int C, int groups, int x_dtype, int y_dtype, int p_dtype) 
     return HSQ_E_INVAL;
   return M % groups == 0 ? HSQ_OK : HSQ_E_SHAPE;
 }
+
+// Memory of one operand (p may be null).
+struct Span {
+  const void *p;
+  size_t bytes;
+};
+// Whether every operand that a call writes lies apart from all its others:
+// the kernels read their inputs while other workgroups already store.
+bool written_apart(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  auto meet = [](const Span &a, const Span &b) {
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    return x && y && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (const Span *w = written.begin(); w != written.end(); ++w) {
+    for (const Span *o = w + 1; o != written.end(); ++o)
+      if (meet(*w, *o)) return false;
+    for (const Span &r : read)
+      if (meet(*w, r)) return false;
+  }
+  return true;
+}
+size_t type_bytes(int dtype) { return dtype == HSQ_F32 ? 4 : 2; }
 
 size_t workspace_bytes(int M, int K, int N, int r, int batch, int group) {
   if (check_sizes(M, K, N, r, batch) != HSQ_OK || !group_ok(group) || K % group != 0) return 0;
@@ -775,6 +798,10 @@ int hsq_linear(const uint16_t *X, int M, int K, int N, int dtype, const uint16_t
     if (p && !aligned16(p)) return HSQ_E_ALIGN;
   const LinPlan L = plan_linear(M, K, N);
   if (L.total > 0 && (!workspace || ws_bytes < L.total)) return HSQ_E_WORKSPACE;
+  const size_t m = M, k = K, n = N, y_bytes = m * n * type_bytes(y_dtype);
+  if (!written_apart({{Y, y_bytes}, {Z, m * n * 2}, {workspace, L.total}},
+                     {{X, m * k * 2}, {W, k * n * 2}, {bias, n * 2}, {residual == Y ? nullptr : residual, y_bytes}}))
+    return HSQ_E_INVAL;
   char *ws = (char *)workspace;
   hipStream_t s = (hipStream_t)stream;
   LinGemm a{};
@@ -820,6 +847,13 @@ int hsq_linear_backward(const void *dY, int y_dtype, const uint16_t *X, int M, i
     if (p && !aligned16(p)) return HSQ_E_ALIGN;
   const LinPlan L = plan_linear_backward(M, K, N);
   if (ws_bytes < L.total) return HSQ_E_WORKSPACE;
+  const size_t m = M, k = K, n = N;
+  if (!written_apart({{dX, m * k * 2}, {dW, k * n * 2}, {dbias, n * 2}, {workspace, L.total}},
+                     {{dY, m * n * type_bytes(y_dtype)},
+                      {dW ? X : nullptr, m * k * 2},
+                      {dX ? W : nullptr, k * n * 2},
+                      {act == HSQ_ACT_IDENTITY ? nullptr : Z, m * n * 2}}))
+    return HSQ_E_INVAL;
   char *ws = (char *)workspace;
   hipStream_t s = (hipStream_t)stream;
   // dZ is dY itself where nothing changes it: no activation, the operand
@@ -879,6 +913,14 @@ int hsq_layer_norm(const void *X, int x_dtype, int M, int C, int groups, const v
   const void *ptrs[] = {X, weight, bias, Y, mean, rstd};
   for (const void *p : ptrs)
     if (p && !aligned16(p)) return HSQ_E_ALIGN;
+  const size_t m = M, mc = m * C, gc = (size_t)groups * C;
+  // Y over X of its own type: a thread loads its part of a row before it stores it
+  const void *x = X == Y && x_dtype == y_dtype ? nullptr : X;
+  if (!written_apart({{Y, mc * type_bytes(y_dtype)}, {mean, m * 4}, {rstd, m * 4}},
+                     {{x, mc * type_bytes(x_dtype)},
+                      {weight, gc * type_bytes(p_dtype)},
+                      {bias, gc * type_bytes(p_dtype)}}))
+    return HSQ_E_INVAL;
   NormArgs a{};
   a.X = X; a.w = weight; a.b = bias; a.Y = Y; a.mean = mean; a.rstd = rstd;
   a.M = M; a.C = C; a.groups = groups; a.rows = M / groups;
@@ -905,6 +947,17 @@ int hsq_layer_norm_backward(const void *dY, int y_dtype, const void *X, int x_dt
   const bool params = dweight || dbias;
   if (params && (!workspace || ws_bytes < hsq_layer_norm_backward_workspace_bytes(M, C, groups)))
     return HSQ_E_WORKSPACE;
+  const size_t m = M, mc = m * C, g_bytes = (size_t)groups * C * type_bytes(p_dtype);
+  if (!written_apart({{dX, mc * type_bytes(x_dtype)},
+                      {dweight, g_bytes},
+                      {dbias, g_bytes},
+                      {params ? workspace : nullptr, hsq_layer_norm_backward_workspace_bytes(M, C, groups)}},
+                     {{dY, mc * type_bytes(y_dtype)},
+                      {X, mc * type_bytes(x_dtype)},
+                      {mean, m * 4},
+                      {rstd, m * 4},
+                      {weight, g_bytes}}))
+    return HSQ_E_INVAL;
   hipStream_t s = (hipStream_t)stream;
   NormArgs a{};
   a.dY = dY; a.X = X; a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd); a.w = weight;
