@@ -11,6 +11,7 @@ if not torch.cuda.is_available():  # collected on CPU-only hosts, never run ther
 
 import w4a4_rank_assisted_amd as hsq  # noqa: E402
 from exact_sums import operands, same, signs  # noqa: E402
+from linear_cases import DEEP, units  # noqa: E402
 from test_gpu_linear import BACKWARD, FORWARD, LARGE  # noqa: E402
 
 DEV = torch.device("cuda:0")
@@ -49,6 +50,14 @@ def backward(M, K, N, dt, seed):
     # dY in fp32, whose dZ is formed by a pass of its own; the products launched apart
     same(hsq.linear_backward(dY.float(), X, W, need_weight=False, need_bias=False)[0], rX, "dX from fp32")
     same(hsq.linear_backward(dY.float(), X, W, need_input=False, need_bias=False)[1], rW, "dW from fp32")
+
+
+@pytest.mark.parametrize("dt", [BF, F16])
+@pytest.mark.parametrize("M,K,N,product,tiles", DEEP)
+def test_every_kind_of_tile(M, K, N, product, tiles, dt):
+    assert units(M, K, N, product)[0] == tiles
+    say(f"[exact] {product} {tiles}: M={M} K={K} N={N} {dt}")
+    (forward if product == "fwd" else backward)(M, K, N, dt, M + K + N)
 
 
 @pytest.mark.parametrize("M,K,N,dt", [c[:4] for c in FORWARD] + [(*s, BF) for s in DEPTHS])

@@ -355,6 +355,12 @@ hipError_t launch_linear(const LinGemm &a, bool skinny, hipStream_t s);
 // gradient from the partial rows of the preparing launch (at least one).
 hipError_t launch_linear_backward(const LinGemm &dx, const LinGemm &dw, const SumArgs &db, int dtype, hipStream_t s);
 
+// The units that a forward call, or a backward call for both gradients, is
+// launched with, so that the tests can name the tiles a size reaches: skinny,
+// splits, ragged, full, cut, parts for the forward product and zeros, or for
+// dX and for dW (12 values).  Exported, but not part of the interface.
+extern "C" void hsq_internal_linear_units(int M, int K, int N, int backward, int *out);
+
 struct LinDz {
   const void *dY;          // M x N, fp32 or dtype
   int dy_f32;

@@ -1146,6 +1146,25 @@ LinPlan plan_linear_backward(int M, int K, int N) {
   return p;
 }
 
+extern "C" void hsq_internal_linear_units(int M, int K, int N, int backward, int *out) {
+  LinGemm job[2] = {};
+  bool skinny = false;
+  if (backward) {
+    const LinPlan p = plan_linear_backward(M, K, N);
+    job[0].I = M; job[0].J = K; job[0].R = N; job[0].splits = p.splits_dx; job[0].ragged = p.ragged_w;
+    job[1].I = K; job[1].J = N; job[1].R = M; job[1].splits = p.splits_dw; job[1].ragged = p.ragged_x;
+  } else {
+    const LinPlan p = plan_linear(M, K, N);
+    skinny = p.skinny;
+    job[0].I = M; job[0].J = N; job[0].R = K; job[0].splits = p.splits; job[0].ragged = p.ragged_x;
+  }
+  if (!skinny) plan_units(job[0], job[1]);
+  for (const LinGemm &j : job) {
+    const int v[6] = {skinny, j.splits, j.ragged, j.full, j.cut, j.parts};
+    out = std::copy(v, v + 6, out);
+  }
+}
+
 hipError_t launch_linear(const LinGemm &a, bool skinny, hipStream_t s) {
   return a.dtype == kBf16 ? run_forward<kBf16>(a, skinny, s) : run_forward<kF16>(a, skinny, s);
 }
