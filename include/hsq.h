@@ -475,7 +475,10 @@ int hsq_linear(const uint16_t *X, int M, int K, int N, int dtype, const uint16_t
  *   dZ = dY * act'(Z)      dX = dZ W^T      dW = X^T dZ      dbias[n] = sum_m dZ[m,n]
  *
  * (dL/dresidual is dY itself.)  dZ is rounded to `dtype` as the operand of
- * the two products; dbias sums the unrounded dZ.
+ * the two products, an fp32 dY too; dbias sums the unrounded dZ.  In HSQ_F16
+ * a dZ of 2^-25 and less counts as 0 in dX and dW, one below 2^-14 keeps fewer
+ * bits, and one of 65520 and more is infinite: scale the loss by a power of two,
+ * which changes nothing else, to keep it in between.
  *   dY      in : M x N of `y_dtype` (HSQ_F32 or `dtype`)
  *   X, W    in : as for hsq_linear
  *   Z       in : M x N of `dtype`, from hsq_linear (ignored and may be NULL

@@ -72,6 +72,35 @@ def test_backward(M, K, N, dt):
     backward(M, K, N, dt, 3 * M + K + N)
 
 
+@pytest.mark.parametrize("act", ["identity", "silu"])
+def test_range_of_an_fp16_dz(act):
+    """dZ is an fp16 operand of dX and dW, whatever dY's type: what lies outside
+    fp16 is lost there, not in dbias, and a loss scaled by a power of two brings
+    it back."""
+    say(f"[fp16 dZ] {act}")
+    M, K, N = 4096, 96, 136
+    X, W, _, _, dY = operands(generator(3), M, K, N, F16)
+    Z = torch.full((M, N), 100.0, device=DEV, dtype=F16)    # silu' = 1 there, to within 2^-80
+
+    def grads(scale):
+        return hsq.linear_backward(dY.float() * scale, X, W, Z, act=act)
+
+    def check(got, scale):
+        for t, ref in zip(got, (dY.double() @ W.double().t().contiguous(), X.double().t().contiguous() @ dY.double(),
+                                dY.sum(0, dtype=F64))):
+            assert (ref != 0).any() and torch.equal(t, (ref * scale).to(F32).to(F16))
+
+    check(grads(1.0), 1.0)
+    check(grads(2.0 ** -14), 2.0 ** -14)                     # the least normal value
+    check(grads(2.0 ** -24), 2.0 ** -24)                     # the least subnormal one
+    dX, dW, db = grads(2.0 ** -25)                           # half of it: to even, zero
+    assert not dX.any() and not dW.any()
+    same(db.double() * 2.0 ** 24, (dY.sum(0, dtype=F64) / 2).round(), "db")
+    dX, dW, db = grads(65536.0)
+    # every term of a hit row or column is an infinity or NaN
+    assert not torch.isfinite(dX[(dY != 0).any(1)]).any() and not torch.isfinite(dW[:, (dY != 0).any(0)]).any()
+
+
 @pytest.mark.parametrize("M,K,N", LARGE)
 def test_longest_sums(M, K, N):
     """Every output through its row and column sums, some rows and columns one by

@@ -687,7 +687,9 @@ def linear_backward(dY, X, W, preact=None, *, act: str = "identity", need_input:
     """Gradients of ``linear``: dY (M, N) of X's type or fp32, X (M, K), W
     (K, N), preact (M, N) as ``linear`` returned it (not needed for the
     identity).  Returns (dX, dW, dbias) in X's type, None where not needed;
-    the residual's gradient is dY itself."""
+    the residual's gradient is dY itself.  dX and dW are products of dZ =
+    dY act'(Z) rounded to X's type (an fp32 dY too): for fp16 scale the loss so
+    that dZ lies well inside 2^-14 .. 65504."""
     T = _t()
     lib = _load()
     dts = T.code
