@@ -517,7 +517,8 @@ int hsq_linear_backward(const void *dY, int y_dtype, const uint16_t *X, int M, i
  * and is at most 65535, M <= 2^25, M * C < 2^31; eps is finite and not
  * negative.
  * No other output may overlap another operand: HSQ_E_INVAL.
- * Arithmetic is fp32, the variance taken around the finished mean.
+ * Arithmetic is fp32, the variance taken around the finished mean: a row whose
+ * squared differences do not sum within fp32 has rstd 0.
  * Errors: HSQ_E_INVAL, HSQ_E_SHAPE, HSQ_E_ALIGN, HSQ_E_HIP. */
 int hsq_layer_norm(const void *X, int x_dtype, int M, int C, int groups, const void *weight,
                    const void *bias, int p_dtype, float eps, void *Y, int y_dtype, float *mean,

@@ -75,3 +75,20 @@ def test_rows_of_one_value(C, dt):
     close(y, ry, ty, dt, "Y")
     close(mean, rm, tm, F32, "mean")
     close(rstd, rr, tr, F32, "rstd")
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("C", [64, 1152, 4096, 16384])
+def test_rows_beyond_the_range_of_their_squares(C, dt):
+    """Rows of +-2^k: mean 0 and variance 2^2k, whose sum of C leaves fp32 from
+    C 2^2k = 2^128 on.  Then rstd is 0 and y the bias; below, y is w + b or b - w."""
+    say(f"[norm large values] C={C} {dt}")
+    _, w, b, _ = make(C, 2, C, 1, F32, F32, F32)
+    sign = torch.ones(C, device=DEV)
+    sign[1::2] = -1
+    held, beyond = 2.0 ** 56, 2.0 ** 64
+    X = torch.stack([sign * held, sign * beyond, -sign * held]).to(dt)
+    y, mean, rstd = hsq.layer_norm(X, w, b, eps=1e-6, y_dtype=NAME[dt], return_stats=True)
+    assert not mean.any() and rstd.tolist() == [1 / held, 0.0, 1 / held]
+    for row, s in ((0, sign), (1, torch.zeros_like(sign)), (2, -sign)):
+        assert torch.equal(y[row], (s * w + b).to(dt))
