@@ -437,7 +437,9 @@ int hsq_closed_form_l2(const float *HL1, const double *Cinv, int K, int N, int r
 
 /* ---- 16-bit linear layer with bias, activation and residual ----
  * The unquantized form of the layer, for the projections a W4A4 model keeps
- * in 16 bits and for tuning around the quantized ones:
+ * in 16 bits and, with the gradients below, for training those and the norms
+ * (the W4A4 layer itself has no gradient: a backward pass ends there unless the
+ * caller gives the layer's dequantized weight to hsq_linear_backward):
  *
  *   Z[m,n] = sum_k X[m,k] W[k,n] + bias[n]
  *   Y[m,n] = act(Z[m,n]) + residual[m,n]

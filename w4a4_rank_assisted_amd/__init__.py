@@ -7,7 +7,9 @@ anything: if ``_lib/libhsq.so`` is missing or cannot be loaded, every call
 raises.
 
 Half-precision inputs may be passed as torch.bfloat16 / torch.float16
-tensors or as int16 / uint16 tensors holding the bit patterns.
+tensors or as int16 / uint16 tensors holding the bit patterns (the 16-bit
+linear and the layer normalisation, which know both types, take the former
+alone).
 """
 
 from __future__ import annotations

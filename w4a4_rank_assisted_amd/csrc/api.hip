@@ -115,9 +115,11 @@ int calib_sizes(int K) {
 // 16-bit linear: every matrix, its row length rounded up to 8, stays below
 // 2^31 bytes (32-bit buffer offsets).
 constexpr long long kLinMaxElems = 1LL << 30;
-// Widths stay where every launch has fewer than 2^32 threads a dimension (the
-// sum of partial rows runs 32 threads per column); likewise the norm's rows,
-// of which the shortest take a wave each.
+// Widths stay where every launch has fewer than 2^32 threads a dimension, with
+// room to spare: the weight gradient of up to 256 input channels has N / 64
+// workgroups of 512 threads and the bias gradient N / 32.  The norm's rows are counted in 32 bits
+// by kernels that step past the last one by up to 4096; the limit leaves room
+// there too, and for a wave to each.
 constexpr int kLinMaxWidth = 1 << 24;
 constexpr int kNormMaxRows = 1 << 25;
 

@@ -14,9 +14,12 @@
 // Statistics and parameter sums are fp32.
 //
 // Measured on an MI355X (a large copy: 4.92 TB/s): 8192 x 1152 bf16 with
-// parameters per half of the rows, forward 11 us (38 MB; one row alone takes
-// 3 us), backward 18.6 us (57 MB: 18 us, its partial
-// rows 4 us, overlapping); 1537 x 2241 fp32 backward 16 us (35 MB).
+// parameters per half of the rows, forward 11-12 us (38 MB; one row alone takes
+// 3 us), backward 18.6 us a call in a stream of calls (57 MB, 3.1 TB/s; under
+// the tracer its two launches take 18.0 and 3.8); 1537 x 2241 fp32 backward 16
+// us (35 MB).  The backward pass runs eight waves a CU, too few for the memory:
+// its accumulators leave no room for more at these widths.  Rows that do not
+// start on 16 bytes: 8192 x 8191 76 us, 8192 x 8192 48.
 #include "hsq_internal.h"
 
 #include <algorithm>
@@ -137,10 +140,13 @@ constexpr int kRowThreads = 256;   // threads of a workgroup with one or four wa
 template <int W>
 constexpr int norm_threads() { return W > 4 ? W * 64 : kRowThreads; }
 
-// W waves to a row, NV runs of 8 elements to a lane: C <= 512 W NV.  Sixteen
-// waves a CU go from row to row with the next one on its way: 8192 x 8192 bf16
-// 47 us (5.8 TB/s) against 60 with a workgroup per row, 4096 x 2240 fp32 16
-// against 19, 16384 x 1152 18 against 21; 32 waves 52, 17 and 19.
+// W waves to a row, NV runs of 8 elements to a lane: C <= 512 W NV.  A launch
+// has sixteen waves a CU that go from row to row with the next one on its way:
+// 8192 x 8192 bf16 47 us (5.7 TB/s) against 60 with a workgroup per row, 4096 x
+// 2240 fp32 16 against 19, 16384 x 1152 18 against 21; 32 waves 52, 17 and 19.
+// Above 12288 channels, and for fp32 rows above 8192, a lane needs more than 128
+// registers and eight of the waves are resident: the workgroups run in two
+// rounds (4096 x 16384 bf16 54 us, 5.0 TB/s; 2048 x 12288 fp32 42 us, 4.8).
 template <int TX, int TY, int W, int NV>
 __global__ __launch_bounds__(norm_threads<W>()) void k_layer_norm(NormArgs a) {
   constexpr int RPB = norm_threads<W>() / (64 * W);     // rows per workgroup
@@ -369,7 +375,7 @@ __global__ __launch_bounds__(kSumCols * kSumShares) void k_sum_parts(SumArgs a) 
 
 template <int TX, int TY, int W, int NV>
 hipError_t run_norm(const NormArgs &a, bool backward, hipStream_t s) {
-  // forward: sixteen waves a CU, each going from row to row
+  // forward: a grid of sixteen waves a CU, each going from row to row
   constexpr int RPB = norm_threads<W>() / (64 * W), kGrid = 256 * 1024 / norm_threads<W>();
   if (backward)
     hipLaunchKernelGGL((k_layer_norm_bwd<TX, TY, W, NV>), dim3((unsigned)a.parts, (unsigned)a.groups),

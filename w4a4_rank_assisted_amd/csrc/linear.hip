@@ -12,17 +12,23 @@
 // registers by the transposing LDS read.  Few rows (M <= 48) of the forward
 // product stream the weights instead (k_lin_skinny).
 //
-// What bounds them (MI355X; a large copy runs at 4.92 TB/s, a large library
-// product in bf16 at 1230 TFLOP/s, both measured):
-//   - many tokens: the chip's power.  2048 x 4096 x 12288 with silu takes 175-191
-//     us (1080-1180 TFLOP/s); 4096 x 8192 x 8192, two whole rounds of tiles, runs
-//     at 1.93 GHz with the matrix cores busy for 63 % of the cycles; on zeros it
-//     runs a quarter faster, and deeper buffers, fewer barriers or staging
-//     through registers change nothing.  The two gradients of 2048 x 12288 x
-//     4096 take 350-375 us.
-//   - few tokens: the read of W.  1 x 4096 x 12288: 21.3 us, 4.7 TB/s; 16 x 12288 x
-//     4096 with residual: 23.3 us, 4.35 TB/s, the second launch 4 us of it.
-//   - small ones: their launches.  333 x 1001 x 777: 14.8 us in two.
+// What bounds them (MI355X; torch's copy of 2 GiB runs at 4.92 TB/s, its bf16
+// product of 8192^3 at 1230 TFLOP/s; other boxes gave 5.1 and 1330):
+//   - many tokens: power and the feeding of the matrix cores.  2048 x 4096 x 12288
+//     with silu takes 175-191 us (1080-1180 TFLOP/s); 4096 x 8192 x 8192, two
+//     whole rounds of tiles, runs at 1.93 GHz with the matrix cores busy for 63 %
+//     of the cycles and waits in 28 % of the waves' (without loads and LDS reads:
+//     2.10 GHz, 82 % busy); on zeros it runs a quarter faster, and deeper
+//     buffers, fewer barriers or staging through registers change nothing.  The
+//     two gradients of 2048 x 12288 x 4096 take 350-375 us.
+//   - one to 48 tokens forward: the read of W.  1 x 4096 x 12288: 21.3 us, 4.7
+//     TB/s; 16 x 12288 x 4096 with residual: 23.3 us, 4.35 TB/s, the second
+//     launch 4 us of it.
+//   - 49 to some 200 tokens, and the gradients of few rows: tiles of 128 rows for
+//     few of them.  64 x 4096 x 12288: 46 us, gradients of 6 x 8768 x 9471: 192,
+//     two and three times what their bytes take.
+//   - small ones: their launches.  333 x 1001 x 777 in two: 15-15.5 us in bf16
+//     without an epilogue, 16.8 in fp16 with GELU, residual and fp32 Y.
 #include "hsq_internal.h"
 
 #include <algorithm>
@@ -734,7 +740,10 @@ __global__ __launch_bounds__(64 * kSkWaves, 5 - MT) void k_lin_skinny(LinGemm a)
       for (int m = 0; m < MT; ++m) acc[m][j] = mfma<DT>(b, x[m], acc[m][j]);
     }
   };
-  // one run in flight per wave: sixteen waves per CU keep 128 KB on the way
+  // One run of 8 KB in flight per wave.  Two spilled within the 128 registers
+  // that leave room for four workgroups a CU (MT = 1); skinny_splits launches
+  // fewer: 256 workgroups for 16 x 12288 x 4096, four waves and 32 KB a CU, 480
+  // for 1 x 4096 x 12288.
   for (int run = r0 + wave; run < r1; run += kSkWaves) {
     v4u w[8];
     load(run, w);
@@ -798,7 +807,11 @@ __device__ __forceinline__ void pad_rows(const uint16_t *src, int rows, int cols
 }
 
 // dZ = dY act'(Z), rounded to the operand type of the two products, and the
-// column sums of the unrounded dZ over a slice of the rows.  256 columns per
+// column sums of the unrounded dZ over a slice of the rows.  The rounding is
+// what the 16-bit matrix cores take; it puts dX and dW 1.4 times as far from the
+// exact gradient as their own rounding does (2.3e-3 against 1.7e-3 in bf16,
+// 4096 x 1152 x 4608), and a second operand for its rest would double the
+// products' time.  256 columns per
 // workgroup: thread t takes columns 8 (t % 32) .. + 7 of rows t / 32, t / 32 +
 // 8, ... of its slice.
 constexpr int kDzCols = 256, kDzRows = 8;
@@ -930,9 +943,11 @@ int gemm_splits(int I, int J, int R) {
 // Whether a product with rows that are no multiple of 8 reads them as they are
 // (128 x 128 tiles staged through registers, 0.45 us a stage instead of 0.3) or
 // from padded copies of `elems` elements (3.5 us and their way out and back at
-// 4.5 TB/s).  As they are / padded, us: 202 x 1502 x 359 13.6 / 16.6, 333 x 1001 x
-// 777 14.8 / 17.7, gradients of 1500 x 1023 x 1401 33 / 55, of 6 x 8768 x 9471 193 /
-// 223; 80 tiles of an unsplit 4001 63 / 55; many tiles, 4000 x 999 x 3999, 81 / 55.
+// 4.5 TB/s).  As they are / padded, us (no epilogue): 202 x 1502 x 359 13.7 / 16.9,
+// 333 x 1001 x 777 14.8 / 17.9, 900 x 2500 x 1201 26 / 31, 1000 x 4001 x 2001 (128
+// tiles, two splits) 42 / 46, gradients of 6 x 8768 x 9471 192 / 224; the other
+// way, gradients of 1500 x 1023 x 1401 36 / 31 and many tiles, 4000 x 999 x 3999,
+// 81 / 54.
 bool reads_ragged(int I, int J, int R, long long elems) {
   return quarters(I, J) <= kCus / 2 && 0.15f / 32 * R / gemm_splits(I, J, R) <= 3.5f + 4.0f / 4.5e6f * elems;
 }
@@ -1027,7 +1042,7 @@ void plan_units(LinGemm &a, LinGemm &b) {
 }
 
 // Splits of K of the weight-streaming kernel: the fewest whose workgroups
-// fill nine tenths of whole rounds over the CUs, at least 256 of K each.
+// fill nine tenths of whole rounds of one a CU, at least 256 of K each.
 // 1 x 4096 x 12288 (96 strips): 5 splits 22.1 us, 4 and 8 22.4, 3 25.8; 16 x
 // 12288 x 4096 (32 strips): 8 splits 23.6 us, 16 24.9, 12 26.8.
 int skinny_splits(int J, int K) {
