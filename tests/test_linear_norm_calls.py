@@ -104,6 +104,7 @@ END = 64 * 256 * 2     # bytes of X, Y, Z and the residual in 16 bits
     (dict(Z=at(3)), True), (dict(Z=at(3), Y=at(3)), True),
     (dict(ydt=hsq.F32, Y=at(5) - END), True), (dict(ydt=hsq.F32, Y=at(5) - 2 * END), False),
     (dict(X=at(1)), False), (dict(res=at(1)), False),                   # two inputs may share memory
+    (dict(ws=at(0) + 16), False),                                       # no workspace is needed here
     (dict(M=300, K=2048, N=256, ws=at(4)), True), (dict(M=300, K=2048, N=256, ws=at(1)), True),
 ])
 def test_linear_outputs_over_operands(kw, refused):

@@ -117,9 +117,9 @@ int calib_sizes(int K) {
 constexpr long long kLinMaxElems = 1LL << 30;
 // Widths stay where every launch has fewer than 2^32 threads a dimension, with
 // room to spare: the weight gradient of up to 256 input channels has N / 64
-// workgroups of 512 threads and the bias gradient N / 32.  The norm's rows are counted in 32 bits
-// by kernels that step past the last one by up to 4096; the limit leaves room
-// there too, and for a wave to each.
+// workgroups of 512 threads and the bias gradient N / 32.  The norm's rows are
+// counted in 32 bits by kernels that step past the last one by up to 4096; the
+// limit leaves room there too, and for a wave to each.
 constexpr int kLinMaxWidth = 1 << 24;
 constexpr int kNormMaxRows = 1 << 25;
 
@@ -145,7 +145,7 @@ int norm_check(int M, int C, int groups, int x_dtype, int y_dtype, int p_dtype) 
   return M % groups == 0 ? HSQ_OK : HSQ_E_SHAPE;
 }
 
-// Memory of one operand (p may be null).
+// Memory of one operand (none where p is null or bytes 0).
 struct Span {
   const void *p;
   size_t bytes;
@@ -155,7 +155,7 @@ struct Span {
 bool written_apart(std::initializer_list<Span> written, std::initializer_list<Span> read) {
   auto meet = [](const Span &a, const Span &b) {
     const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-    return x && y && x < y + b.bytes && y < x + a.bytes;
+    return x && y && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
   };
   for (const Span *w = written.begin(); w != written.end(); ++w) {
     for (const Span *o = w + 1; o != written.end(); ++o)
