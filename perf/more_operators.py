@@ -297,7 +297,7 @@ def prepare(case, seed):
             cu = torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
             hsq.kv_cache_write(k, v, s["cache"], table, s["lens"], cu, quant=c["quant"], max_tokens=max(lens))
         if c["op"] == "attention":
-            need = hsq.kv_attention_workspace_bytes(s["Q"].shape[0], c["Hq"], H, D, B, max(queries),
+            need = hsq.kv_attention_workspace_bytes(s["Q"].shape[0], c["Hq"], H, D, B, c["q"],
                                                     table.shape[1] * page)
             s["workspace"] = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
         return s
