@@ -65,7 +65,8 @@ extern "C" {
 #define HSQ_OK            0
 #define HSQ_E_INVAL      -1  /* null pointer, size out of range, bad dtype or kernel choice; the
                               * 16-bit linear and the norm: an output over another operand */
-#define HSQ_E_SHAPE      -2  /* K not a positive multiple of 64, or a window outside the matrix */
+#define HSQ_E_SHAPE      -2  /* K not a positive multiple of 64, a window outside the matrix, sizes
+                              * that do not divide or that no kernel has (the 4-bit cache) */
 #define HSQ_E_ALIGN      -3  /* a pointer is not 16-byte aligned */
 #define HSQ_E_WORKSPACE  -4  /* workspace missing or smaller than the size function returns */
 #define HSQ_E_HIP        -5  /* the HIP runtime refused a launch */
@@ -75,7 +76,8 @@ extern "C" {
 /* ---- output dtypes ---- */
 #define HSQ_F32   0
 #define HSQ_BF16  1
-#define HSQ_F16   2  /* the 16-bit linear and the layer normalisation only */
+#define HSQ_F16   2  /* the 16-bit linear, the layer normalisation, the layer with 16-bit
+                      * activations and the 4-bit cache only */
 
 /* ---- kernel choice for the residual contraction ---- */
 #define HSQ_KERNEL_AUTO    0  /* SKINNY for M <= 64, TILED otherwise */
@@ -546,6 +548,135 @@ int hsq_layer_norm_backward(const void *dY, int y_dtype, const void *X, int x_dt
                             int groups, const float *mean, const float *rstd, const void *weight,
                             int p_dtype, void *dX, void *dweight, void *dbias, void *workspace,
                             size_t ws_bytes, void *stream);
+
+/* ---- the layer with its activations left in 16 bits, for few tokens ----
+ * The same weights (packed residual, scales, lambda, L1, L2, bias) under
+ * activations that are not quantized: the weight-only form, for decoding,
+ * where the read of the weights is all that counts.
+ *
+ *   xh[m,k] = X[m,k] / lambda[k]
+ *   Y[m,n]  = sum_g sw[g,n] sum_{k in g} xh[m,k] qw[k,n]
+ *             + sum_j (sum_k xh[m,k] L1[k,j]) L2[j,n] + bias[n] + residual[m,n]
+ *
+ *   X         in : M x K of `dtype` (HSQ_BF16 or HSQ_F16), 1 <= M <= 64
+ *   group        : 64 or 128, divides K
+ *   lambda    in : K fp16, or NULL: 1
+ *   packed_w  in : batch blobs of hsq_pack_weights, back to back
+ *   sw        in : batch x K/group x N fp16
+ *   L1, L2    in : batch x K x r and batch x r x N of `dtype` (NULL where r = 0)
+ *   bias      in : batch x N of `dtype`, or NULL
+ *   residual  in : batch x M x N of `y_dtype`, or NULL; may be Y itself
+ *   Y         out: batch x M x N of `y_dtype`, which is HSQ_F32 or `dtype`
+ *   workspace    : ws_bytes >= hsq_w4a16_workspace_bytes(M, K, N, r, batch,
+ *                  group, lambda != NULL, y_dtype) device bytes (NULL is fine
+ *                  where that is 0); its contents on entry do not matter, and
+ *                  calls that overlap in time need one each
+ * Products and sums are fp32, rounded once at the store.  With lambda, xh enters
+ * the residual's product as fp16 numbers under a power of two per row and group:
+ * 11 bits where Y is bf16, 22 bits where it is fp16 or fp32.  A row of xh that
+ * holds an infinity or a NaN gives NaN; one whose 31 |xh| do not sum within
+ * fp32 over a group may.  Sizes as for the linear (K % 64, r, batch), with
+ * M * K, M * N, K * N < 2^31.  No output (the workspace among them) may overlap
+ * another operand, except Y the residual, all of it: HSQ_E_INVAL.
+ * Errors: HSQ_E_INVAL, HSQ_E_SHAPE, HSQ_E_ALIGN, HSQ_E_WORKSPACE, HSQ_E_HIP. */
+#define HSQ_W4A16_MAX_M 64
+size_t hsq_w4a16_workspace_bytes(int M, int K, int N, int r, int batch, int group, int smooth, int y_dtype);
+int hsq_w4a16_lowrank_linear(const uint16_t *X, int M, int K, int N, int batch, int group, int dtype,
+                             const uint16_t *lambda, const uint8_t *packed_w, const uint16_t *sw,
+                             const uint16_t *L1, const uint16_t *L2, int r, const uint16_t *bias,
+                             const void *residual, void *Y, int y_dtype, void *workspace,
+                             size_t ws_bytes, void *stream);
+
+/* ---- key / value cache in 4 bits ----
+ * Keys and values of a decoder's attention, quantized as they are written.  Per
+ * token, head and group of 64 channels x:
+ *
+ *   HSQ_AQ_ASYMMETRIC  lo = min(0, min x), hi = max(0, max x)
+ *                      s = fp16_rne((hi - lo) / 15), z = clamp(rint(-lo / s), 0, 15)
+ *                      n = clamp(rint(x / s) + z, 0, 15)
+ *   HSQ_AQ_SYMMETRIC   s = fp16_rne(max |x| / 7), z = 8
+ *                      n = clamp(rint(x / s), -8, 7) + 8
+ *
+ * and the value held is s (n - z).  The quotients are those of the real numbers,
+ * ties to even; s saturates at 65504, and s = 0 holds zeros; a group with an
+ * infinity or a NaN holds NaN.
+ *
+ * The cache is a device buffer of num_pages pages of hsq_kv_page_bytes(
+ * page_size, kv_heads, head_dim) bytes, 16-byte aligned, in a layout of the
+ * library's own (it can be copied page by page).  head_dim is 64, 128 or 256;
+ * page_size, in tokens, a power of two from 32 to 2^20.  Every call says where the
+ * sequences lie by
+ *   block_table in : batch x table_width int32, position t of sequence b is on
+ *                    page block_table[b][t / page_size]
+ *   kv_lens     in : batch int32, tokens of each sequence, the call's own included
+ *   cu_tokens   in : batch + 1 int32, sequence b's rows of the call are
+ *                    [cu_tokens[b], cu_tokens[b+1]) of T; or NULL: T / batch rows
+ *                    each.  Its n rows are positions kv_lens[b] - n and on.
+ *   max_tokens     : no sequence has more rows (ignored where cu_tokens is NULL);
+ *                    rows beyond it are left alone
+ * (these three arrays are 4-byte aligned).  They are read on the device only, and
+ * whatever they hold, no access leaves the operands: a position that is
+ * negative, at or past table_width * page_size, or on a page that is not in [0,
+ * num_pages), is not there: it is not written, reads back as 0, and takes no part
+ * in the attention.  Rows of no sequence are left as they were.  Two rows of one
+ * call must not be written to the same place (a page named twice).
+ * Limits: batch <= 65535, heads <= 4096, T <= 2^24, table_width * page_size <=
+ * 2^30, and launches of fewer than 2^23 workgroups: HSQ_E_INVAL.  Strides are in elements from
+ * row to row, multiples of 8 and no less than a dense row; the heads of a row are
+ * dense. */
+size_t hsq_kv_page_bytes(int page_size, int kv_heads, int head_dim);
+
+/* Writes T rows of keys and values (T x kv_heads x head_dim, HSQ_BF16 or HSQ_F16,
+ * row strides k_stride and v_stride) into the cache.  quant is HSQ_AQ_SYMMETRIC or
+ * HSQ_AQ_ASYMMETRIC; a cache may hold both.  The cache may not overlap K or V.
+ * Errors: HSQ_E_INVAL, HSQ_E_SHAPE (head_dim, page_size, T not a multiple of
+ * batch where cu_tokens is NULL, a stride), HSQ_E_ALIGN, HSQ_E_HIP. */
+int hsq_kv_cache_write(const uint16_t *K, int k_stride, const uint16_t *V, int v_stride, int T, int dtype,
+                       int kv_heads, int head_dim, int quant, uint8_t *cache, int num_pages, int page_size,
+                       const int32_t *block_table, int table_width, const int32_t *kv_lens,
+                       const int32_t *cu_tokens, int batch, int max_tokens, void *stream);
+
+/* Reads back the values held of the rows that a write with the same arguments
+ * writes (any stretch of a sequence: kv_lens is where it ends): K and V, T x
+ * kv_heads x head_dim dense, of dtype HSQ_F32, HSQ_BF16 or HSQ_F16, one rounding.
+ * Neither may overlap the other or the cache.  Errors as hsq_kv_cache_write. */
+int hsq_kv_cache_read(const uint8_t *cache, int num_pages, int page_size, int kv_heads, int head_dim,
+                      const int32_t *block_table, int table_width, const int32_t *kv_lens,
+                      const int32_t *cu_tokens, int batch, int T, int max_tokens, void *K, void *V,
+                      int dtype, void *stream);
+
+/* Attention of T query rows over the cache:
+ *
+ *   e[i,t] = scale q_i . k_t        y_i = sum_t exp(e[i,t]) v_t / sum_t exp(e[i,t])
+ *   lse[i] = log sum_t exp(e[i,t])
+ *
+ * per query head h, over head h / (q_heads / kv_heads) of the cache.  Row i of a
+ * sequence's n is at position kv_lens[b] - n + i and sees, with causal = 1, the
+ * tokens that are not after it and, where window > 0, less than window before it;
+ * with causal = 0 (window 0) all kv_lens[b] tokens.  A row that sees nothing is 0
+ * with lse = -infinity; what it does not see has no part in it, NaN either.
+ *   Q       in : T x q_heads x head_dim of `dtype` (HSQ_BF16 or HSQ_F16), row
+ *                stride q_stride
+ *   scale      : positive, 1e30 at most
+ *   Y       out: T x q_heads x head_dim dense of y_dtype (HSQ_F32 or `dtype`)
+ *   lse     out: T x q_heads fp32, or NULL
+ *   workspace  : ws_bytes >= hsq_kv_attention_workspace_bytes(T, q_heads,
+ *                kv_heads, head_dim, batch, max_tokens, table_width * page_size)
+ *                device bytes (NULL is fine where that is 0); contents do not
+ *                matter; calls that overlap in time need one each
+ * (max_tokens is T / batch where cu_tokens is NULL.)  The scores are fp32; exp(e)
+ * times a value's scale is rounded to 11 bits for a 16-bit Y, to 22 for fp32.
+ * Results do not depend on timing: sums run in a fixed order.  No output (the
+ * workspace among them) may overlap another operand: HSQ_E_INVAL.
+ * Errors: HSQ_E_INVAL, HSQ_E_SHAPE (as above, or kv_heads does not divide
+ * q_heads), HSQ_E_ALIGN, HSQ_E_WORKSPACE, HSQ_E_HIP. */
+size_t hsq_kv_attention_workspace_bytes(int T, int q_heads, int kv_heads, int head_dim, int batch,
+                                        int max_tokens, int capacity);
+int hsq_kv_attention(const uint16_t *Q, int q_stride, int T, int dtype, int q_heads, const uint8_t *cache,
+                     int num_pages, int page_size, int kv_heads, int head_dim, const int32_t *block_table,
+                     int table_width, const int32_t *kv_lens, const int32_t *cu_tokens, int batch,
+                     int max_tokens, float scale, int causal, int window, void *Y, int y_dtype, float *lse,
+                     void *workspace, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }

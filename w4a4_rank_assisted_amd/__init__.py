@@ -8,8 +8,8 @@ raises.
 
 Half-precision inputs may be passed as torch.bfloat16 / torch.float16
 tensors or as int16 / uint16 tensors holding the bit patterns (the 16-bit
-linear and the layer normalisation, which know both types, take the former
-alone).
+linear, the layer normalisation, the layer with 16-bit activations and the
+4-bit cache, which know both types, take the former alone).
 """
 
 from __future__ import annotations
@@ -100,6 +100,14 @@ def _load():
             "hsq_layer_norm": ([P, I, I, I, I, P, P, I, ctypes.c_float, P, I, P, P, P], I),
             "hsq_layer_norm_backward_workspace_bytes": ([I, I, I], S),
             "hsq_layer_norm_backward": ([P, I, P, I, I, I, I, P, P, P, I, P, P, P, P, S, P], I),
+            "hsq_w4a16_workspace_bytes": ([I, I, I, I, I, I, I, I], S),
+            "hsq_w4a16_lowrank_linear": ([P, I, I, I, I, I, I, P, P, P, P, P, I, P, P, P, I, P, S, P], I),
+            "hsq_kv_page_bytes": ([I, I, I], S),
+            "hsq_kv_cache_write": ([P, I, P, I, I, I, I, I, I, P, I, I, P, I, P, P, I, I, P], I),
+            "hsq_kv_cache_read": ([P, I, I, I, I, P, I, P, P, I, I, I, P, P, I, P], I),
+            "hsq_kv_attention_workspace_bytes": ([I, I, I, I, I, I, I], S),
+            "hsq_kv_attention": ([P, I, I, I, I, P, I, I, I, I, P, I, P, P, I, I, ctypes.c_float, I, I, P, I, P, P, S,
+                                  P], I),
             "hsq_closed_form_l2": ([P, P, I, I, I, I, P, P, P, P, P, S, P], I),
         }
         for name, (args, res) in sig.items():
@@ -377,7 +385,19 @@ class Layer:
                 workspace_bytes(max_tokens, self.K, self.N, self.r, self.batch, group),
                 dtype=torch.uint8, device=qw.device)
 
-    def __call__(self, X, y_dtype: str = "bf16", out=None, kernel: str = "auto"):
+    def __call__(self, X, y_dtype: str = "bf16", out=None, kernel: str = "auto", weight_only: bool = False,
+                 residual=None):
+        """Y (batch, M, N) on the current stream.  weight_only leaves the
+        activations in 16 bits (w4a16_lowrank_linear, M <= 64), the form for
+        decoding single tokens; it may add a residual, and has one kernel."""
+        if weight_only:
+            need = w4a16_workspace_bytes(X.shape[0], self.K, self.N, self.r, self.batch, self.group, True, y_dtype)
+            ws = self.workspace if self.workspace is not None and self.workspace.numel() >= need else None
+            return w4a16_lowrank_linear(X, self.packed, self.sw, self.lam, self.L1, self.L2, self.bias, residual,
+                                        N=self.N, batch=self.batch, group=self.group, y_dtype=y_dtype, out=out,
+                                        workspace=ws)
+        if residual is not None:
+            raise ValueError("residual goes with weight_only")
         ws = self.workspace
         need = workspace_bytes(X.shape[0], self.K, self.N, self.r, self.batch, self.group)
         if ws is None or ws.numel() < need:
@@ -557,10 +577,11 @@ class _Torch:
     def __init__(self):
         torch = _torch()
         self.Tensor, self.empty, self.empty_like = torch.Tensor, torch.empty, torch.empty_like
-        self.f32, self.u8 = torch.float32, torch.uint8
+        self.f32, self.u8, self.i32 = torch.float32, torch.uint8, torch.int32
         self.named = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
         self.code = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
         self.half = (torch.bfloat16, torch.float16)
+        self.scales = (torch.float16, torch.int16, torch.uint16)
         self.any = (torch.float32, torch.bfloat16, torch.float16)
         self.current_device = torch._C._cuda_getDevice
         self.stream = torch._C._cuda_getCurrentRawStream   # see _stream
@@ -802,3 +823,226 @@ def layer_norm_backward(dY, X, mean, rstd, weight=None, *, groups: int = 1, need
     _check(lib.hsq_layer_norm_backward(py, dts[dY.dtype], px, dts[xdt], M, C, groups, pm, pr, pw, dts[pdt], _ptr(dX),
                                        _ptr(dw), _ptr(db), ps, nbytes, T.stream(dev)), "hsq_layer_norm_backward")
     return dX, dw, db
+
+
+# ------------------------------------------- the layer with 16-bit activations
+W4A16_MAX_M = 64
+
+
+def w4a16_workspace_bytes(M: int, K: int, N: int, r: int = 0, batch: int = 1, group: int = 64,
+                          smooth: bool = False, y_dtype: str = "f32") -> int:
+    """Workspace of w4a16_lowrank_linear.  smooth: a lambda is given.  That of
+    y_dtype "f32" is enough for every output type."""
+    if (M | K | N | r | batch | group) >> 31:
+        return 0
+    return int(_load().hsq_w4a16_workspace_bytes(M, K, N, r, batch, group, int(bool(smooth)),
+                                                 {"f32": F32, "bf16": BF16, "f16": F16}[y_dtype]))
+
+
+def w4a16_lowrank_linear(X, packed_w, sw, lam=None, L1=None, L2=None, bias=None, residual=None, *, N: int,
+                         batch: int = 1, group: int = 64, y_dtype=None, out=None, workspace=None):
+    """The layer with its activations left in 16 bits, for up to 64 tokens:
+    Y[b] = (X / lam) (deq(packed_w[b], sw[b]) + L1[b] L2[b]) + bias[b] + residual[b].
+    X (M, K) bf16 or fp16; packed_w (batch * blob,) of pack_weights; sw (batch,
+    K/group, N) fp16; lam (K,) fp16 or None; L1 (batch, K, r), L2 (batch, r, N),
+    bias (batch, N) of X's type; residual (batch, M, N) of Y's type, which may be
+    ``out``.  Y (batch, M, N) is of X's type, or fp32 with y_dtype="f32"."""
+    T = _t()
+    lib = _load()
+    dts = T.code
+    dev = _device(T, X, "X")
+    px = _arg(T, X, "X", dev, T.half)
+    M, K = X.shape
+    dt = X.dtype
+    half = (dt,)
+    _fit("hsq_w4a16_lowrank_linear", M | K | N | batch | group)
+    if group not in (64, 128):
+        raise ValueError(f"group {group} is not 64 or 128")
+    pw = _arg(T, packed_w, "packed_w", dev, (T.u8,), (batch * lib.hsq_packed_weight_bytes(K, N),))
+    ps = _arg(T, sw, "sw", dev, T.scales, (batch, K // group, N))
+    pl = None if lam is None else _arg(T, lam, "lam", dev, T.scales, (K,))
+    r, p1, p2 = 0, None, None
+    if L1 is not None:
+        r = L1.shape[-1]
+        if r:
+            p1 = _arg(T, L1, "L1", dev, half, (batch, K, r))
+            p2 = _arg(T, L2, "L2", dev, half, (batch, r, N))
+    pb = None if bias is None else _arg(T, bias, "bias", dev, half, (batch, N))
+    ydt = dt if y_dtype is None else _y_type(T, y_dtype, dt, (T.f32, dt))
+    pr = None if residual is None else _arg(T, residual, "residual", dev, (ydt,), (batch, M, N))
+    if out is None:
+        out = T.empty((batch, M, N), dtype=ydt, device=X.device)
+        po = out.data_ptr()
+    else:
+        po = _arg(T, out, "out", dev, (ydt,), (batch, M, N))
+    nbytes = pws = None
+    if lam is None and not r:
+        workspace, pws, nbytes = None, None, 0          # nothing to prepare
+    else:
+        workspace, pws, nbytes = _scratch(
+            T, workspace, lambda: lib.hsq_w4a16_workspace_bytes(M, K, N, r, batch, group, int(lam is not None),
+                                                                dts[ydt]), X, dev)
+    _check(lib.hsq_w4a16_lowrank_linear(px, M, K, N, batch, group, dts[dt], pl, pw, ps, p1, p2, r, pb, pr, po, dts[ydt],
+                                        pws, nbytes, T.stream(dev)), "hsq_w4a16_lowrank_linear")
+    return out
+
+
+# ------------------------------------------------ key / value cache in 4 bits
+KV_TILE = 32
+
+
+def kv_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
+    if (page_size | kv_heads | head_dim) >> 31:
+        return 0
+    return int(_load().hsq_kv_page_bytes(page_size, kv_heads, head_dim))
+
+
+def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device=None):
+    """An empty cache, (num_pages, kv_heads, bytes of a head's page) uint8 zeros on
+    the current device: the shape tells the calls below its heads and page size."""
+    torch = _torch()
+    n = kv_page_bytes(page_size, kv_heads, head_dim)
+    if n == 0 or num_pages < 1:
+        raise HsqError(E_SHAPE, "kv_cache")
+    return torch.zeros((num_pages, kv_heads, n // kv_heads), dtype=torch.uint8,
+                       device="cuda" if device is None else device)
+
+
+def _kv_where(T, cache, head_dim: int, block_table, kv_lens, cu_tokens, dev):
+    """(cache pointer, pages, heads, page size, table pointer, width, lens pointer, cu pointer, batch)."""
+    pc = _arg(T, cache, "cache", dev, (T.u8,))
+    if cache.dim() != 3:
+        raise ValueError(f"cache: shape {tuple(cache.shape)} is not that of kv_cache")
+    tile = kv_page_bytes(KV_TILE, 1, head_dim)
+    if tile == 0:
+        raise HsqError(E_SHAPE, f"head_dim {head_dim}")
+    pages, heads, n = cache.shape
+    if n == 0 or n % tile:
+        raise ValueError(f"cache: {n} bytes a head are no pages of head_dim {head_dim}")
+    pt = _arg(T, block_table, "block_table", dev, (T.i32,))
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table: shape {tuple(block_table.shape)} is not (batch, pages)")
+    batch, width = block_table.shape
+    pl = _arg(T, kv_lens, "kv_lens", dev, (T.i32,), (batch,))
+    pq = None if cu_tokens is None else _arg(T, cu_tokens, "cu_tokens", dev, (T.i32,), (batch + 1,))
+    return pc, pages, heads, n // tile * KV_TILE, pt, width, pl, pq, batch
+
+
+def _token_rows(T, t, name, dev, dtypes, shape):
+    """(T, heads, head_dim) rows whose heads are dense, at any distance of a
+    multiple of 8 elements (a slice of a joint projection) -> (pointer, stride)."""
+    if not isinstance(t, T.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on HIP device {dev}, the current device and that of the other operands")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
+    if t.dim() != 3 or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}")
+    n, h, d = t.shape
+    st = t.stride()
+    dense = h * d
+    if (d > 1 and st[2] != 1) or (h > 1 and st[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    row = st[0] if n > 1 else dense
+    if row < dense or row % 8:
+        raise ValueError(f"{name}: {row} elements from token to token, not a multiple of 8 from {dense} on")
+    return t.data_ptr(), row
+
+
+def kv_cache_write(K, V, cache, block_table, kv_lens, cu_tokens=None, *, quant: str = "asym", max_tokens=None):
+    """Quantises keys and values (T, kv_heads, head_dim), bf16 or fp16, into the
+    cache (in place).  Sequence b's tokens are rows cu_tokens[b] .. cu_tokens[b+1]
+    (int32, None: T / batch each) and its last positions: kv_lens[b] (int32) counts
+    them already.  block_table (batch, pages) int32.  max_tokens: no sequence has
+    more rows (None: T).  quant "asym" or "sym".  K and V may be slices of one
+    joint projection."""
+    T = _t()
+    lib = _load()
+    dev = _device(T, K, "K")
+    D = K.shape[-1]
+    pc, pages, heads, page, pt, width, pl, pq, batch = _kv_where(T, cache, D, block_table, kv_lens, cu_tokens, dev)
+    pk, ks = _token_rows(T, K, "K", dev, T.half, (None, heads, D))
+    n = K.shape[0]
+    pv, vs = _token_rows(T, V, "V", dev, (K.dtype,), (n, heads, D))
+    if quant not in _ACT_QUANT:
+        raise ValueError(f"quant {quant!r} is not 'asym' or 'sym'")
+    top = n if max_tokens is None else max_tokens
+    _fit("hsq_kv_cache_write", n | heads | pages | page | width | batch | top | ks | vs)
+    _check(lib.hsq_kv_cache_write(pk, ks, pv, vs, n, T.code[K.dtype], heads, D, _ACT_QUANT[quant], pc, pages, page, pt,
+                                  width, pl, pq, batch, top, T.stream(dev)), "hsq_kv_cache_write")
+
+
+def kv_cache_read(cache, block_table, kv_lens, cu_tokens=None, *, tokens: int, head_dim: int, dtype: str = "bf16",
+                  max_tokens=None, out=None):
+    """The values held of ``tokens`` rows, as kv_cache_write takes them: (K, V), each
+    (tokens, kv_heads, head_dim) of dtype.  Rows of no sequence are left as they
+    were (out=(K, V)) or undefined."""
+    T = _t()
+    lib = _load()
+    dev = _device(T, cache, "cache")
+    pc, pages, heads, page, pt, width, pl, pq, batch = _kv_where(T, cache, head_dim, block_table, kv_lens, cu_tokens,
+                                                                 dev)
+    if dtype not in T.named:
+        raise ValueError(f"dtype {dtype!r} is not 'f32', 'bf16' or 'f16'")
+    dt = T.named[dtype]
+    shape = (tokens, heads, head_dim)
+    top = tokens if max_tokens is None else max_tokens
+    _fit("hsq_kv_cache_read", tokens | heads | pages | page | width | batch | top)
+    if out is None:
+        K = T.empty(shape, dtype=dt, device=cache.device)
+        V = T.empty_like(K)
+    else:
+        K, V = out
+    pk, pv = _arg(T, K, "K", dev, (dt,), shape), _arg(T, V, "V", dev, (dt,), shape)
+    _check(lib.hsq_kv_cache_read(pc, pages, page, heads, head_dim, pt, width, pl, pq, batch, tokens, top, pk, pv,
+                                 T.code[dt], T.stream(dev)), "hsq_kv_cache_read")
+    return K, V
+
+
+def kv_attention_workspace_bytes(tokens: int, q_heads: int, kv_heads: int, head_dim: int, batch: int,
+                                 max_tokens: int, capacity: int) -> int:
+    """Workspace of kv_attention.  capacity: tokens a row of the block table has
+    pages for; max_tokens as in the call (tokens / batch without cu_tokens)."""
+    if (tokens | q_heads | kv_heads | head_dim | batch | max_tokens | capacity) >> 31:
+        return 0
+    return int(_load().hsq_kv_attention_workspace_bytes(tokens, q_heads, kv_heads, head_dim, batch, max_tokens,
+                                                        capacity))
+
+
+def kv_attention(Q, cache, block_table, kv_lens, cu_tokens=None, *, scale=None, causal: bool = True,
+                 window: int = 0, y_dtype=None, out=None, return_lse: bool = False, max_tokens=None,
+                 workspace=None):
+    """Attention of Q (T, q_heads, head_dim), bf16 or fp16, over the cache, whose
+    heads each serve q_heads / kv_heads query heads.  Rows, lengths and pages as in
+    kv_cache_write: query i of a sequence's n is its token kv_lens[b] - n + i.
+    causal: it sees no later token, and with window > 0 only less than window
+    back; otherwise all kv_lens[b].  scale: head_dim ** -0.5 unless given.  Y is of
+    Q's type, or fp32 with y_dtype="f32"; return_lse: (Y, log of the sums of exp,
+    (T, q_heads) fp32).  Q may be a slice of a joint projection."""
+    T = _t()
+    lib = _load()
+    dts = T.code
+    dev = _device(T, Q, "Q")
+    D = Q.shape[-1]
+    pc, pages, heads, page, pt, width, pl, pq, batch = _kv_where(T, cache, D, block_table, kv_lens, cu_tokens, dev)
+    px, qs = _token_rows(T, Q, "Q", dev, T.half, (None, None, D))
+    n, q_heads, _ = Q.shape
+    dt = Q.dtype
+    ydt = dt if y_dtype is None else _y_type(T, y_dtype, dt, (T.f32, dt))
+    top = n if max_tokens is None else max_tokens
+    _fit("hsq_kv_attention", n | q_heads | heads | pages | page | width | batch | top | qs | window)
+    if out is None:
+        out = T.empty((n, q_heads, D), dtype=ydt, device=Q.device)
+        po = out.data_ptr()
+    else:
+        po = _arg(T, out, "out", dev, (ydt,), (n, q_heads, D))
+    lse = T.empty((n, q_heads), dtype=T.f32, device=Q.device) if return_lse else None
+    each = max(1, n // batch) if pq is None and batch else top
+    workspace, ps, nbytes = _scratch(
+        T, workspace, lambda: lib.hsq_kv_attention_workspace_bytes(n, q_heads, heads, D, batch, each,
+                                                                   min(width * page, 1 << 30)), Q, dev)
+    _check(lib.hsq_kv_attention(px, qs, n, dts[dt], q_heads, pc, pages, page, heads, D, pt, width, pl, pq, batch, top,
+                                D ** -0.5 if scale is None else scale, int(bool(causal)), window, po, dts[ydt],
+                                _ptr(lse), ps, nbytes, T.stream(dev)), "hsq_kv_attention")
+    return (out, lse) if return_lse else out

@@ -167,6 +167,53 @@ bool written_apart(std::initializer_list<Span> written, std::initializer_list<Sp
 }
 size_t type_bytes(int dtype) { return dtype == HSQ_F32 ? 4 : 2; }
 
+// 4-bit cache: what every call says of the sequences.  On success c is filled in.
+constexpr int kKvMaxRows = 1 << 24, kKvMaxHeads = 4096, kKvMaxBatch = 65535, kKvMaxCapacity = 1 << 30;
+constexpr long long kKvMaxBlocks = 1LL << 23;
+
+bool kv_dim_ok(int head_dim) { return head_dim == 64 || head_dim == 128 || head_dim == 256; }
+
+int kv_page_shift(int page_size) {   // log2 of its tiles, or -1
+  if (page_size < kKvTile || page_size > (1 << 20) || (page_size & (page_size - 1))) return -1;
+  return __builtin_ctz((unsigned)page_size) - __builtin_ctz((unsigned)kKvTile);
+}
+
+int kv_check(KvCache &c, const uint8_t *cache, int num_pages, int page_size, int kv_heads, int head_dim,
+             const int32_t *table, int width, const int32_t *lens, const int32_t *cu, int batch, int T,
+             int max_tokens) {
+  if (T < 1 || T > kKvMaxRows || batch < 1 || batch > kKvMaxBatch || kv_heads < 1 || kv_heads > kKvMaxHeads ||
+      num_pages < 1 || width < 1 || (cu && (max_tokens < 1 || max_tokens > T)))
+    return HSQ_E_INVAL;
+  const int shift = kv_page_shift(page_size);
+  if (!kv_dim_ok(head_dim) || shift < 0 || (!cu && T % batch != 0)) return HSQ_E_SHAPE;
+  if ((long long)width * page_size > kKvMaxCapacity) return HSQ_E_INVAL;
+  if (!cache || !table || !lens) return HSQ_E_INVAL;
+  if (!aligned16(cache)) return HSQ_E_ALIGN;
+  for (const int32_t *p : {table, lens, cu})
+    if ((uintptr_t)p & 3u) return HSQ_E_ALIGN;
+  c = KvCache{cache, num_pages, shift, kv_heads, head_dim, table, width, lens, cu, batch, T, cu ? max_tokens : T / batch};
+  const long long tiles = (c.max_tokens + 2LL * kKvTile - 2) / kKvTile;
+  return tiles * batch * kv_heads < kKvMaxBlocks ? HSQ_OK : HSQ_E_INVAL;
+}
+
+size_t kv_cache_bytes(const KvCache &c) {
+  return (((size_t)c.num_pages * c.H) << c.page_shift) * (size_t)kv_tile_bytes(c.D);
+}
+
+// Bytes from the first element of T rows to their last.
+size_t rows_bytes(int T, int stride, size_t row, int elem) { return ((size_t)(T - 1) * stride + row) * elem; }
+
+int kv_attention_sizes(int T, int q_heads, int kv_heads, int head_dim, int batch, int max_tokens, int capacity) {
+  if (T < 1 || T > kKvMaxRows || batch < 1 || batch > kKvMaxBatch || kv_heads < 1 || kv_heads > kKvMaxHeads ||
+      q_heads < 1 || q_heads > kKvMaxHeads || max_tokens < 1 || max_tokens > T || capacity < 1 ||
+      capacity > kKvMaxCapacity)
+    return HSQ_E_INVAL;
+  if (!kv_dim_ok(head_dim) || q_heads % kv_heads != 0) return HSQ_E_SHAPE;
+  const long long rows = (long long)max_tokens * (q_heads / kv_heads);
+  // workgroups of 16 rows, and the parts of few
+  return (rows + 15) / 16 * kv_heads * batch < kKvMaxBlocks && rows < (1LL << 30) ? HSQ_OK : HSQ_E_INVAL;
+}
+
 size_t workspace_bytes(int M, int K, int N, int r, int batch, int group) {
   if (check_sizes(M, K, N, r, batch) != HSQ_OK || !group_ok(group) || K % group != 0) return 0;
   return plan_workspace(M, K, N, r, batch, group).total;
@@ -459,7 +506,7 @@ const char *hsq_status_string(int status) {
   switch (status) {
     case HSQ_OK: return "ok";
     case HSQ_E_INVAL: return "invalid argument";
-    case HSQ_E_SHAPE: return "invalid shape (K must be a positive multiple of 64; window inside the matrix)";
+    case HSQ_E_SHAPE: return "invalid shape (K must be a positive multiple of 64; window inside the matrix; sizes that do not divide)";
     case HSQ_E_ALIGN: return "pointer not 16-byte aligned";
     case HSQ_E_WORKSPACE: return "workspace missing or too small";
     case HSQ_E_HIP: return "HIP launch failed";
@@ -972,6 +1019,139 @@ int hsq_layer_norm_backward(const void *dY, int y_dtype, const void *X, int x_dt
   if (e == hipSuccess && params)
     e = launch_sum_parts(SumArgs{a.part, (size_t)2 * C, a.parts, C, dweight, dbias, p_dtype}, groups, s);
   return debug_check(hip_status(e), stream);
+}
+
+// ---------------------------------------------------------------- 16-bit activations
+
+size_t hsq_w4a16_workspace_bytes(int M, int K, int N, int r, int batch, int group, int smooth, int y_dtype) {
+  if (check_sizes(M, K, N, r, batch) != HSQ_OK || M > HSQ_W4A16_MAX_M || !group_ok(group) || K % group != 0) return 0;
+  return plan_w4a16(M, K, r, batch, group, smooth != 0, y_dtype).total;
+}
+
+int hsq_w4a16_lowrank_linear(const uint16_t *X, int M, int K, int N, int batch, int group, int dtype,
+                             const uint16_t *lambda, const uint8_t *packed_w, const uint16_t *sw,
+                             const uint16_t *L1, const uint16_t *L2, int r, const uint16_t *bias,
+                             const void *residual, void *Y, int y_dtype, void *workspace,
+                             size_t ws_bytes, void *stream) {
+  const int st = check_sizes(M, K, N, r, batch);
+  if (st != HSQ_OK) return st;
+  if (M > HSQ_W4A16_MAX_M || !group_ok(group) || !lin_types_ok(dtype, y_dtype)) return HSQ_E_INVAL;
+  if (K % group != 0) return HSQ_E_SHAPE;
+  if (!X || !packed_w || !sw || !Y || (r > 0 && (!L1 || !L2))) return HSQ_E_INVAL;
+  const void *ptrs[] = {X, lambda, packed_w, sw, L1, L2, bias, residual, Y, workspace};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return HSQ_E_ALIGN;
+  const W4a16Plan P = plan_w4a16(M, K, r, batch, group, lambda != nullptr, y_dtype);
+  if (P.total > 0 && (!workspace || ws_bytes < P.total)) return HSQ_E_WORKSPACE;
+  const size_t m = M, k = K, n = N, b = batch, y_bytes = b * m * n * type_bytes(y_dtype);
+  if (!written_apart({{Y, y_bytes}, {workspace, P.total}},
+                     {{X, m * k * 2}, {lambda, k * 2}, {packed_w, b * packed_bytes(K, N)}, {sw, b * (k / group) * n * 2},
+                      {r > 0 ? L1 : nullptr, b * k * r * 2}, {r > 0 ? L2 : nullptr, b * n * r * 2}, {bias, b * n * 2},
+                      {residual == Y ? nullptr : residual, y_bytes}}))
+    return HSQ_E_INVAL;
+  char *ws = (char *)workspace;
+  W4a16Args a{};
+  a.X = X; a.lam = lambda; a.L1 = r > 0 ? L1 : nullptr; a.L2 = r > 0 ? L2 : nullptr; a.bias = bias; a.res = residual;
+  a.w = packed_w; a.w_stride = packed_bytes(K, N); a.sw = sw; a.Y = Y;
+  a.hi = (uint16_t *)(ws + P.hi_off); a.lo = (uint16_t *)(ws + P.lo_off);
+  a.es = (float *)(ws + P.es_off); a.uw = (float *)(ws + P.uw_off);
+  a.M = M; a.K = K; a.N = N; a.r = r; a.batch = batch; a.bpg = group / kGroup; a.dtype = dtype; a.y_dtype = y_dtype;
+  a.terms = P.terms; a.u_slices = P.u_slices; a.slice = P.slice;
+  return debug_check(hip_status(launch_w4a16(a, (hipStream_t)stream)), stream);
+}
+
+// ---------------------------------------------------------------- 4-bit cache
+
+size_t hsq_kv_page_bytes(int page_size, int kv_heads, int head_dim) {
+  const int shift = kv_page_shift(page_size);
+  if (shift < 0 || kv_heads < 1 || kv_heads > kKvMaxHeads || !kv_dim_ok(head_dim)) return 0;
+  return ((size_t)kv_heads << shift) * (size_t)kv_tile_bytes(head_dim);
+}
+
+int hsq_kv_cache_write(const uint16_t *K, int k_stride, const uint16_t *V, int v_stride, int T, int dtype,
+                       int kv_heads, int head_dim, int quant, uint8_t *cache, int num_pages, int page_size,
+                       const int32_t *block_table, int table_width, const int32_t *kv_lens,
+                       const int32_t *cu_tokens, int batch, int max_tokens, void *stream) {
+  KvMoveArgs a{};
+  const int st = kv_check(a.c, cache, num_pages, page_size, kv_heads, head_dim, block_table, table_width, kv_lens,
+                          cu_tokens, batch, T, max_tokens);
+  if (st != HSQ_OK) return st;
+  if (!K || !V || (dtype != HSQ_BF16 && dtype != HSQ_F16) || !aq_ok(quant)) return HSQ_E_INVAL;
+  const int row = kv_heads * head_dim;
+  if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0) return HSQ_E_SHAPE;
+  if (!aligned16(K) || !aligned16(V)) return HSQ_E_ALIGN;
+  const size_t b = batch;
+  if (!written_apart({{cache, kv_cache_bytes(a.c)}},
+                     {{K, rows_bytes(T, k_stride, row, 2)}, {V, rows_bytes(T, v_stride, row, 2)},
+                      {block_table, b * table_width * 4}, {kv_lens, b * 4}, {cu_tokens, (b + 1) * 4}}))
+    return HSQ_E_INVAL;
+  a.k = const_cast<uint16_t *>(K); a.v = const_cast<uint16_t *>(V);
+  a.k_stride = k_stride; a.v_stride = v_stride; a.dtype = dtype; a.asym = quant == HSQ_AQ_ASYMMETRIC;
+  return debug_check(hip_status(launch_kv_write(a, (hipStream_t)stream)), stream);
+}
+
+int hsq_kv_cache_read(const uint8_t *cache, int num_pages, int page_size, int kv_heads, int head_dim,
+                      const int32_t *block_table, int table_width, const int32_t *kv_lens,
+                      const int32_t *cu_tokens, int batch, int T, int max_tokens, void *K, void *V,
+                      int dtype, void *stream) {
+  KvMoveArgs a{};
+  const int st = kv_check(a.c, cache, num_pages, page_size, kv_heads, head_dim, block_table, table_width, kv_lens,
+                          cu_tokens, batch, T, max_tokens);
+  if (st != HSQ_OK) return st;
+  if (!K || !V || (dtype != HSQ_F32 && dtype != HSQ_BF16 && dtype != HSQ_F16)) return HSQ_E_INVAL;
+  if (!aligned16(K) || !aligned16(V)) return HSQ_E_ALIGN;
+  const int row = kv_heads * head_dim;
+  const size_t b = batch, bytes = (size_t)T * row * type_bytes(dtype);
+  if (!written_apart({{K, bytes}, {V, bytes}},
+                     {{cache, kv_cache_bytes(a.c)}, {block_table, b * table_width * 4}, {kv_lens, b * 4},
+                      {cu_tokens, (b + 1) * 4}}))
+    return HSQ_E_INVAL;
+  a.k = K; a.v = V;
+  a.k_stride = a.v_stride = row; a.dtype = dtype;
+  return debug_check(hip_status(launch_kv_read(a, (hipStream_t)stream)), stream);
+}
+
+size_t hsq_kv_attention_workspace_bytes(int T, int q_heads, int kv_heads, int head_dim, int batch, int max_tokens,
+                                        int capacity) {
+  if (kv_attention_sizes(T, q_heads, kv_heads, head_dim, batch, max_tokens, capacity) != HSQ_OK) return 0;
+  return plan_kv_attention(T, q_heads, kv_heads, head_dim, batch, max_tokens, capacity).total;
+}
+
+int hsq_kv_attention(const uint16_t *Q, int q_stride, int T, int dtype, int q_heads, const uint8_t *cache,
+                     int num_pages, int page_size, int kv_heads, int head_dim, const int32_t *block_table,
+                     int table_width, const int32_t *kv_lens, const int32_t *cu_tokens, int batch,
+                     int max_tokens, float scale, int causal, int window, void *Y, int y_dtype, float *lse,
+                     void *workspace, size_t ws_bytes, void *stream) {
+  KvAttnArgs a{};
+  int st = kv_check(a.c, cache, num_pages, page_size, kv_heads, head_dim, block_table, table_width, kv_lens, cu_tokens,
+                    batch, T, max_tokens);
+  if (st != HSQ_OK) return st;
+  const int capacity = table_width * page_size;
+  st = kv_attention_sizes(T, q_heads, kv_heads, head_dim, batch, a.c.max_tokens, capacity);
+  if (st != HSQ_OK) return st;
+  if (!Q || !Y || !lin_types_ok(dtype, y_dtype) || !(scale > 0.0f) || !(scale <= 1e30f) ||
+      (causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal))
+    return HSQ_E_INVAL;
+  const int row = q_heads * head_dim;
+  if (q_stride < row || q_stride % 8 != 0) return HSQ_E_SHAPE;
+  const void *ptrs[] = {Q, Y, lse, workspace};
+  for (const void *p : ptrs)
+    if (p && !aligned16(p)) return HSQ_E_ALIGN;
+  const KvAttnPlan P = plan_kv_attention(T, q_heads, kv_heads, head_dim, batch, a.c.max_tokens, capacity);
+  if (P.total > 0 && (!workspace || ws_bytes < P.total)) return HSQ_E_WORKSPACE;
+  const size_t b = batch, t = T;
+  if (!written_apart({{Y, t * row * type_bytes(y_dtype)}, {lse, t * q_heads * 4}, {workspace, P.total}},
+                     {{Q, rows_bytes(T, q_stride, row, 2)}, {cache, kv_cache_bytes(a.c)},
+                      {block_table, b * table_width * 4}, {kv_lens, b * 4}, {cu_tokens, (b + 1) * 4}}))
+    return HSQ_E_INVAL;
+  a.Q = Q; a.q_stride = q_stride; a.dtype = dtype; a.Hq = q_heads; a.gr = q_heads / kv_heads;
+  a.scale2 = scale * 1.4426950408889634f;
+  a.causal = causal; a.window = window;
+  a.Y = Y; a.y_dtype = y_dtype; a.lse = lse;
+  a.part_ol = (float2 *)workspace;
+  a.part = (float *)((char *)workspace + P.part_off);
+  a.splits = P.splits;
+  return debug_check(hip_status(launch_kv_attention(a, P, (hipStream_t)stream)), stream);
 }
 
 }  // extern "C"

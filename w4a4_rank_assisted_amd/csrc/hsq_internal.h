@@ -401,6 +401,113 @@ int norm_backward_parts(int M, int C, int groups);
 hipError_t launch_layer_norm(const NormArgs &a, hipStream_t s);
 hipError_t launch_layer_norm_backward(const NormArgs &a, hipStream_t s);
 
+// ---------------------------------------------------------------------------
+// The layer with 16-bit activations (w4a16.hip)
+// ---------------------------------------------------------------------------
+// Workspace.  With smoothing, xh = X / lambda is kept as fp16 numbers under a
+// power of two per row and scale group: xh = 2^e (hi + lo), lo only where the
+// output holds more bits than hi does.
+//   hi, lo: M x K fp16      es: M16 x K/group fp32 (2^e), M16 = 16 ceil(M/16)
+//   uw:     u_slices x (batch*r) x M16 fp32, one slice of U per slice of K
+struct W4a16Plan {
+  int terms = 1;           // 2: hi and lo
+  int u_slices = 0, slice = 0;   // slices of K of the preparing launch, channels of one
+  size_t hi_off = 0, lo_off = 0, es_off = 0, uw_off = 0, total = 0;
+};
+W4a16Plan plan_w4a16(int M, int K, int r, int batch, int group, bool smooth, int y_dtype);
+
+struct W4a16Args {
+  const uint16_t *X;       // M x K of dtype
+  const uint16_t *lam;     // K fp16, or null
+  const uint16_t *L1, *L2; // batch x K x r, batch x r x N of dtype (null: r = 0)
+  const uint16_t *bias;    // batch x N, or null
+  const void *res;         // batch x M x N of y_dtype, or null
+  const uint8_t *w;        // packed residuals, w_stride bytes apart (nibble part read)
+  size_t w_stride;
+  const uint16_t *sw;      // batch x K/group x N fp16
+  void *Y;
+  uint16_t *hi, *lo;       // workspace
+  float *es, *uw;
+  int M, K, N, r, batch, bpg, dtype, y_dtype;
+  int terms, u_slices, slice;
+};
+hipError_t launch_w4a16(const W4a16Args &a, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// 4-bit key / value cache (kv_cache.hip) and attention over it (kv_attention.hip)
+//
+// A page holds, per head, page_size / 32 tiles of 32 tokens.  A tile of D
+// channels (G = D / 64 groups, one scale and one zero per token and group) is
+// 32 D + 192 G bytes, laid out as the attention's matrix operands, so that a
+// wave reads it once, 16 bytes a lane, straight into registers:
+//
+//   K codes  dword x = a D/32 + i of lane slot l = c + 16 q (byte (x/4) 1024 +
+//            16 l + 4 (x%4)) holds token 16 a + c, channels 32 i + 8 q + j:
+//            j = 0, 2, 1, 3 in the low nibbles of bytes 0 .. 3, j + 4 in the
+//            high ones (two shifts and masks then give neighbours j, j + 1)
+//   V codes  dword x = 2 p + a of lane slot l = c + 16 q: byte b holds token
+//            16 a + 4 q + r with r = 0, 2, 1, 3, channel 32 p + c in its low
+//            nibble and 32 p + 16 + c in its high one: no byte is shared by two
+//            tokens, so appending one never reads another
+//   scales   fp16, K then V: [group][q][4 a + r] for token 16 a + 4 q + r
+//   zeros    bytes 16 + z (as the attention adds them), K then V: [q][group][a][b], b as in the V codes
+//
+// 16 + n is a code as the matrix operand sees it: the nibble under a constant
+// exponent, in bf16 and in fp16 alike.
+// ---------------------------------------------------------------------------
+constexpr int kKvTile = 32;                  // tokens per tile
+constexpr int kKvGroup = 64;                 // channels per scale
+constexpr int kv_tile_bytes(int D) { return 32 * D + 192 * (D / kKvGroup); }
+
+// The cache and the sequences a call works on; everything the device reads from
+// table, lens and cu is checked against the sizes here before it is used.
+struct KvCache {
+  const uint8_t *cache;    // num_pages x H x 2^page_shift x kv_tile_bytes(D)
+  int num_pages, page_shift, H, D;   // a page is 2^page_shift tiles
+  const int32_t *table;    // B x width page numbers
+  int width;
+  const int32_t *lens;     // B: tokens of each sequence, the call's own included
+  const int32_t *cu;       // B + 1 first rows, or null: T / B rows each
+  int B, T, max_tokens;
+};
+
+struct KvMoveArgs {
+  KvCache c;
+  void *k, *v;             // T x H x D rows (inputs of a write, outputs of a read)
+  int k_stride, v_stride;  // elements from token to token
+  int dtype, asym;
+};
+hipError_t launch_kv_write(const KvMoveArgs &a, hipStream_t s);
+hipError_t launch_kv_read(const KvMoveArgs &a, hipStream_t s);
+
+struct KvAttnArgs {
+  KvCache c;
+  const uint16_t *Q;       // T rows of Hq x D, q_stride elements apart
+  int q_stride, dtype, Hq, gr;   // gr = Hq / H query heads to a head of the cache
+  float scale2;            // scale log2(e)
+  int causal, window;      // window 0: none
+  void *Y;                 // T x Hq x D
+  int y_dtype;
+  float *lse;              // T x Hq, or null
+  // split sequences: unscaled sums of the parts, and their (offset, weight)
+  float *part;             // T x Hq x splits x D
+  float2 *part_ol;         // T x Hq x splits
+  int splits;
+};
+
+// How a call is launched: by tokens (the waves of a workgroup share its rows and
+// deal the tokens out, `splits` workgroups to a block of rows) or by rows (a wave
+// has rows of its own and all of their tokens).
+struct KvAttnPlan {
+  bool by_rows = false;
+  int mt = 1;              // row tiles of 16 to a wave
+  int waves = 8;
+  int splits = 1;
+  size_t part_off = 0, total = 0;
+};
+KvAttnPlan plan_kv_attention(int T, int Hq, int H, int D, int B, int max_tokens, int64_t capacity);
+hipError_t launch_kv_attention(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s);
+
 }  // namespace hsq
 
 // ---------------------------------------------------------------------------
@@ -415,6 +522,32 @@ typedef unsigned v2u __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+
+// Rows of sequence b among the T of a call (clamped: whatever cu holds).
+__device__ __forceinline__ void kv_rows(const KvCache &c, int b, int &start, int &n) {
+  if (c.cu) {
+    start = min(max(c.cu[b], 0), c.T);
+    n = min(max(c.cu[b + 1], start), c.T) - start;
+  } else {
+    n = c.T / c.B;
+    start = b * n;
+  }
+}
+
+// Tokens of sequence b that the cache can hold: its length, cut at the end of
+// the page table.
+__device__ __forceinline__ int kv_len(const KvCache &c, int b) {
+  const int64_t cap = ((int64_t)c.width << c.page_shift) * kKvTile;
+  return (int)min((int64_t)max(c.lens[b], 0), cap);
+}
+
+// Tile `tile` of sequence b, head h; null where the table names no page.
+__device__ __forceinline__ const uint8_t *kv_tile_at(const KvCache &c, int b, int h, int tile) {
+  const int page = c.table[(size_t)b * c.width + (tile >> c.page_shift)];
+  if ((unsigned)page >= (unsigned)c.num_pages) return nullptr;
+  const size_t at = (((size_t)page * c.H + h) << c.page_shift) + (tile & ((1 << c.page_shift) - 1));
+  return c.cache + at * (size_t)kv_tile_bytes(c.D);
+}
 
 // Buffer resource over `bytes` bytes at p (raw, untyped; reads past the end
 // return zero).  Loads through it take a 32-bit per-lane offset plus a
