@@ -91,7 +91,8 @@ def attention64(Q, k, v, ks, vs, pos, scale, causal, window, y_dtype):
     31 |q|, each addition off by 2 U, then a few roundings; exp2's argument is off
     by U (4 |e| log2(e) + 64) and its result by two units (so eta, relative);
     p s is rounded to fp16 (2^-11) or to two (2^-21), not below 2^-32 of the row's
-    largest; the sums over N tokens add 2 N U."""
+    largest; the sums over N tokens add 2 N U: of |v|, or, where the result has 16
+    bits, of p s n and p s z apart, 30 p s in all."""
     n, Hq, D = Q.shape
     N, H, _ = k.shape
     G = D // 64
@@ -128,7 +129,11 @@ def attention64(Q, k, v, ks, vs, pos, scale, causal, window, y_dtype):
         eta = de + U32 * (4 * 1.45 * big + 64) * 0.7 + 8 * U32
         ps = (p[:, :, None] * vs[None, :, hk].double()).amax(1)                       # n, G
         floor = (15 * N * 2.0 ** -32 * ps / div).repeat_interleave(64, 1)
-        t1 = aa * (eta + h + 2 * (N + 64) * U32) + yy.abs() * (eta + 2 * (N + 64) * U32 + 8 * U32) + floor
+        apart = 0.0
+        if y_dtype != torch.float32:
+            sums = (torch.mm(p, vs[:, hk].double()) / div).repeat_interleave(64, 1)
+            apart = 30 * sums * 2 * (N + 64) * U32
+        t1 = aa * (eta + h + 2 * (N + 64) * U32) + apart + yy.abs() * (eta + 2 * (N + 64) * U32 + 8 * U32) + floor
         y[:, hq] = yy
         ty[:, hq] = t1 + half_step(y_dtype) * (yy.abs() + t1) + tiny(y_dtype)
         l = torch.log(tot[:, 0]) + top

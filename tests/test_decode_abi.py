@@ -153,7 +153,8 @@ def test_sizes():
         assert f(64, K, 64, 32, 16, 64, 1, hsq.F32) < 1 << 35
     g = lib.hsq_kv_attention_workspace_bytes
     assert g(1, 32, 8, 128, 1, 1, 131072) > 0            # one sequence is split
-    assert g(64, 32, 8, 128, 64, 1, 131072) == 0         # a batch fills the chip
+    assert g(1024, 32, 8, 128, 1024, 1, 131072) == 0     # a large batch fills the chip
+    assert g(2048, 32, 8, 128, 1, 2048, 131072) == 0     # and so does a prompt
     assert g(0, 32, 8, 128, 1, 1, 64) == 0 and g(1, 32, 5, 128, 1, 1, 64) == 0 and g(1, 32, 8, 96, 1, 1, 64) == 0
     # a bound on the rows that is larger never needs more
     for D in (64, 128, 256):

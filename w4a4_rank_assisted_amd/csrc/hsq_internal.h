@@ -500,8 +500,7 @@ struct KvAttnArgs {
 // has rows of its own and all of their tokens).
 struct KvAttnPlan {
   bool by_rows = false;
-  int mt = 1;              // row tiles of 16 to a wave
-  int waves = 8;
+  int rows = 4;            // of a workgroup
   int splits = 1;
   size_t part_off = 0, total = 0;
 };

@@ -2,242 +2,133 @@
 //
 //   e[i,t] = scale q_i . k_t,   y_i = sum_t exp(e[i,t]) v_t / sum_t exp(e[i,t])
 //
-// over the tokens t that query i sees.  Keys and values are s (n - z) with one
-// scale s and zero z per token and group g of 64 channels, so the codes enter the
-// matrix products as small integers (exact in 16 bits) and the scales stay with
-// the (query, token) pairs in fp32:
+// over the tokens t that query i sees.  Keys and values are s (n - z), one scale s
+// and zero z per token and group g of 64 channels, so the codes enter the matrix
+// products as they are and everything else stays with the (query, token) pairs:
 //
-//   q . k_t        = sum_g s_g (sum_d q_d (16 + n_d) - (16 + z_g) sum_d q_d)
-//   sum_t p_t v_t  = sum_t (p_t s_g) (n_d - z_g)
+//   q . k_t        = sum_g s_g (sum_d q_d n_d - z_g sum_d q_d)
+//   sum_t p_t v_t  = sum_t (p_t s_g) n_d - sum_t (p_t s_g) z_g
 //
-// 16 + n is a nibble under a constant exponent, two operations a pair; the second
-// product runs in fp16, where one packed subtraction a pair makes it n - z.  p s is
-// the only value that is rounded: to fp16 (11 bits), or, where the result is fp32,
-// to the sum of two.  Its range is kept by the row's offset o, a whole number:
-// p = 2^(e log2(e) - o) with o such that p s stays below 2^15; o moves, and the
-// sums with it by an exact power of two, only when a tile would exceed that (seven
-// doublings above the tile that set it), so the running maximum of the softmax
-// costs one comparison a tile.
+// (where the result is fp32 the second is summed as (p_t s_g) (n_d - z_g), which
+// costs a subtraction a pair of codes and keeps what the difference cancels).
+// A nibble n in the lowest bits of a 16-bit half is the subnormal fp16 number n
+// 2^-24, and in the next four n 2^-20; the matrix unit takes both exactly.  A dword
+// of eight codes is thus four masks and one shift; the powers of two go into the
+// queries and the end.  Queries are held in fp16 under a power of two per row
+// (what that loses is below 2^-38 of the row's largest channel).  Products are exact
+// and sums fp32.  p s is the only value that is rounded: to fp16 (11 bits), or,
+// where the result is fp32, to the sum of two.  Its range is kept by the row's offset
+// o, a whole number: p = 2^(e log2(e) - o) with o such that p s stays below 2^15; o
+// moves, and the sums with it by an exact power of two, only when a tile would
+// exceed that (seven doublings above the tile that set it), so the running
+// maximum of the softmax costs one comparison a tile.
 //
-// Both products are formed transposed (tokens x queries, channels x queries): a
-// lane then holds tokens 16 a + 4 q + r of its query in the first product's result
-// and needs the same ones for the second's operand, so p never leaves the
-// registers, and the loop has no LDS and no barrier.
+// Three forms, by the query rows that share a head of the cache in one sequence:
+//
+// - Up to 8 rows (a token or two of a few heads each): the 4 x 4 products.  A lane
+//   is a token of its group's channels in the first and two channels in the
+//   second, so no lane's work is lost on rows that do not exist, which in 16 x 16
+//   tiles is three quarters at four rows.  The first product leaves tokens 4 c .. 4 c + 3
+//   of row j in lane 4 c + j, which is the second's operand.  The call is bound by
+//   the read of the cache.
+// - Up to 63 rows: 16 x 16 products, transposed (tokens x queries, channels x
+//   queries), so that here too a lane needs for the second product the tokens that
+//   the first one gave it.
+// - More (prompts): the same, two row tiles to a wave, and each wave has rows of its own.
+//
+// In none of them p leaves the registers, and the loop has no LDS and no barrier.
+// In the first two the waves of a workgroup deal out its tokens, and
+// workgroups split long sequences (k_kv_join adds their parts).
 #include "hsq_internal.h"
 
 #include <algorithm>
+#include <utility>
 
 namespace hsq {
 
 namespace {
 
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 constexpr float kNoOffset = -1e30f;      // of a row that has seen nothing
 constexpr float kTop = 8.0f;             // p s of the tile that sets the offset stays below 2^kTop
 constexpr float kMaxPs = 32768.0f;       // what moves the offset
 constexpr float kMaxP = 1099511627776.0f;   // 2^40: the same for tokens of scale 0
+constexpr float kHidden = -__builtin_inff();   // the score of a token that is not seen
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kTiny = 5.9604644775390625e-8f;   // 2^-24: of a code in the lowest bits
 
-template <int DT>
 __device__ __forceinline__ v4f mfma16(v4u a, v4u b, v4f c) {
-  if constexpr (DT == kBf16)
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
-// The eight codes of a dword as 16 + n: the low nibbles of bytes 0, 2 | 1, 3, then the high ones.
-template <int DT>
-__device__ __forceinline__ v4u expand(uint32_t w) {
-  if constexpr (DT == kBf16) {
-    constexpr uint32_t m = 0x00780078u, k = 0x41804180u;
-    return (v4u){(w << 3 & m) | k, (w >> 5 & m) | k, (w >> 1 & m) | k, (w >> 9 & m) | k};
-  } else {
-    constexpr uint32_t m = 0x03C003C0u, k = 0x4C004C00u;
-    return (v4u){(w << 6 & m) | k, (w >> 2 & m) | k, (w << 2 & m) | k, (w >> 6 & m) | k};
-  }
+// 16 products of 4 x 4; with BLOCK >= 0 each half of the wave takes block BLOCK of
+// its own eight blocks of a for all of them.
+template <int BLOCK>
+__device__ __forceinline__ v4f mfma4(v2u a, v2u b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(v4h, a), __builtin_bit_cast(v4h, b), c, BLOCK >= 0 ? 3 : 0,
+                                            BLOCK >= 0 ? BLOCK : 0, 0);
 }
+
+constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;   // codes as n 2^-24 and n 2^-20
 
 __device__ __forceinline__ uint32_t pack_h(float a, float b) {
   v2h h = {(_Float16)a, (_Float16)b};
   return __builtin_bit_cast(uint32_t, h);
 }
-
-// (16 + n) - (16 + z), two at a time
+// n - z, two at a time, under the same power of two (exact, subnormal)
 __device__ __forceinline__ uint32_t minus_h(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, a) - __builtin_bit_cast(v2h, b));
 }
-
-__device__ __forceinline__ float over_q(float v, bool sum) {   // lanes of one column: 16 and 32 apart
-  const float a = __shfl_xor(v, 16);
-  v = sum ? v + a : fmaxf(v, a);
-  const float b = __shfl_xor(v, 32);
-  return sum ? v + b : fmaxf(v, b);
-}
-
-template <int D>
-struct TileRegs {
-  static constexpr int G = D / kKvGroup;
-  v4u k[G], v[G], ks[G], vs[G];
-  v2u kz[G], vz[G];
-};
-
-template <int D>
-__device__ __forceinline__ void load_tile(const uint8_t *p, int lane, TileRegs<D> &t) {
-  constexpr int G = D / kKvGroup;
-  const int q = lane >> 4;
-#pragma unroll
-  for (int x = 0; x < G; ++x) {
-    t.k[x] = *reinterpret_cast<const v4u *>(p + x * 1024 + lane * 16);
-    t.v[x] = *reinterpret_cast<const v4u *>(p + 16 * D + x * 1024 + lane * 16);
-    t.ks[x] = *reinterpret_cast<const v4u *>(p + 32 * D + x * 64 + q * 16);
-    t.vs[x] = *reinterpret_cast<const v4u *>(p + 32 * D + 64 * G + x * 64 + q * 16);
-    t.kz[x] = *reinterpret_cast<const v2u *>(p + 32 * D + 128 * G + (q * G + x) * 8);
-    t.vz[x] = *reinterpret_cast<const v2u *>(p + 32 * D + 160 * G + (q * G + x) * 8);
-  }
-}
-
 __device__ __forceinline__ float half_of(v4u w, int i) { return f16_to_f32((uint16_t)(w[i >> 1] >> (16 * (i & 1)))); }
+__device__ __forceinline__ float half_of(v2u w, int i) { return f16_to_f32((uint16_t)(w[i >> 1] >> (16 * (i & 1)))); }
+// Zero r of four tokens in a dword (bytes 0, 2, 1, 3).
+__device__ __forceinline__ float zero_of(uint32_t w, int r) {
+  return (float)(w >> (8 * (((r & 1) << 1) | (r >> 1))) & 0xFFu);
+}
 
-// Sums of a wave: MT row tiles, lane's query is column lane % 16 of each.
-template <int D, int MT>
-struct Sums {
-  static constexpr int G = D / kKvGroup;
-  v4f acc[MT][D / 16];     // channels 16 nt + 4 (lane / 16) + r
-  float o[MT], l[MT];      // l: this lane's tokens only
-};
+// Reductions over lanes that differ in the bits of FROM .. TO.
+template <int FROM, int TO>
+__device__ __forceinline__ float max_over(float v) {
+#pragma unroll
+  for (int m = FROM; m <= TO; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
+  return v;
+}
+template <int FROM, int TO>
+__device__ __forceinline__ float sum_over(float v) {
+#pragma unroll
+  for (int m = FROM; m <= TO; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
 
-// One tile of 32 tokens.  MASK: token t0 + i is seen by row tile m's query where
-// lo[m] <= t0 + i < hi[m].
-template <int D, int MT, int DT, bool SPLIT, bool MASK>
-__device__ __forceinline__ void step(const TileRegs<D> &t, const v4u (&Q)[MT][D / 32], const float (&qs)[MT][D / 64],
-                                     float c2, int t0, const int *lo, const int *hi, Sums<D, MT> &s) {
-  constexpr int G = D / kKvGroup;
-  const int q = (threadIdx.x & 63) >> 4;
-  float e[MT][8];
+// Eight channels of a query as fp16 under 2^-ex, the last four by another 1/16 (they
+// meet the codes of the high nibbles).
+__device__ __forceinline__ void unpack8(v4u w, int dtype, float *f) {
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int x = a * (D / 32) + 2 * g;
-      const v4u k0 = expand<DT>(t.k[x >> 2][x & 3]), k1 = expand<DT>(t.k[(x + 1) >> 2][(x + 1) & 3]);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        v4f d = mfma16<DT>(k0, Q[m][2 * g], (v4f){0.0f, 0.0f, 0.0f, 0.0f});
-        d = mfma16<DT>(k1, Q[m][2 * g + 1], d);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float z = (float)(t.kz[g][a] >> (8 * (((r & 1) << 1) | (r >> 1))) & 0xFFu);
-          const float u = __builtin_fmaf(-z, qs[m][g], d[r]);
-          const float k = half_of(t.ks[g], 4 * a + r);
-          e[m][4 * a + r] = g ? __builtin_fmaf(u, k, e[m][4 * a + r]) : u * k;
-        }
-      }
-    }
+  for (int e = 0; e < 4; ++e) {
+    f[2 * e] = dtype == kBf16 ? bf16_to_f32(w[e] & 0xFFFFu) : f16_to_f32((uint16_t)w[e]);
+    f[2 * e + 1] = dtype == kBf16 ? __uint_as_float(w[e] & 0xFFFF0000u) : f16_to_f32((uint16_t)(w[e] >> 16));
   }
-  if (MASK) {
+}
+__device__ __forceinline__ float largest8(v4u w, int dtype) {
+  float f[8], m = 0.0f;
+  unpack8(w, dtype, f);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int tok = t0 + 16 * (i >> 2) + 4 * q + (i & 3);
-        if (tok < lo[m] || tok >= hi[m]) e[m][i] = -__builtin_inff();
-      }
-  }
-  float p[MT][8], ps[MT][G][8];
-  bool moved = false;
-  auto weigh = [&](int m) __attribute__((always_inline)) {
-    float top = 0.0f, topp = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      p[m][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(e[m][i], c2, -s.o[m]));
-      topp = fmaxf(topp, p[m][i]);
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        float w = p[m][i] * half_of(t.vs[g], i);
-        // a hidden token's scale may be anything, NaN among it
-        if (MASK) w = e[m][i] == -__builtin_inff() ? 0.0f : w;
-        ps[m][g][i] = w;
-        top = fmaxf(top, w);
-      }
-    }
-    return top > kMaxPs || topp > kMaxP;
-  };
-#pragma unroll
-  for (int m = 0; m < MT; ++m) moved |= weigh(m);
-  if (__builtin_expect(__any(moved), 0)) {
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      float top = -__builtin_inff();
-      bool mine = false;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float b = e[m][i] * c2;
-        mine |= p[m][i] > kMaxP;
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-          mine |= ps[m][g][i] > kMaxPs;
-          const float v = half_of(t.vs[g], i);
-          top = fmaxf(top, b + __builtin_amdgcn_logf(fmaxf(v, 5.9604644775390625e-8f)));
-        }
-      }
-      top = over_q(top, false);
-      if (over_q(mine ? 1.0f : 0.0f, false) > 0.0f) {
-        const float o = __builtin_ceilf(top) - kTop;
-        const float al = __builtin_amdgcn_exp2f(s.o[m] - o);
-        s.o[m] = o;
-        s.l[m] *= al;
-#pragma unroll
-        for (int n = 0; n < D / 16; ++n) s.acc[m][n] *= al;
-      }
-      weigh(m);
-    }
-  }
-  v4u w[MT][G], w2[MT][G];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s.l[m] += p[m][i];
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t hi = pack_h(ps[m][g][2 * i], ps[m][g][2 * i + 1]);   // (a bit_cast of w[m][g][i] reads w[m][g][0])
-        w[m][g][i] = hi;
-        if (SPLIT) {
-          const v2h h = __builtin_bit_cast(v2h, hi);
-          w2[m][g][i] = pack_h(ps[m][g][2 * i] - (float)h[0], ps[m][g][2 * i + 1] - (float)h[1]);
-        }
-      }
-  }
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    v4u zz;
-#pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      const v4u z = expand<kF16>(t.vz[g][a]);
-      zz[2 * a] = z[0];
-      zz[2 * a + 1] = z[1];
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {         // channels 32 p ..: 32 tokens in two dwords
-      const int pr = 2 * g + h;
-      const v4u v0 = expand<kF16>(t.v[pr >> 1][2 * (pr & 1)]), v1 = expand<kF16>(t.v[pr >> 1][2 * (pr & 1) + 1]);
-      const v4u b0 = {minus_h(v0[0], zz[0]), minus_h(v0[1], zz[1]), minus_h(v1[0], zz[2]), minus_h(v1[1], zz[3])};
-      const v4u b1 = {minus_h(v0[2], zz[0]), minus_h(v0[3], zz[1]), minus_h(v1[2], zz[2]), minus_h(v1[3], zz[3])};
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        s.acc[m][2 * pr] = mfma16<kF16>(b0, w[m][g], s.acc[m][2 * pr]);
-        s.acc[m][2 * pr + 1] = mfma16<kF16>(b1, w[m][g], s.acc[m][2 * pr + 1]);
-        if (SPLIT) {
-          s.acc[m][2 * pr] = mfma16<kF16>(b0, w2[m][g], s.acc[m][2 * pr]);
-          s.acc[m][2 * pr + 1] = mfma16<kF16>(b1, w2[m][g], s.acc[m][2 * pr + 1]);
-        }
-      }
-    }
-  }
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+  return m;
+}
+__device__ __forceinline__ v4u scaled8(v4u w, int dtype, float by) {
+  float f[8];
+  unpack8(w, dtype, f);
+  return (v4u){pack_h(f[0] * by, f[1] * by), pack_h(f[2] * by, f[3] * by), pack_h(f[4] * by * 0.0625f, f[5] * by * 0.0625f),
+               pack_h(f[6] * by * 0.0625f, f[7] * by * 0.0625f)};
+}
+// The power of two that takes a row's largest channel to [2^13, 2^14), and the
+// factor from the products' sums to scores in powers of two.
+__device__ __forceinline__ float row_power(float top, float scale2, float &to_score) {
+  const int ex = min(max((int)(__float_as_uint(top) >> 23) - 13, 1), 240);
+  to_score = __uint_as_float((uint32_t)ex << 23) * 16777216.0f * scale2;
+  return __uint_as_float((uint32_t)(254 - ex) << 23);
 }
 
 // Tokens [lo, hi) that token i of a sequence sees.
@@ -262,6 +153,7 @@ __device__ __forceinline__ void tiles_of_rows(const KvAttnArgs &a, int r0, int r
 
 // Tiles of one part of [first, last).
 constexpr int kMinTiles = 16;             // a part is 512 tokens at least
+constexpr int kMaxParts = 64;
 __device__ __forceinline__ int tiles_of_part(int first, int last, int splits) {
   return max((last - first + splits - 1) / splits, kMinTiles);
 }
@@ -290,66 +182,297 @@ __device__ __forceinline__ float lse_of(float o, float l) {
 }
 __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
-template <int D, int MT, int W, int DT, bool SPLIT, bool ROWS>
-__global__ __launch_bounds__(64 * W) void k_kv_attention(KvAttnArgs a, int blocks) {
+
+// ------------------------------------------------------------------ 16 x 16
+// One side of a tile: codes, scales, zeros.
+template <int D>
+struct Side {
+  static constexpr int G = D / kKvGroup;
+  v4u code[G], s[G];
+  v2u z[G];
+};
+
+template <int D, bool V>
+__device__ __forceinline__ void load_side(const uint8_t *p, int lane, Side<D> &t) {
+  constexpr int G = D / kKvGroup;
+  const int q = lane >> 4;
+#pragma unroll
+  for (int x = 0; x < G; ++x) t.code[x] = *reinterpret_cast<const v4u *>(p + (V ? 16 * D : 0) + x * 1024 + lane * 16);
+#pragma unroll
+  for (int x = 0; x < G; ++x) {
+    t.s[x] = *reinterpret_cast<const v4u *>(p + 32 * D + (V ? 64 * G : 0) + x * 64 + q * 16);
+    t.z[x] = *reinterpret_cast<const v2u *>(p + 32 * D + 128 * G + (V ? 32 * G : 0) + (q * G + x) * 8);
+  }
+}
+
+// Sums of a wave: MT row tiles, lane's query is column lane % 16 of each.
+template <int D, int MT>
+struct Sums {
+  static constexpr int G = D / kKvGroup;
+  v4f acc[MT][D / 16];     // channels 16 nt + 4 (lane / 16) + r, times 2^-24 (nt even) and 2^-20
+  v4f zero[MT][G];         // the sums of (p s) z, times 2^-24: all four alike
+  float o[MT], l[MT];      // l: this lane's tokens only
+};
+
+// The scores of 32 tokens: e[m][4 a + r] of token 16 a + 4 q + r.
+template <int D, int MT>
+__device__ __forceinline__ void scores(const Side<D> &t, const v4u (&Q)[MT][D / 32], const float (&qs)[MT][D / 64],
+                                       float (&e)[MT][8]) {
+  constexpr int G = D / kKvGroup;
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      v4u k[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int i = a * (D / 32) + 2 * g + x;
+        const uint32_t w = t.code[i >> 2][i & 3], v = w >> 8;
+        k[x] = (v4u){w & kLow, v & kLow, w & kHigh, v & kHigh};
+      }
+      const uint32_t zw = t.z[g][a] & 0x0F0F0F0Fu;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        v4f d = mfma16(k[0], Q[m][2 * g], (v4f){0.0f, 0.0f, 0.0f, 0.0f});
+        d = mfma16(k[1], Q[m][2 * g + 1], d);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float u = __builtin_fmaf(-zero_of(zw, r), qs[m][g], d[r]);
+          e[m][4 * a + r] = __builtin_fmaf(u, half_of(t.s[g], 4 * a + r), g ? e[m][4 * a + r] : 0.0f);
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);   // half of the operands at a time
+  }
+}
+
+// Their weights: l, and p s as the second product's operand (w, and w2 what its
+// rounding leaves).  vs: the values' scales; c2: from e to powers of two; masked:
+// some e is hidden.
+template <int D, int MT, bool SPLIT>
+__device__ __forceinline__ void weigh(const float (&e)[MT][8], v4u (&vs)[D / 64], const float (&c2)[MT], bool masked,
+                                      Sums<D, MT> &s, v4u (&w)[MT][D / 64], v4u (&w2)[MT][D / 64]) {
+  constexpr int G = D / kKvGroup;
+  float p[MT][8], top[MT], topp[MT];
+  auto form = [&]() __attribute__((always_inline)) {
+    // the scales stay packed: converted for both uses at once they would hold 8 G registers
+#pragma unroll
+    for (int g = 0; g < G; ++g) asm volatile("" : "+v"(vs[g]));
+    bool moved = false;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      topp[m] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[m][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(e[m][i], c2[m], -s.o[m]));
+        topp[m] = fmaxf(topp[m], p[m][i]);
+      }
+      top[m] = 0.0f;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float ps[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ps[i] = __builtin_fmaf(p[m][i], half_of(vs[g], i), 0.0f);
+        if (masked) {      // a hidden token's scale may be anything, NaN among it
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ps[i] = e[m][i] == kHidden ? 0.0f : ps[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top[m] = fmaxf(top[m], ps[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t hi = pack_h(ps[2 * i], ps[2 * i + 1]);   // (a bit_cast of w[m][g][i] reads w[m][g][0])
+          w[m][g][i] = hi;
+          if (SPLIT) {
+            const v2h h = __builtin_bit_cast(v2h, hi);
+            w2[m][g][i] = pack_h(ps[2 * i] - (float)h[0], ps[2 * i + 1] - (float)h[1]);
+          }
+        }
+      }
+      moved |= top[m] > kMaxPs || topp[m] > kMaxP;
+    }
+    return __any(moved) != 0;
+  };
+  if (__builtin_expect(form(), 0)) {
+    // rare: the rows that exceed the range take the offset of this tile's largest
+    // p s; one value at a time, since the registers used here are the kernel's
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float mine = top[m] > kMaxPs || topp[m] > kMaxP ? 1.0f : 0.0f;
+      float most = kHidden;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          asm volatile("" : "+v"(vs[g]));
+          most = fmaxf(most, __builtin_fmaf(e[m][i], c2[m], __builtin_amdgcn_logf(fmaxf(half_of(vs[g], i), kTiny))));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      most = max_over<16, 32>(most);
+      const bool move = max_over<16, 32>(mine) > 0.0f;
+      const float o = move ? __builtin_ceilf(most) - kTop : s.o[m];
+      const float al = move ? __builtin_amdgcn_exp2f(s.o[m] - o) : 1.0f;
+      s.o[m] = o;
+      s.l[m] *= al;
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) s.acc[m][n] *= al;
+#pragma unroll
+      for (int g = 0; g < G; ++g) s.zero[m][g] *= al;
+    }
+    form();
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s.l[m] += p[m][i];
+}
+
+// The second product.
+template <int D, int MT, bool SPLIT>
+__device__ __forceinline__ void values(const Side<D> &t, const v4u (&w)[MT][D / 64], const v4u (&w2)[MT][D / 64],
+                                       Sums<D, MT> &s) {
+#pragma unroll
+  for (int g = 0; g < D / kKvGroup; ++g) {
+    const uint32_t z0 = t.z[g][0], z1 = t.z[g][1];
+    const v4u zz = {z0 & kLow, z0 >> 8 & kLow, z1 & kLow, z1 >> 8 & kLow};
+    const v4u zh = {z0 << 4 & kHigh, z0 >> 4 & kHigh, z1 << 4 & kHigh, z1 >> 4 & kHigh};
+    if (!SPLIT) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) s.zero[m][g] = mfma16(zz, w[m][g], s.zero[m][g]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {         // channels 32 p ..: 32 tokens in two dwords
+      const int pr = 2 * g + h;
+      const uint32_t v0 = t.code[pr >> 1][2 * (pr & 1)], v1 = t.code[pr >> 1][2 * (pr & 1) + 1], u0 = v0 >> 8, u1 = v1 >> 8;
+      v4u b0 = {v0 & kLow, u0 & kLow, v1 & kLow, u1 & kLow}, b1 = {v0 & kHigh, u0 & kHigh, v1 & kHigh, u1 & kHigh};
+      if (SPLIT) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          b0[i] = minus_h(b0[i], zz[i]);
+          b1[i] = minus_h(b1[i], zh[i]);
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        s.acc[m][2 * pr] = mfma16(b0, w[m][g], s.acc[m][2 * pr]);
+        s.acc[m][2 * pr + 1] = mfma16(b1, w[m][g], s.acc[m][2 * pr + 1]);
+        if (SPLIT) {
+          s.acc[m][2 * pr] = mfma16(b0, w2[m][g], s.acc[m][2 * pr]);
+          s.acc[m][2 * pr + 1] = mfma16(b1, w2[m][g], s.acc[m][2 * pr + 1]);
+        }
+      }
+    }
+  }
+}
+
+// Where a workgroup of rows [r0, ..) of a sequence stands.
+struct Place {
+  int b, h, part, start, rows, len, p0;
+};
+__device__ __forceinline__ Place place_of(const KvAttnArgs &a, int splits) {
+  Place c;
+  c.h = blockIdx.y;
+  c.part = splits == 1 ? 0 : blockIdx.z % splits;
+  c.b = splits == 1 ? blockIdx.z : blockIdx.z / splits;
+  int n;
+  kv_rows(a.c, c.b, c.start, n);
+  c.rows = n * a.gr;
+  c.len = kv_len(a.c, c.b);
+  c.p0 = max(a.c.lens[c.b], 0) - n;
+  return c;
+}
+
+// The sums of a workgroup's waves, in LDS as [wave][row][D + 4] and (offset,
+// weight) [wave][row], joined and stored: the result, or a part of it.
+template <int D, int ROWS, int W>
+__device__ __forceinline__ void join_waves(const KvAttnArgs &a, const Place &c, int r0, const float *lds, const float2 *ol) {
+  constexpr int kLd = D + 4;
+  for (int i = threadIdx.x; i < ROWS * (D / 4); i += 64 * W) {
+    const int row = i / (D / 4), d = i % (D / 4) * 4, rr = r0 + row;
+    if (rr >= c.rows) continue;
+    float o = kNoOffset, l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float v = ol[w * ROWS + row].x;
+      o = v != v || v > o ? v : o;
+    }
+    v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 u = ol[w * ROWS + row];
+      const float f = __builtin_amdgcn_exp2f(u.x - o);
+      l = __builtin_fmaf(u.y, f, l);
+      const v4f v = *reinterpret_cast<const v4f *>(lds + (w * ROWS + row) * kLd + d);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(v[r], f, y[r]);
+    }
+    const int ti = rr / a.gr;
+    const size_t yr = (size_t)(c.start + ti) * a.Hq + c.h * a.gr + (rr - ti * a.gr);
+    if (a.splits == 1) {
+      store_y(a, yr * D + d, y * inverse(l));
+      if (a.lse && d == 0) a.lse[yr] = lse_of(o, l);
+    } else {
+      *reinterpret_cast<v4f *>(a.part + (yr * a.splits + c.part) * D + d) = y;
+      if (d == 0) a.part_ol[yr * a.splits + c.part] = make_float2(o, l);
+    }
+  }
+}
+
+template <int D, int MT, int W, bool SPLIT, bool ROWS>
+__global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) void k_kv_attention(KvAttnArgs a) {
   constexpr int G = D / kKvGroup, kRows = 16 * MT * (ROWS ? W : 1), kLd = D + 4;
   extern __shared__ float lds[];
   const int lane = threadIdx.x & 63, q = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  int id = blockIdx.x;
-  const int blk = blocks - 1 - id % blocks;     // the last rows see the most: first
-  id /= blocks;
-  const int h = id % a.c.H;
-  id /= a.c.H;
-  const int part = ROWS ? 0 : id % a.splits, b = ROWS ? id : id / a.splits;
-  int start, n;
-  kv_rows(a.c, b, start, n);
-  const int rows = n * a.gr, r0 = blk * kRows + (ROWS ? wave * 16 * MT : 0);
-  if (r0 >= rows) return;
-  const int len = kv_len(a.c, b), p0 = max(a.c.lens[b], 0) - n;
+  const Place c = place_of(a, ROWS ? 1 : a.splits);
+  // the last rows see the most: first
+  const int r0 = (int)(gridDim.x - 1 - blockIdx.x) * kRows + (ROWS ? wave * 16 * MT : 0);
+  if (r0 >= c.rows) return;
+  const int r1 = min(r0 + 16 * MT, c.rows);
   int first, last;
-  tiles_of_rows(a, r0, min(r0 + 16 * MT, rows), p0, len, first, last);
+  tiles_of_rows(a, r0, r1, c.p0, c.len, first, last);
   if (!ROWS) {
     const int per = tiles_of_part(first, last, a.splits);
-    first += part * per;
-    if (part > 0 && first >= last) return;
+    first += c.part * per;
+    if (c.part > 0 && first >= last) return;
     last = min(last, first + per);
   }
-
   // this lane's queries
   v4u Q[MT][D / 32];
-  float qs[MT][G];
+  float qs[MT][G], c2[MT];
   int lo[MT], hi[MT];
-  int full_lo = 0, full_hi = 1 << 30;           // tokens that every row of the wave sees
-  size_t at[MT];                                // row of Y (heads counted), or none
+  size_t at[MT];                                // row of Y (heads counted)
   bool live[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int row = r0 + 16 * m + col;
-    live[m] = row < rows;
-    const int i = min(row, rows - 1) / a.gr, head = h * a.gr + (live[m] ? row - i * a.gr : 0);
-    const Seen s = seen_by(a, i, p0, len);
+    live[m] = row < c.rows;
+    const int i = min(row, c.rows - 1) / a.gr, head = c.h * a.gr + (live[m] ? row - i * a.gr : 0);
+    const Seen s = seen_by(a, i, c.p0, c.len);
     lo[m] = s.lo;
     hi[m] = s.hi;
-    at[m] = (size_t)(start + i) * a.Hq + head;
-    const uint16_t *src = a.Q + (size_t)(start + i) * a.q_stride + (size_t)head * D + 8 * q;
+    at[m] = (size_t)(c.start + i) * a.Hq + head;
+    const uint16_t *src = a.Q + (size_t)(c.start + i) * a.q_stride + (size_t)head * D + 8 * q;
+    float top = 0.0f;
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x)
+    for (int x = 0; x < D / 32; ++x) {
       Q[m][x] = live[m] ? *reinterpret_cast<const v4u *>(src + 32 * x) : (v4u){0u, 0u, 0u, 0u};
-    constexpr uint32_t one = DT == kBf16 ? 0x3F803F80u : 0x3C003C00u;
-    const v4u ones = {one, one, one, one};
+      top = fmaxf(top, largest8(Q[m][x], a.dtype));
+    }
+    const float by = row_power(max_over<16, 32>(top), a.scale2, c2[m]);
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) Q[m][x] = scaled8(Q[m][x], a.dtype, by);
+    const v4u ones = {0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u};   // codes of 1
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      v4f d = mfma16<DT>(ones, Q[m][2 * g], (v4f){0.0f, 0.0f, 0.0f, 0.0f});
-      d = mfma16<DT>(ones, Q[m][2 * g + 1], d);
+      v4f d = mfma16(ones, Q[m][2 * g], (v4f){0.0f, 0.0f, 0.0f, 0.0f});
+      d = mfma16(ones, Q[m][2 * g + 1], d);
       qs[m][g] = d[0];
     }
   }
-  {
-    const Seen s0 = seen_by(a, r0 / a.gr, p0, len), s1 = seen_by(a, (min(r0 + 16 * MT, rows) - 1) / a.gr, p0, len);
-    full_lo = s1.lo;
-    full_hi = s0.hi;
-  }
+  // tokens that every row of the wave sees
+  const int full_lo = seen_by(a, (r1 - 1) / a.gr, c.p0, c.len).lo, full_hi = seen_by(a, r0 / a.gr, c.p0, c.len).hi;
   Sums<D, MT> s;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -357,20 +480,62 @@ __global__ __launch_bounds__(64 * W) void k_kv_attention(KvAttnArgs a, int block
     s.l[m] = 0.0f;
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) s.acc[m][x] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int g = 0; g < G; ++g) s.zero[m][g] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
   }
-  for (int tile = first + (ROWS ? 0 : wave); tile < last; tile += ROWS ? 1 : W) {
-    const uint8_t *p = kv_tile_at(a.c, b, h, tile);
-    if (!p) continue;                           // on no page: not there
-    TileRegs<D> t;
-    load_tile<D>(p, lane, t);
-    const int t0 = tile * kKvTile;
-    if (t0 >= full_lo && t0 + kKvTile <= full_hi)
-      step<D, MT, DT, SPLIT, false>(t, Q, qs, a.scale2, t0, lo, hi, s);
-    else
-      step<D, MT, DT, SPLIT, true>(t, Q, qs, a.scale2, t0, lo, hi, s);
+  // A side's registers are loaded again as soon as they have been used: the next
+  // keys travel while this tile's weights and values are worked on, the next
+  // values while its scores are.  A tile on no page reads page 0 and is hidden.
+  constexpr int kStep = ROWS ? 1 : W;
+  int tile = first + (ROWS ? 0 : wave);
+  if (tile < last) {
+    Side<D> tk, tv;
+    const uint8_t *p = kv_tile_at(a.c, c.b, c.h, tile);
+    bool there = p != nullptr;
+    if (!there) p = a.c.cache;
+    load_side<D, false>(p, lane, tk);
+    load_side<D, true>(p, lane, tv);
+    for (;;) {
+      const int next = tile + kStep;
+      const uint8_t *pn = kv_tile_at(a.c, c.b, c.h, min(next, last - 1));
+      const bool there_n = pn != nullptr;
+      if (!there_n) pn = a.c.cache;
+      float e[MT][8];
+      scores<D, MT>(tk, Q, qs, e);
+      __builtin_amdgcn_sched_barrier(0);
+      load_side<D, false>(pn, lane, tk);
+      __builtin_amdgcn_sched_barrier(0);
+      const int t0 = tile * kKvTile;
+      const bool masked = t0 < full_lo || t0 + kKvTile > full_hi || !there;
+      if (masked) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int tok = t0 + 16 * (i >> 2) + 4 * q + (i & 3);
+            if (tok < lo[m] || tok >= hi[m] || !there) e[m][i] = kHidden;
+          }
+      }
+      v4u w[MT][G], w2[MT][G];
+      weigh<D, MT, SPLIT>(e, tv.s, c2, masked, s, w, w2);
+      values<D, MT, SPLIT>(tv, w, w2, s);
+      if (next >= last) break;
+      __builtin_amdgcn_sched_barrier(0);
+      load_side<D, true>(pn, lane, tv);
+      __builtin_amdgcn_sched_barrier(0);
+      tile = next;
+      there = there_n;
+    }
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) s.l[m] = over_q(s.l[m], true);
+  for (int m = 0; m < MT; ++m) {
+    s.l[m] = sum_over<16, 32>(s.l[m]);
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x) {
+      const float up = x & 1 ? 1048576.0f : 16777216.0f;
+      s.acc[m][x] = s.acc[m][x] * up - s.zero[m][x / 4] * 16777216.0f;
+    }
+  }
   if (ROWS) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -382,7 +547,6 @@ __global__ __launch_bounds__(64 * W) void k_kv_attention(KvAttnArgs a, int block
     }
     return;
   }
-  // the waves' sums meet in LDS: [wave][row][D + 4], then (offset, weight) [wave][row]
   float2 *ol = reinterpret_cast<float2 *>(lds + W * 16 * MT * kLd);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -392,109 +556,449 @@ __global__ __launch_bounds__(64 * W) void k_kv_attention(KvAttnArgs a, int block
     if (q == 0) ol[row] = make_float2(s.o[m], s.l[m]);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * MT * (D / 4); i += 64 * W) {
-    const int row = i / (D / 4), d = i % (D / 4) * 4, rr = r0 + row;
-    if (rr >= rows) continue;
-    float o = kNoOffset, l = 0.0f;
+  join_waves<D, 16 * MT, W>(a, c, r0, lds, ol);
+}
+
+// ------------------------------------------------------------------ 4 x 4
+// A lane's half u = lane / 32 has groups 2 j + u (j < kSets), or, where there is one
+// group, the second of two tiles.  As a token t = lane % 32 (= 4 c + r): its
+// group's channels, two dwords of each lane slot t % 16 + 16 q; the scales and zeros
+// of the four tokens 4 c ...  As channels: 32 p + lane % 16 and 16 more, p = 2 g +
+// (lane / 16) % 2, the tokens 16 a + 4 q .. as dword 2 p + a of slot lane % 16 + 16 q.
+template <int D>
+struct Side4 {
+  static constexpr int kSets = D <= 128 ? 1 : D / 128;
+  v2u code[kSets][4], s[kSets];
+  uint32_t z[kSets];
+};
+
+template <int D, bool V>
+__device__ __forceinline__ void load_side4(const uint8_t *p, int lane, Side4<D> &t) {
+  constexpr int G = D / kKvGroup;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float v = ol[w * 16 * MT + row].x;
-      o = v != v || v > o ? v : o;
-    }
-    v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int j = 0; j < Side4<D>::kSets; ++j) {
+    const int g = G == 1 ? 0 : 2 * j + (lane >> 5), c = (lane >> 2) & 7;
+    const int x = V ? 2 * (2 * g + ((lane >> 4) & 1)) : ((lane >> 4) & 1) * (D / 32) + 2 * g;
+    const uint8_t *at = p + (V ? 16 * D : 0) + (x >> 2) * 1024 + (x & 3) * 4 + (lane & 15) * 16;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float2 u = ol[w * 16 * MT + row];
-      const float f = __builtin_amdgcn_exp2f(u.x - o);
-      l = __builtin_fmaf(u.y, f, l);
-      const v4f v = *reinterpret_cast<const v4f *>(lds + (w * 16 * MT + row) * kLd + d);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) y[r] = __builtin_fmaf(v[r], f, y[r]);
-    }
-    const int ti = rr / a.gr;
-    const size_t yr = (size_t)(start + ti) * a.Hq + h * a.gr + (rr - ti * a.gr);
-    if (a.splits == 1) {
-      store_y(a, yr * D + d, y * inverse(l));
-      if (a.lse && d == 0) a.lse[yr] = lse_of(o, l);
-    } else {
-      *reinterpret_cast<v4f *>(a.part + (yr * a.splits + part) * D + d) = y;
-      if (d == 0) a.part_ol[yr * a.splits + part] = make_float2(o, l);
-    }
+    for (int q = 0; q < 4; ++q) t.code[j][q] = *reinterpret_cast<const v2u *>(at + q * 256);
+    t.s[j] = *reinterpret_cast<const v2u *>(p + 32 * D + (V ? 64 * G : 0) + g * 64 + (c & 3) * 16 + (c >> 2) * 8);
+    t.z[j] = *reinterpret_cast<const uint32_t *>(p + 32 * D + 128 * G + (V ? 32 * G : 0) + ((c & 3) * G + g) * 8 + (c >> 2) * 4);
   }
 }
 
-// The parts of a row, in order: a wave a row, D / 4 lanes of it at work.
+// The zeros of all 32 tokens, as a lane of channels meets them: [q][a].
 template <int D>
-__global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a, int blocks, int block_rows) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int id = blockIdx.x;
-  const int blk = id % blocks;
-  id /= blocks;
-  const int h = id % a.c.H, b = id / a.c.H;
+__device__ __forceinline__ void load_zeros4(const uint8_t *p, int lane, v2u (&z)[Side4<D>::kSets][4]) {
+  constexpr int G = D / kKvGroup;
+#pragma unroll
+  for (int j = 0; j < Side4<D>::kSets; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      z[j][q] = *reinterpret_cast<const v2u *>(p + 32 * D + 160 * G + (q * G + (G == 1 ? 0 : 2 * j + (lane >> 5))) * 8);
+}
+
+// Sums of a wave: R sets of four rows; lane's row of each is lane % 4 in o, l, zero
+// (and there its tokens only), the four of acc are rows.
+template <int D, int R>
+struct Sums4 {
+  static constexpr int kSets = Side4<D>::kSets;
+  v4f low[R][kSets], high[R][kSets];   // channels 32 p + lane % 16 (times 2^-24), and 16 more (2^-20)
+  float zero[R][kSets], o[R], l[R];
+};
+
+template <int I>
+__device__ __forceinline__ float quad(float v) {   // of lane I of the four
+  return dpp_f32<I * 0x55>(v);
+}
+
+template <int D, int R, bool SPLIT, int... C>
+__device__ __forceinline__ void values4(const Side4<D> &t, const v2u (&w)[R][Side4<D>::kSets],
+                                        const v2u (&w2)[R][Side4<D>::kSets],
+                                        const v2u (&z)[Side4<D>::kSets][4], Sums4<D, R> &s,
+                                        std::integer_sequence<int, C...>) {
+  auto chunk = [&](auto ic) __attribute__((always_inline)) {
+    constexpr int c = decltype(ic)::value;     // tokens 4 c ..: a = c / 4, q = c % 4
+#pragma unroll
+    for (int j = 0; j < Side4<D>::kSets; ++j) {
+      const uint32_t v = t.code[j][c & 3][c >> 2], u = v >> 8;
+      v2u lo = {v & kLow, u & kLow}, hi = {v & kHigh, u & kHigh};
+      if (SPLIT) {
+        const uint32_t x = z[j][c & 3][c >> 2];
+        lo = (v2u){minus_h(lo[0], x & kLow), minus_h(lo[1], x >> 8 & kLow)};
+        hi = (v2u){minus_h(hi[0], x << 4 & kHigh), minus_h(hi[1], x >> 4 & kHigh)};
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        s.low[r][j] = mfma4<c>(w[r][j], lo, s.low[r][j]);
+        s.high[r][j] = mfma4<c>(w[r][j], hi, s.high[r][j]);
+        if (SPLIT) {
+          s.low[r][j] = mfma4<c>(w2[r][j], lo, s.low[r][j]);
+          s.high[r][j] = mfma4<c>(w2[r][j], hi, s.high[r][j]);
+        }
+      }
+    }
+  };
+  (chunk(std::integral_constant<int, C>{}), ...);
+}
+
+template <int D, int R, int W, bool SPLIT>
+__global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? (D == 64 ? 4 : 3) : 2) void k_kv_attention4(KvAttnArgs a) {
+  constexpr int G = D / kKvGroup, kSets = Side4<D>::kSets, kTiles = G == 1 ? 2 : 1, kRows = 4 * R, kLd = D + 4;
+  __shared__ float lds[W * kRows * kLd];
+  __shared__ float2 ol[W * kRows];
+  const int lane = threadIdx.x & 63, half = lane >> 5, c4 = (lane >> 2) & 7, j4 = lane & 3;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Place c = place_of(a, a.splits);
+  const int r0 = blockIdx.x * kRows;
+  if (r0 >= c.rows) return;
+  const int r1 = min(r0 + kRows, c.rows);
+  int first, last;
+  tiles_of_rows(a, r0, r1, c.p0, c.len, first, last);
+  const int per = tiles_of_part(first, last, a.splits);
+  first += c.part * per;
+  if (c.part > 0 && first >= last) return;
+  last = min(last, first + per);
+
+  // the first tiles' pages, keys and values are on their way before the queries are
+  int tile = first + wave * kTiles;
+  const uint8_t *p = a.c.cache;
+  bool there = false;
+  Side4<D> tk, tv;
+  auto locate = [&](int t, const uint8_t *&at, bool &is) __attribute__((always_inline)) {
+    const uint8_t *x = t < last ? kv_tile_at(a.c, c.b, c.h, t) : nullptr;
+    if (kTiles == 2) {
+      const uint8_t *y = t + 1 < last ? kv_tile_at(a.c, c.b, c.h, t + 1) : nullptr;
+      x = half ? y : x;
+    }
+    is = x != nullptr;
+    at = is ? x : a.c.cache;
+  };
+  locate(tile, p, there);
+  load_side4<D, false>(p, lane, tk);
+  load_side4<D, true>(p, lane, tv);
+  v2u zeros[kSets][4];
+  if (SPLIT) load_zeros4<D>(p, lane, zeros);
+
+  // Q: dims 64 g + 32 i + 8 q .. of row j4, eight at a time
+  v4u Q[R][kSets][8];
+  float qs[R][kSets], c2[R];
+  int lo[R], hi[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = r0 + 4 * r + j4, i = min(row, c.rows - 1) / a.gr;
+    const bool live = row < c.rows;
+    const int head = c.h * a.gr + (live ? row - i * a.gr : 0);
+    const Seen s = seen_by(a, i, c.p0, c.len);
+    lo[r] = s.lo;
+    hi[r] = s.hi;
+    const uint16_t *src = a.Q + (size_t)(c.start + i) * a.q_stride + (size_t)head * D;
+    float top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kSets; ++j)
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int g = G == 1 ? 0 : 2 * j + half;
+        Q[r][j][n] = live ? *reinterpret_cast<const v4u *>(src + 64 * g + 32 * (n & 1) + 8 * (n >> 1)) : (v4u){0u, 0u, 0u, 0u};
+        top = fmaxf(top, largest8(Q[r][j][n], a.dtype));
+      }
+    if (G > 1) top = max_over<32, 32>(top);
+    const float by = row_power(top, a.scale2, c2[r]);
+#pragma unroll
+    for (int j = 0; j < kSets; ++j) {
+      v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        Q[r][j][n] = scaled8(Q[r][j][n], a.dtype, by);
+        d = mfma4<-1>((v2u){0x00010001u, 0x00010001u}, (v2u){Q[r][j][n][0], Q[r][j][n][1]}, d);   // codes of 1
+        d = mfma4<-1>((v2u){0x00100010u, 0x00100010u}, (v2u){Q[r][j][n][2], Q[r][j][n][3]}, d);
+      }
+      qs[r][j] = d[0];
+    }
+  }
+  const int full_lo = seen_by(a, (r1 - 1) / a.gr, c.p0, c.len).lo, full_hi = seen_by(a, r0 / a.gr, c.p0, c.len).hi;
+  Sums4<D, R> s;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    s.o[r] = kNoOffset;
+    s.l[r] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kSets; ++j) {
+      s.low[r][j] = s.high[r][j] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+      s.zero[r][j] = 0.0f;
+    }
+  }
+
+  for (; tile < last;) {
+    const int next = tile + W * kTiles;
+    const uint8_t *pn;
+    bool there_n;
+    locate(min(next, last - 1), pn, there_n);
+    // scores of tokens 4 c4 + i, this half's groups, then all
+    float e[R][4];
+#pragma unroll
+    for (int j = 0; j < kSets; ++j) {
+      v4f d[R][2];
+#pragma unroll
+      for (int r = 0; r < R; ++r) d[r][0] = d[r][1] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const uint32_t w = tk.code[j][n >> 1][n & 1], v = w >> 8;
+        const v2u lo2 = {w & kLow, v & kLow}, hi2 = {w & kHigh, v & kHigh};
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          d[r][0] = mfma4<-1>(lo2, (v2u){Q[r][j][n][0], Q[r][j][n][1]}, d[r][0]);
+          d[r][1] = mfma4<-1>(hi2, (v2u){Q[r][j][n][2], Q[r][j][n][3]}, d[r][1]);
+        }
+      }
+      const uint32_t zw = tk.z[j] & 0x0F0F0F0Fu;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float u = __builtin_fmaf(-zero_of(zw, i), qs[r][j], d[r][0][i] + d[r][1][i]);
+          e[r][i] = __builtin_fmaf(u, half_of(tk.s[j], i), j ? e[r][i] : 0.0f);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    load_side4<D, false>(pn, lane, tk);
+    __builtin_amdgcn_sched_barrier(0);
+    if (G > 1) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = __float_as_uint(e[r][i]);
+          const auto y = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+          e[r][i] = __uint_as_float(y[0]) + __uint_as_float(y[1]);
+        }
+    }
+    const int t0 = tile * kKvTile;
+    const bool masked = t0 < full_lo || t0 + kTiles * kKvTile > full_hi || !__all(there);
+    if (masked) {
+      const int tok0 = t0 + (kTiles == 2 ? 32 * half : 0) + 4 * c4;
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tok0 + i < lo[r] || tok0 + i >= hi[r] || !there) e[r][i] = kHidden;
+    }
+    // weights
+    v2u w[R][kSets], w2[R][kSets];
+    float pw[R][4], ps[R][kSets][4], top[R], topp[R];
+    auto form = [&]() __attribute__((always_inline)) {
+      bool moved = false;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        top[r] = topp[r] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          pw[r][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(e[r][i], c2[r], -s.o[r]));
+          topp[r] = fmaxf(topp[r], pw[r][i]);
+        }
+#pragma unroll
+        for (int j = 0; j < kSets; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            ps[r][j][i] = __builtin_fmaf(pw[r][i], half_of(tv.s[j], i), 0.0f);
+            // a hidden token's scale may be anything, NaN among it
+            if (masked) ps[r][j][i] = e[r][i] == kHidden ? 0.0f : ps[r][j][i];
+            top[r] = fmaxf(top[r], ps[r][j][i]);
+          }
+        moved |= top[r] > kMaxPs || topp[r] > kMaxP;
+      }
+      return __any(moved) != 0;
+    };
+    if (__builtin_expect(form(), 0)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float mine = top[r] > kMaxPs || topp[r] > kMaxP ? 1.0f : 0.0f;
+        float most = kHidden;
+#pragma unroll
+        for (int j = 0; j < kSets; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!masked || e[r][i] != kHidden)
+              most = fmaxf(most, __builtin_fmaf(e[r][i], c2[r], __builtin_amdgcn_logf(fmaxf(half_of(tv.s[j], i), kTiny))));
+        most = max_over<4, 32>(most);
+        const bool move = max_over<4, 32>(mine) > 0.0f;
+        const float o = move ? __builtin_ceilf(most) - kTop : s.o[r];
+        const float al = move ? __builtin_amdgcn_exp2f(s.o[r] - o) : 1.0f;
+        s.o[r] = o;
+        s.l[r] *= al;
+        const v4f rows = {quad<0>(al), quad<1>(al), quad<2>(al), quad<3>(al)};
+#pragma unroll
+        for (int j = 0; j < kSets; ++j) {
+          s.zero[r][j] *= al;
+          s.low[r][j] *= rows;
+          s.high[r][j] *= rows;
+        }
+      }
+      form();
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s.l[r] += pw[r][i];
+#pragma unroll
+      for (int j = 0; j < kSets; ++j) {
+        const uint32_t zw = tv.z[j] & 0x0F0F0F0Fu;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t x = pack_h(ps[r][j][2 * i], ps[r][j][2 * i + 1]);
+          w[r][j][i] = x;
+          const v2h h = __builtin_bit_cast(v2h, x);
+          if (SPLIT) w2[r][j][i] = pack_h(ps[r][j][2 * i] - (float)h[0], ps[r][j][2 * i + 1] - (float)h[1]);
+          // the zeros' share of what the product will hold: of the rounded weights
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+            if (!SPLIT) s.zero[r][j] = __builtin_fmaf((float)h[y], zero_of(zw, 2 * i + y), s.zero[r][j]);
+        }
+      }
+    }
+    values4<D, R, SPLIT>(tv, w, w2, zeros, s, std::make_integer_sequence<int, 8>{});
+    __builtin_amdgcn_sched_barrier(0);
+    load_side4<D, true>(pn, lane, tv);
+    if (SPLIT) load_zeros4<D>(pn, lane, zeros);
+    __builtin_amdgcn_sched_barrier(0);
+    tile = next;
+    there = there_n;
+  }
+  // rows of channels, less the zeros' share; the sums over tokens of o, l are a row's
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float l = G == 1 ? sum_over<4, 32>(s.l[r]) : sum_over<4, 16>(s.l[r]);
+    if (lane < 4) ol[wave * kRows + 4 * r + lane] = make_float2(s.o[r], l);
+#pragma unroll
+    for (int j = 0; j < kSets; ++j) {
+      const float z = sum_over<4, 16>(s.zero[r][j]);
+      const v4f zr = {quad<0>(z), quad<1>(z), quad<2>(z), quad<3>(z)};
+      v4f y0 = s.low[r][j] * 16777216.0f - zr, y1 = s.high[r][j] * 1048576.0f - zr;
+      if (G == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y0[i] = sum_over<32, 32>(y0[i]);
+          y1[i] = sum_over<32, 32>(y1[i]);
+        }
+      }
+      const int g = G == 1 ? 0 : 2 * j + half, ch = 32 * (2 * g + ((lane >> 4) & 1)) + (lane & 15);
+      if (G > 1 || half == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lds[(wave * kRows + 4 * r + i) * kLd + ch] = y0[i];
+          lds[(wave * kRows + 4 * r + i) * kLd + ch + 16] = y1[i];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  join_waves<D, kRows, W>(a, c, r0, lds, ol);
+}
+
+// The parts of a row: groups of D / 4 lanes take every kGroups-th part, and their
+// sums meet in order.
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a, int block_rows) {
+  constexpr int kLanes = D / 4, kGroups = 256 / kLanes;
+  __shared__ float l_of[kGroups];
+  __shared__ v4f y_of[kGroups][kLanes];
+  const int tid = threadIdx.x, lane = tid % kLanes, grp = tid / kLanes, r = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   int start, n;
   kv_rows(a.c, b, start, n);
-  const int rows = n * a.gr, r0 = blk * block_rows;
-  if (r0 >= rows) return;
+  const int rows = n * a.gr, r0 = r / block_rows * block_rows;
+  if (r >= rows) return;
   const int len = kv_len(a.c, b), p0 = max(a.c.lens[b], 0) - n;
   int first, last;
   tiles_of_rows(a, r0, min(r0 + block_rows, rows), p0, len, first, last);
   const int per = tiles_of_part(first, last, a.splits), parts = max(1, (last - first + per - 1) / per);
-  for (int r = wave; r < block_rows && r0 + r < rows; r += 4) {
-    const int ti = (r0 + r) / a.gr;
-    const size_t yr = (size_t)(start + ti) * a.Hq + h * a.gr + (r0 + r - ti * a.gr);
-    const float2 *ol = a.part_ol + yr * a.splits;
-    float o = kNoOffset, l = 0.0f;
-    for (int w = 0; w < parts; ++w) {
-      const float v = ol[w].x;
-      o = v != v || v > o ? v : o;
-    }
-    if (lane * 4 >= D) continue;
-    v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int w = 0; w < parts; ++w) {
-      const float f = __builtin_amdgcn_exp2f(ol[w].x - o);
-      l = __builtin_fmaf(ol[w].y, f, l);
-      const v4f v = *reinterpret_cast<const v4f *>(a.part + (yr * a.splits + w) * D + lane * 4);
+  const int ti = r / a.gr;
+  const size_t yr = (size_t)(start + ti) * a.Hq + h * a.gr + (r - ti * a.gr);
+  const float2 *ol = a.part_ol + yr * a.splits;
+  const float *part = a.part + yr * a.splits * D + lane * 4;
+  // splits <= kMaxParts: this group's parts, all on their way at once
+  constexpr int kMine = kMaxParts / kGroups;
+  v4f v[kMine];
+  float2 u[kMine];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(v[e], f, y[e]);
-    }
-    store_y(a, yr * D + lane * 4, y * inverse(l));
-    if (a.lse && lane == 0) a.lse[yr] = lse_of(o, l);
+  for (int i = 0; i < kMine; ++i) {
+    const int w = min(grp + i * kGroups, parts - 1);
+    u[i] = ol[w];
+    v[i] = *reinterpret_cast<const v4f *>(part + (size_t)w * D);
   }
+  float o = kNoOffset, l = 0.0f;
+  for (int w = 0; w < parts; w += 64) {       // the largest offset, NaN above all
+    const float x = ol[min(w + (tid & 63), parts - 1)].x;
+    o = x != x || x > o ? x : o;
+  }
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) {
+    const float x = __shfl_xor(o, m);
+    o = x != x || x > o ? x : o;
+  }
+  v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    if (grp + i * kGroups >= parts) continue;
+    const float f = __builtin_amdgcn_exp2f(u[i].x - o);
+    l = __builtin_fmaf(u[i].y, f, l);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(v[i][e], f, y[e]);
+  }
+  y_of[grp][lane] = y;
+  if (lane == 0) l_of[grp] = l;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int g = 1; g < kGroups; ++g) {
+    y += y_of[g][lane];
+    l += l_of[g];
+  }
+  store_y(a, yr * D + lane * 4, y * inverse(l));
+  if (a.lse && lane == 0) a.lse[yr] = lse_of(o, l);
 }
 
-template <int D, int MT, int W, bool ROWS>
-hipError_t launch_cfg(const KvAttnArgs &a, hipStream_t s) {
-  constexpr int kRows = 16 * MT * (ROWS ? W : 1);
-  const int blocks = ceil_div(a.c.max_tokens * a.gr, kRows);
-  const unsigned grid = (unsigned)blocks * a.c.H * a.c.B * (ROWS ? 1 : a.splits);
-  const size_t lds = ROWS ? 0 : (size_t)W * 16 * MT * ((D + 4) * sizeof(float) + sizeof(float2));
-  auto go = [&](auto kernel) {
-    if (lds > 64 * 1024) {
-      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-      if (e != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(64 * W), lds, s, a, blocks);
-    return hipGetLastError();
-  };
-  hipError_t e;
-  if (a.dtype == kBf16)
-    e = a.y_dtype == kF32 ? go(k_kv_attention<D, MT, W, kBf16, true, ROWS>)
-                          : go(k_kv_attention<D, MT, W, kBf16, false, ROWS>);
-  else
-    e = a.y_dtype == kF32 ? go(k_kv_attention<D, MT, W, kF16, true, ROWS>)
-                          : go(k_kv_attention<D, MT, W, kF16, false, ROWS>);
-  if (e == hipSuccess && !ROWS && a.splits > 1) {
-    hipLaunchKernelGGL((k_kv_join<D>), dim3((unsigned)blocks * a.c.H * a.c.B), dim3(256), 0, s, a, blocks, kRows);
-    e = hipGetLastError();
+template <typename Kernel>
+hipError_t go(Kernel kernel, dim3 grid, int threads, size_t lds, const KvAttnArgs &a, hipStream_t s) {
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
   }
-  return e;
+  hipLaunchKernelGGL(kernel, grid, dim3((unsigned)threads), lds, s, a);
+  return hipGetLastError();
+}
+
+constexpr int kWaves = 4;
+
+template <int D, int MT, bool ROWS>
+hipError_t launch16(const KvAttnArgs &a, dim3 grid, hipStream_t s) {
+  const size_t lds = ROWS ? 0 : (size_t)kWaves * 16 * MT * ((D + 4) * sizeof(float) + sizeof(float2));
+  return a.y_dtype == kF32 ? go(k_kv_attention<D, MT, kWaves, true, ROWS>, grid, 64 * kWaves, lds, a, s)
+                           : go(k_kv_attention<D, MT, kWaves, false, ROWS>, grid, 64 * kWaves, lds, a, s);
+}
+
+template <int D, int R>
+hipError_t launch4(const KvAttnArgs &a, dim3 grid, hipStream_t s) {
+  return a.y_dtype == kF32 ? go(k_kv_attention4<D, R, kWaves, true>, grid, 64 * kWaves, 0, a, s)
+                           : go(k_kv_attention4<D, R, kWaves, false>, grid, 64 * kWaves, 0, a, s);
 }
 
 template <int D>
 hipError_t launch_d(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s) {
-  if (p.by_rows) return D == 256 ? launch_cfg<D, 1, 4, true>(a, s) : launch_cfg<D, D == 256 ? 1 : 2, 4, true>(a, s);
-  return launch_cfg<D, 1, D == 256 ? 4 : 8, false>(a, s);
+  const dim3 grid((unsigned)ceil_div(a.c.max_tokens * a.gr, p.rows), (unsigned)a.c.H, (unsigned)(a.c.B * p.splits));
+  hipError_t e;
+  constexpr int kMt = D == 256 ? 1 : 2;      // two row tiles of 256 channels would not fit the registers
+  if (p.by_rows) return launch16<D, kMt, true>(a, grid, s);
+  if (p.rows == 4) e = launch4<D, 1>(a, grid, s);
+  else if (p.rows == 8) e = launch4<D, D == 256 ? 1 : 2>(a, grid, s);
+  else if (p.rows == 16) e = launch16<D, 1, false>(a, grid, s);
+  else e = launch16<D, kMt, false>(a, grid, s);
+  if (e == hipSuccess && p.splits > 1) {
+    hipLaunchKernelGGL((k_kv_join<D>), dim3((unsigned)(a.c.max_tokens * a.gr), (unsigned)a.c.H, (unsigned)a.c.B), dim3(256),
+                       0, s, a, p.rows);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace
@@ -503,17 +1007,18 @@ KvAttnPlan plan_kv_attention(int T, int Hq, int H, int D, int B, int max_tokens,
   KvAttnPlan p;
   const long long rows = (long long)max_tokens * (Hq / H);
   p.by_rows = rows >= 64;
-  p.mt = p.by_rows && D < 256 ? 2 : 1;
-  p.waves = p.by_rows || D == 256 ? 4 : 8;
-  if (!p.by_rows) {
-    const long long wgs = ((rows + 15) / 16) * H * B;
-    const long long most = std::max<long long>(1, (capacity + kMinTiles * kKvTile - 1) / (kMinTiles * kKvTile));
-    p.splits = (int)std::min<long long>({std::max<long long>(1, 512 / wgs), most, 64});
-    if (p.splits > 1) {
-      const size_t parts = (size_t)T * Hq * p.splits;
-      p.part_off = align_up(parts * sizeof(float2), 256);
-      p.total = p.part_off + parts * D * sizeof(float);
-    }
+  if (p.by_rows) {
+    p.rows = kWaves * (D == 256 ? 16 : 32);
+    return p;
+  }
+  p.rows = rows <= 4 ? 4 : rows <= 8 && D < 256 ? 8 : rows <= 16 || D == 256 ? 16 : 32;
+  const long long wgs = (rows + p.rows - 1) / p.rows * H * B;
+  const long long most = std::max<long long>(1, (capacity + kMinTiles * kKvTile - 1) / (kMinTiles * kKvTile));
+  p.splits = (int)std::min<long long>({std::max<long long>(1, 2048 / wgs), most, kMaxParts});
+  if (p.splits > 1) {
+    const size_t parts = (size_t)T * Hq * p.splits;
+    p.part_off = align_up(parts * sizeof(float2), 256);
+    p.total = p.part_off + parts * D * sizeof(float);
   }
   return p;
 }
