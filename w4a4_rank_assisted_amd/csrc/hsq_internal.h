@@ -501,6 +501,7 @@ struct KvAttnArgs {
 struct KvAttnPlan {
   bool by_rows = false;
   int rows = 4;            // of a workgroup
+  int waves = 4;
   int splits = 1;
   size_t part_off = 0, total = 0;
 };

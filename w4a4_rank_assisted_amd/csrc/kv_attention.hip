@@ -82,7 +82,12 @@ __device__ __forceinline__ uint32_t minus_h(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ float half_of(v4u w, int i) { return f16_to_f32((uint16_t)(w[i >> 1] >> (16 * (i & 1)))); }
 __device__ __forceinline__ float half_of(v2u w, int i) { return f16_to_f32((uint16_t)(w[i >> 1] >> (16 * (i & 1)))); }
-// Zero r of four tokens in a dword (bytes 0, 2, 1, 3).
+// The zeros of four tokens in a dword (bytes 0, 2, 1, 3), masked at once.
+__device__ __forceinline__ uint32_t zeros_of(uint32_t w) {
+  w &= 0x0F0F0F0Fu;
+  asm("" : "+v"(w));      // else every byte is masked by itself
+  return w;
+}
 __device__ __forceinline__ float zero_of(uint32_t w, int r) {
   return (float)(w >> (8 * (((r & 1) << 1) | (r >> 1))) & 0xFFu);
 }
@@ -110,18 +115,26 @@ __device__ __forceinline__ void unpack8(v4u w, int dtype, float *f) {
     f[2 * e + 1] = dtype == kBf16 ? __uint_as_float(w[e] & 0xFFFF0000u) : f16_to_f32((uint16_t)(w[e] >> 16));
   }
 }
-__device__ __forceinline__ float largest8(v4u w, int dtype) {
-  float f[8], m = 0.0f;
-  unpack8(w, dtype, f);
+typedef unsigned short v2us __attribute__((ext_vector_type(2)));
+// The larger magnitudes of two pairs, by their bits: infinities and NaN on top.
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(v2us, a), __builtin_bit_cast(v2us, b & 0x7FFF7FFFu)));
+}
+__device__ __forceinline__ uint32_t larger8(uint32_t top, v4u w) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
-  return m;
+  for (int e = 0; e < 4; ++e) top = larger(top, w[e]);
+  return top;
+}
+__device__ __forceinline__ float magnitude(uint32_t top, int dtype) {
+  const uint32_t h = max(top & 0xFFFFu, top >> 16);
+  return dtype == kBf16 ? bf16_to_f32(h) : f16_to_f32((uint16_t)h);
 }
 __device__ __forceinline__ v4u scaled8(v4u w, int dtype, float by) {
   float f[8];
   unpack8(w, dtype, f);
-  return (v4u){pack_h(f[0] * by, f[1] * by), pack_h(f[2] * by, f[3] * by), pack_h(f[4] * by * 0.0625f, f[5] * by * 0.0625f),
-               pack_h(f[6] * by * 0.0625f, f[7] * by * 0.0625f)};
+  const float high = by * 0.0625f;
+  return (v4u){pack_h(f[0] * by, f[1] * by), pack_h(f[2] * by, f[3] * by), pack_h(f[4] * high, f[5] * high),
+               pack_h(f[6] * high, f[7] * high)};
 }
 // The power of two that takes a row's largest channel to [2^13, 2^14), and the
 // factor from the products' sums to scores in powers of two.
@@ -152,7 +165,7 @@ __device__ __forceinline__ void tiles_of_rows(const KvAttnArgs &a, int r0, int r
 }
 
 // Tiles of one part of [first, last).
-constexpr int kMinTiles = 16;             // a part is 512 tokens at least
+constexpr int kMinTiles = 32;             // a part is 1024 tokens at least
 constexpr int kMaxParts = 64;
 __device__ __forceinline__ int tiles_of_part(int first, int last, int splits) {
   return max((last - first + splits - 1) / splits, kMinTiles);
@@ -230,7 +243,7 @@ __device__ __forceinline__ void scores(const Side<D> &t, const v4u (&Q)[MT][D / 
         const uint32_t w = t.code[i >> 2][i & 3], v = w >> 8;
         k[x] = (v4u){w & kLow, v & kLow, w & kHigh, v & kHigh};
       }
-      const uint32_t zw = t.z[g][a] & 0x0F0F0F0Fu;
+      const uint32_t zw = zeros_of(t.z[g][a]);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         v4f d = mfma16(k[0], Q[m][2 * g], (v4f){0.0f, 0.0f, 0.0f, 0.0f});
@@ -454,13 +467,13 @@ __global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) 
     hi[m] = s.hi;
     at[m] = (size_t)(c.start + i) * a.Hq + head;
     const uint16_t *src = a.Q + (size_t)(c.start + i) * a.q_stride + (size_t)head * D + 8 * q;
-    float top = 0.0f;
+    uint32_t top = 0;
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) {
       Q[m][x] = live[m] ? *reinterpret_cast<const v4u *>(src + 32 * x) : (v4u){0u, 0u, 0u, 0u};
-      top = fmaxf(top, largest8(Q[m][x], a.dtype));
+      top = larger8(top, Q[m][x]);
     }
-    const float by = row_power(max_over<16, 32>(top), a.scale2, c2[m]);
+    const float by = row_power(max_over<16, 32>(magnitude(top, a.dtype)), a.scale2, c2[m]);
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) Q[m][x] = scaled8(Q[m][x], a.dtype, by);
     const v4u ones = {0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u};   // codes of 1
@@ -572,18 +585,27 @@ struct Side4 {
   uint32_t z[kSets];
 };
 
+// A lane's offsets within a tile: codes of K and V, scales, zeros of K (those of V
+// lie a constant further).
+struct Lane4 { uint32_t k, v, s, z; };
+template <int D>
+__device__ __forceinline__ Lane4 lane4(int lane, int j) {
+  constexpr int G = D / kKvGroup;
+  const uint32_t g = G == 1 ? 0 : 2 * j + (lane >> 5), c = (lane >> 2) & 7;
+  const uint32_t xk = ((lane >> 4) & 1) * (D / 32) + 2 * g, xv = 2 * (2 * g + ((lane >> 4) & 1)), slot = (lane & 15) * 16;
+  return {(xk >> 2) * 1024 + (xk & 3) * 4 + slot, 16 * D + (xv >> 2) * 1024 + (xv & 3) * 4 + slot,
+          32 * D + g * 64 + (c & 3) * 16 + (c >> 2) * 8, 32 * D + 128 * G + ((c & 3) * G + g) * 8 + (c >> 2) * 4};
+}
+
 template <int D, bool V>
-__device__ __forceinline__ void load_side4(const uint8_t *p, int lane, Side4<D> &t) {
+__device__ __forceinline__ void load_side4(const uint8_t *p, const Lane4 (&o)[Side4<D>::kSets], Side4<D> &t) {
   constexpr int G = D / kKvGroup;
 #pragma unroll
   for (int j = 0; j < Side4<D>::kSets; ++j) {
-    const int g = G == 1 ? 0 : 2 * j + (lane >> 5), c = (lane >> 2) & 7;
-    const int x = V ? 2 * (2 * g + ((lane >> 4) & 1)) : ((lane >> 4) & 1) * (D / 32) + 2 * g;
-    const uint8_t *at = p + (V ? 16 * D : 0) + (x >> 2) * 1024 + (x & 3) * 4 + (lane & 15) * 16;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) t.code[j][q] = *reinterpret_cast<const v2u *>(at + q * 256);
-    t.s[j] = *reinterpret_cast<const v2u *>(p + 32 * D + (V ? 64 * G : 0) + g * 64 + (c & 3) * 16 + (c >> 2) * 8);
-    t.z[j] = *reinterpret_cast<const uint32_t *>(p + 32 * D + 128 * G + (V ? 32 * G : 0) + ((c & 3) * G + g) * 8 + (c >> 2) * 4);
+    for (int q = 0; q < 4; ++q) t.code[j][q] = *reinterpret_cast<const v2u *>(p + (V ? o[j].v : o[j].k) + q * 256);
+    t.s[j] = *reinterpret_cast<const v2u *>(p + o[j].s + (V ? 64 * G : 0));
+    t.z[j] = *reinterpret_cast<const uint32_t *>(p + o[j].z + (V ? 32 * G : 0));
   }
 }
 
@@ -592,10 +614,11 @@ template <int D>
 __device__ __forceinline__ void load_zeros4(const uint8_t *p, int lane, v2u (&z)[Side4<D>::kSets][4]) {
   constexpr int G = D / kKvGroup;
 #pragma unroll
-  for (int j = 0; j < Side4<D>::kSets; ++j)
+  for (int j = 0; j < Side4<D>::kSets; ++j) {
+    const uint32_t at = 32 * D + 160 * G + (G == 1 ? 0 : 2 * j + (lane >> 5)) * 8;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      z[j][q] = *reinterpret_cast<const v2u *>(p + 32 * D + 160 * G + (q * G + (G == 1 ? 0 : 2 * j + (lane >> 5))) * 8);
+    for (int q = 0; q < 4; ++q) z[j][q] = *reinterpret_cast<const v2u *>(p + at + q * G * 8);
+  }
 }
 
 // Sums of a wave: R sets of four rows; lane's row of each is lane % 4 in o, l, zero
@@ -643,7 +666,7 @@ __device__ __forceinline__ void values4(const Side4<D> &t, const v2u (&w)[R][Sid
 }
 
 template <int D, int R, int W, bool SPLIT>
-__global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? (D == 64 ? 4 : 3) : 2) void k_kv_attention4(KvAttnArgs a) {
+__global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attention4(KvAttnArgs a) {
   constexpr int G = D / kKvGroup, kSets = Side4<D>::kSets, kTiles = G == 1 ? 2 : 1, kRows = 4 * R, kLd = D + 4;
   __shared__ float lds[W * kRows * kLd];
   __shared__ float2 ol[W * kRows];
@@ -675,8 +698,11 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? (D == 64 ? 4 : 3) : 2) 
     at = is ? x : a.c.cache;
   };
   locate(tile, p, there);
-  load_side4<D, false>(p, lane, tk);
-  load_side4<D, true>(p, lane, tv);
+  Lane4 at4[kSets];
+#pragma unroll
+  for (int j = 0; j < kSets; ++j) at4[j] = lane4<D>(lane, j);
+  load_side4<D, false>(p, at4, tk);
+  load_side4<D, true>(p, at4, tv);
   v2u zeros[kSets][4];
   if (SPLIT) load_zeros4<D>(p, lane, zeros);
 
@@ -693,15 +719,16 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? (D == 64 ? 4 : 3) : 2) 
     lo[r] = s.lo;
     hi[r] = s.hi;
     const uint16_t *src = a.Q + (size_t)(c.start + i) * a.q_stride + (size_t)head * D;
-    float top = 0.0f;
+    uint32_t most = 0;
 #pragma unroll
     for (int j = 0; j < kSets; ++j)
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
         const int g = G == 1 ? 0 : 2 * j + half;
         Q[r][j][n] = live ? *reinterpret_cast<const v4u *>(src + 64 * g + 32 * (n & 1) + 8 * (n >> 1)) : (v4u){0u, 0u, 0u, 0u};
-        top = fmaxf(top, largest8(Q[r][j][n], a.dtype));
+        most = larger8(most, Q[r][j][n]);
       }
+    float top = magnitude(most, a.dtype);
     if (G > 1) top = max_over<32, 32>(top);
     const float by = row_power(top, a.scale2, c2[r]);
 #pragma unroll
@@ -751,7 +778,7 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? (D == 64 ? 4 : 3) : 2) 
           d[r][1] = mfma4<-1>(hi2, (v2u){Q[r][j][n][2], Q[r][j][n][3]}, d[r][1]);
         }
       }
-      const uint32_t zw = tk.z[j] & 0x0F0F0F0Fu;
+      const uint32_t zw = zeros_of(tk.z[j]);
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -761,7 +788,7 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? (D == 64 ? 4 : 3) : 2) 
         }
     }
     __builtin_amdgcn_sched_barrier(0);
-    load_side4<D, false>(pn, lane, tk);
+    load_side4<D, false>(pn, at4, tk);
     __builtin_amdgcn_sched_barrier(0);
     if (G > 1) {
 #pragma unroll
@@ -842,7 +869,7 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? (D == 64 ? 4 : 3) : 2) 
       for (int i = 0; i < 4; ++i) s.l[r] += pw[r][i];
 #pragma unroll
       for (int j = 0; j < kSets; ++j) {
-        const uint32_t zw = tv.z[j] & 0x0F0F0F0Fu;
+        const uint32_t zw = SPLIT ? 0 : zeros_of(tv.z[j]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint32_t x = pack_h(ps[r][j][2 * i], ps[r][j][2 * i + 1]);
@@ -858,7 +885,7 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? (D == 64 ? 4 : 3) : 2) 
     }
     values4<D, R, SPLIT>(tv, w, w2, zeros, s, std::make_integer_sequence<int, 8>{});
     __builtin_amdgcn_sched_barrier(0);
-    load_side4<D, true>(pn, lane, tv);
+    load_side4<D, true>(pn, at4, tv);
     if (SPLIT) load_zeros4<D>(pn, lane, zeros);
     __builtin_amdgcn_sched_barrier(0);
     tile = next;
@@ -921,7 +948,8 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a, int block_rows) {
   float2 u[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) {
-    const int w = min(grp + i * kGroups, parts - 1);
+    const int w = grp + i * kGroups;
+    if (w >= parts) continue;
     u[i] = ol[w];
     v[i] = *reinterpret_cast<const v4f *>(part + (size_t)w * D);
   }
@@ -977,10 +1005,10 @@ hipError_t launch16(const KvAttnArgs &a, dim3 grid, hipStream_t s) {
                            : go(k_kv_attention<D, MT, kWaves, false, ROWS>, grid, 64 * kWaves, lds, a, s);
 }
 
-template <int D, int R>
+template <int D, int R, int W>
 hipError_t launch4(const KvAttnArgs &a, dim3 grid, hipStream_t s) {
-  return a.y_dtype == kF32 ? go(k_kv_attention4<D, R, kWaves, true>, grid, 64 * kWaves, 0, a, s)
-                           : go(k_kv_attention4<D, R, kWaves, false>, grid, 64 * kWaves, 0, a, s);
+  return a.y_dtype == kF32 ? go(k_kv_attention4<D, R, W, true>, grid, 64 * W, 0, a, s)
+                           : go(k_kv_attention4<D, R, W, false>, grid, 64 * W, 0, a, s);
 }
 
 template <int D>
@@ -989,8 +1017,8 @@ hipError_t launch_d(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s) {
   hipError_t e;
   constexpr int kMt = D == 256 ? 1 : 2;      // two row tiles of 256 channels would not fit the registers
   if (p.by_rows) return launch16<D, kMt, true>(a, grid, s);
-  if (p.rows == 4) e = launch4<D, 1>(a, grid, s);
-  else if (p.rows == 8) e = launch4<D, D == 256 ? 1 : 2>(a, grid, s);
+  if (p.rows == 4) e = p.waves == 8 ? launch4<D, 1, 8>(a, grid, s) : launch4<D, 1, 4>(a, grid, s);
+  else if (p.rows == 8) e = launch4<D, D == 256 ? 1 : 2, kWaves>(a, grid, s);
   else if (p.rows == 16) e = launch16<D, 1, false>(a, grid, s);
   else e = launch16<D, kMt, false>(a, grid, s);
   if (e == hipSuccess && p.splits > 1) {
@@ -1014,7 +1042,8 @@ KvAttnPlan plan_kv_attention(int T, int Hq, int H, int D, int B, int max_tokens,
   p.rows = rows <= 4 ? 4 : rows <= 8 && D < 256 ? 8 : rows <= 16 || D == 256 ? 16 : 32;
   const long long wgs = (rows + p.rows - 1) / p.rows * H * B;
   const long long most = std::max<long long>(1, (capacity + kMinTiles * kKvTile - 1) / (kMinTiles * kKvTile));
-  p.splits = (int)std::min<long long>({std::max<long long>(1, 2048 / wgs), most, kMaxParts});
+  p.splits = (int)std::min<long long>({std::max<long long>(1, 512 / wgs), most, kMaxParts});
+  if (p.rows == 4 && wgs * p.splits <= 256) p.waves = 8;
   if (p.splits > 1) {
     const size_t parts = (size_t)T * Hq * p.splits;
     p.part_off = align_up(parts * sizeof(float2), 256);
