@@ -572,8 +572,8 @@ int hsq_layer_norm_backward(const void *dY, int y_dtype, const void *X, int x_dt
  *                  where that is 0); its contents on entry do not matter, and
  *                  calls that overlap in time need one each
  * Products and sums are fp32, rounded once at the store.  With lambda, xh enters
- * the residual's product as fp16 numbers under a power of two per row and group:
- * 11 bits where Y is bf16, 22 bits where it is fp16 or fp32.  A row of xh that
+ * them as fp16 numbers under a power of two per row and group: 11 bits where Y is
+ * bf16, 22 bits where it is fp16 or fp32.  A row of xh that
  * holds an infinity or a NaN gives NaN; one whose 31 |xh| do not sum within
  * fp32 over a group may.  Sizes as for the linear (K % 64, r, batch), with
  * M * K, M * N, K * N < 2^31.  No output (the workspace among them) may overlap

@@ -25,9 +25,9 @@ def w4a16_64(X, codes, sw, lam, L1, L2, bias, residual, group, y_dtype):
     The residual's product is taken as x (24 + code) less 24 sum x, both fp32
     sums of exact products: each of the K additions of either is off by one unit
     at most (2 U32) of at most 32 |x| times the scale.  With lambda, x is off by
-    three roundings of fp32 and that of its fp16 terms: 2^-12 (one, for a bf16 Y)
-    or 2^-22 relative to the largest of its group's block where it is below
-    2^-27 of that, else to itself."""
+    three roundings of fp32 and that of its fp16 terms: 2^-11 (one, for a bf16 Y)
+    or 2^-22 of itself, not below 2^-37 of its group's largest; in the rank branch
+    too."""
     x = X.double()
     ex = torch.zeros_like(x)
     M, K = x.shape
@@ -45,7 +45,7 @@ def w4a16_64(X, codes, sw, lam, L1, L2, bias, residual, group, y_dtype):
             u = torch.mm(x, L1[b].double())
             au = torch.mm(x.abs(), L1[b].double().abs())
             y = y + torch.mm(u, L2[b].double())
-            t = t + torch.mm(2 * (K + 4) * U32 * au, L2[b].double().abs())
+            t = t + torch.mm(2 * (K + 4) * U32 * au + torch.mm(ex, L1[b].double().abs()), L2[b].double().abs())
             t = t + 2 * (L1.shape[2] + 1) * U32 * torch.mm(au, L2[b].double().abs())
         if bias is not None:
             y = y + bias[b].double()

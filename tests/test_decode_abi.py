@@ -143,9 +143,9 @@ def test_sizes():
     for bad in ((16, 1, 64), (48, 1, 64), (32, 0, 64), (32, 1, 80), (32, 5000, 64), (1 << 21, 1, 64), (-32, 1, 64)):
         assert lib.hsq_kv_page_bytes(*bad) == 0
     f = lib.hsq_w4a16_workspace_bytes
-    assert f(1, 4096, 4096, 0, 1, 64, 0, hsq.BF16) == 0
-    assert 0 < f(1, 4096, 4096, 4, 1, 64, 0, hsq.BF16) < f(1, 4096, 4096, 4, 1, 64, 1, hsq.BF16) < f(
-        1, 4096, 4096, 4, 1, 64, 1, hsq.F32)
+    assert f(1, 4096, 4096, 0, 1, 64, 0, hsq.BF16) == f(1, 4096, 4096, 4, 1, 64, 1, hsq.F32) == 0   # one launch
+    assert 0 < f(16, 4096, 4096, 4, 1, 64, 0, hsq.BF16) < f(16, 4096, 4096, 4, 1, 64, 1, hsq.BF16) < f(
+        16, 4096, 4096, 4, 1, 64, 1, hsq.F32)
     for bad in ((65, 4096, 64, 4, 1, 64), (0, 64, 64, 4, 1, 64), (1, 96, 64, 4, 1, 64), (1, 192, 64, 4, 1, 128),
                 (1, 64, 64, 33, 1, 64), (1, 64, 64, 4, 17, 64)):
         assert f(*bad, 1, hsq.F32) == 0

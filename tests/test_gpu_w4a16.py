@@ -46,6 +46,10 @@ SHAPES = [
     (17, 640, 130, 1, 64, 3), (33, 1152, 48, 1, 128, 8), (31, 576, 65, 2, 64, 0), (48, 512, 31, 1, 64, 7),
     (49, 448, 97, 1, 64, 1), (64, 1024, 160, 2, 128, 32), (64, 12288, 16, 1, 64, 4), (1, 12288, 9000, 1, 64, 0),
     (5, 128, 9001, 1, 64, 2), (64, 64, 15, 1, 64, 31), (4, 2112, 8200, 1, 64, 0),
+    # up to four rows: U in the same launch with 2, 3 and 4 column tiles, in one before it,
+    # no room for xh in LDS, too many columns
+    (1, 128, 8000, 1, 64, 8), (2, 192, 12000, 1, 64, 3), (1, 256, 4000, 3, 128, 16), (1, 4096, 100, 2, 64, 32),
+    (2, 8320, 40, 1, 64, 16), (4, 12288, 33, 1, 64, 7), (3, 256, 12000, 1, 128, 4), (4, 128, 4096, 1, 64, 32),
 ]
 
 

@@ -875,13 +875,9 @@ def w4a16_lowrank_linear(X, packed_w, sw, lam=None, L1=None, L2=None, bias=None,
         po = out.data_ptr()
     else:
         po = _arg(T, out, "out", dev, (ydt,), (batch, M, N))
-    nbytes = pws = None
-    if lam is None and not r:
-        workspace, pws, nbytes = None, None, 0          # nothing to prepare
-    else:
-        workspace, pws, nbytes = _scratch(
-            T, workspace, lambda: lib.hsq_w4a16_workspace_bytes(M, K, N, r, batch, group, int(lam is not None),
-                                                                dts[ydt]), X, dev)
+    workspace, pws, nbytes = _scratch(
+        T, workspace, lambda: lib.hsq_w4a16_workspace_bytes(M, K, N, r, batch, group, int(lam is not None), dts[ydt]),
+        X, dev)
     _check(lib.hsq_w4a16_lowrank_linear(px, M, K, N, batch, group, dts[dt], pl, pw, ps, p1, p2, r, pb, pr, po, dts[ydt],
                                         pws, nbytes, T.stream(dev)), "hsq_w4a16_lowrank_linear")
     return out

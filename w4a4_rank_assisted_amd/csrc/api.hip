@@ -1025,7 +1025,7 @@ int hsq_layer_norm_backward(const void *dY, int y_dtype, const void *X, int x_dt
 
 size_t hsq_w4a16_workspace_bytes(int M, int K, int N, int r, int batch, int group, int smooth, int y_dtype) {
   if (check_sizes(M, K, N, r, batch) != HSQ_OK || M > HSQ_W4A16_MAX_M || !group_ok(group) || K % group != 0) return 0;
-  return plan_w4a16(M, K, r, batch, group, smooth != 0, y_dtype).total;
+  return plan_w4a16(M, K, N, r, batch, group, smooth != 0, y_dtype).total;
 }
 
 int hsq_w4a16_lowrank_linear(const uint16_t *X, int M, int K, int N, int batch, int group, int dtype,
@@ -1041,7 +1041,7 @@ int hsq_w4a16_lowrank_linear(const uint16_t *X, int M, int K, int N, int batch, 
   const void *ptrs[] = {X, lambda, packed_w, sw, L1, L2, bias, residual, Y, workspace};
   for (const void *p : ptrs)
     if (p && !aligned16(p)) return HSQ_E_ALIGN;
-  const W4a16Plan P = plan_w4a16(M, K, r, batch, group, lambda != nullptr, y_dtype);
+  const W4a16Plan P = plan_w4a16(M, K, N, r, batch, group, lambda != nullptr, y_dtype);
   if (P.total > 0 && (!workspace || ws_bytes < P.total)) return HSQ_E_WORKSPACE;
   const size_t m = M, k = K, n = N, b = batch, y_bytes = b * m * n * type_bytes(y_dtype);
   if (!written_apart({{Y, y_bytes}, {workspace, P.total}},
@@ -1053,10 +1053,10 @@ int hsq_w4a16_lowrank_linear(const uint16_t *X, int M, int K, int N, int batch, 
   W4a16Args a{};
   a.X = X; a.lam = lambda; a.L1 = r > 0 ? L1 : nullptr; a.L2 = r > 0 ? L2 : nullptr; a.bias = bias; a.res = residual;
   a.w = packed_w; a.w_stride = packed_bytes(K, N); a.sw = sw; a.Y = Y;
-  a.hi = (uint16_t *)(ws + P.hi_off); a.lo = (uint16_t *)(ws + P.lo_off);
-  a.es = (float *)(ws + P.es_off); a.uw = (float *)(ws + P.uw_off);
+  if (!P.small) { a.hi = (uint16_t *)(ws + P.hi_off); a.lo = (uint16_t *)(ws + P.lo_off); }
+  a.es = (float *)(ws + P.es_off); a.uw = (float *)(ws + P.uw_off); a.part = (float *)(ws + P.part_off);
   a.M = M; a.K = K; a.N = N; a.r = r; a.batch = batch; a.bpg = group / kGroup; a.dtype = dtype; a.y_dtype = y_dtype;
-  a.terms = P.terms; a.u_slices = P.u_slices; a.slice = P.slice;
+  a.small = P.small; a.own_u = P.own_u; a.terms = P.terms; a.u_slices = P.u_slices; a.slice = P.slice; a.ct = P.ct; a.splits = P.splits;
   return debug_check(hip_status(launch_w4a16(a, (hipStream_t)stream)), stream);
 }
 

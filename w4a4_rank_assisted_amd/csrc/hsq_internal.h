@@ -409,12 +409,17 @@ hipError_t launch_layer_norm_backward(const NormArgs &a, hipStream_t s);
 // output holds more bits than hi does.
 //   hi, lo: M x K fp16      es: M16 x K/group fp32 (2^e), M16 = 16 ceil(M/16)
 //   uw:     u_slices x (batch*r) x M16 fp32, one slice of U per slice of K
+//   part:   splits x batch x M x N fp32, where workgroups split K
 struct W4a16Plan {
+  bool small = false;      // xh in LDS, one launch
+  bool own_u = false;      // which forms U too, otherwise a launch before it does
   int terms = 1;           // 2: hi and lo
   int u_slices = 0, slice = 0;   // slices of K of the preparing launch, channels of one
-  size_t hi_off = 0, lo_off = 0, es_off = 0, uw_off = 0, total = 0;
+  int ct = 1, splits = 1;  // column tiles of a workgroup, workgroups that share them
+  size_t hi_off = 0, lo_off = 0, es_off = 0, uw_off = 0, part_off = 0, total = 0;
 };
-W4a16Plan plan_w4a16(int M, int K, int r, int batch, int group, bool smooth, int y_dtype);
+constexpr int kW4a16Splits = 4;   // at most
+W4a16Plan plan_w4a16(int M, int K, int N, int r, int batch, int group, bool smooth, int y_dtype);
 
 struct W4a16Args {
   const uint16_t *X;       // M x K of dtype
@@ -427,9 +432,9 @@ struct W4a16Args {
   const uint16_t *sw;      // batch x K/group x N fp16
   void *Y;
   uint16_t *hi, *lo;       // workspace
-  float *es, *uw;
+  float *es, *uw, *part;
   int M, K, N, r, batch, bpg, dtype, y_dtype;
-  int terms, u_slices, slice;
+  int small, own_u, terms, u_slices, slice, ct, splits;
 };
 hipError_t launch_w4a16(const W4a16Args &a, hipStream_t s);
 
