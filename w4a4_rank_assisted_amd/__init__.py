@@ -893,6 +893,19 @@ def kv_page_bytes(page_size: int, kv_heads: int, head_dim: int) -> int:
     return int(_load().hsq_kv_page_bytes(page_size, kv_heads, head_dim))
 
 
+_kv_tiles = {}   # head_dim: bytes of a head's KV_TILE tokens, looked up once
+
+
+def _kv_tile(head_dim) -> int:
+    n = _kv_tiles.get(head_dim)
+    if n is None:
+        n = _kv_tiles[head_dim] = kv_page_bytes(KV_TILE, 1, head_dim)
+        if n == 0:
+            del _kv_tiles[head_dim]
+            raise HsqError(E_SHAPE, f"head_dim {head_dim}")
+    return n
+
+
 def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, device=None):
     """An empty cache, (num_pages, kv_heads, bytes of a head's page) uint8 zeros on
     the current device: the shape tells the calls below its heads and page size."""
@@ -907,18 +920,18 @@ def kv_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int = 64, 
 def _kv_where(T, cache, head_dim: int, block_table, kv_lens, cu_tokens, dev):
     """(cache pointer, pages, heads, page size, table pointer, width, lens pointer, cu pointer, batch)."""
     pc = _arg(T, cache, "cache", dev, (T.u8,))
-    if cache.dim() != 3:
-        raise ValueError(f"cache: shape {tuple(cache.shape)} is not that of kv_cache")
-    tile = kv_page_bytes(KV_TILE, 1, head_dim)
-    if tile == 0:
-        raise HsqError(E_SHAPE, f"head_dim {head_dim}")
-    pages, heads, n = cache.shape
+    shape = cache.shape
+    if len(shape) != 3:
+        raise ValueError(f"cache: shape {tuple(shape)} is not that of kv_cache")
+    tile = _kv_tile(head_dim)
+    pages, heads, n = shape
     if n == 0 or n % tile:
         raise ValueError(f"cache: {n} bytes a head are no pages of head_dim {head_dim}")
     pt = _arg(T, block_table, "block_table", dev, (T.i32,))
-    if block_table.dim() != 2:
-        raise ValueError(f"block_table: shape {tuple(block_table.shape)} is not (batch, pages)")
-    batch, width = block_table.shape
+    shape = block_table.shape
+    if len(shape) != 2:
+        raise ValueError(f"block_table: shape {tuple(shape)} is not (batch, pages)")
+    batch, width = shape
     pl = _arg(T, kv_lens, "kv_lens", dev, (T.i32,), (batch,))
     pq = None if cu_tokens is None else _arg(T, cu_tokens, "cu_tokens", dev, (T.i32,), (batch + 1,))
     return pc, pages, heads, n // tile * KV_TILE, pt, width, pl, pq, batch
@@ -933,9 +946,15 @@ def _token_rows(T, t, name, dev, dtypes, shape):
         raise ValueError(f"{name} must be on HIP device {dev}, the current device and that of the other operands")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if t.dim() != 3 or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {shape}")
-    n, h, d = t.shape
+    have = t.shape
+    if len(have) != 3:
+        raise ValueError(f"{name}: shape {tuple(have)} != {shape}")
+    n, h, d = have
+    rows, heads, dim = shape
+    if (rows is not None and n != rows) or (heads is not None and h != heads) or d != dim:
+        raise ValueError(f"{name}: shape {tuple(have)} != {shape}")
+    if t.is_contiguous() and h * d % 8 == 0:
+        return t.data_ptr(), h * d
     st = t.stride()
     dense = h * d
     if (d > 1 and st[2] != 1) or (h > 1 and st[1] != d):
@@ -988,9 +1007,10 @@ def kv_cache_read(cache, block_table, kv_lens, cu_tokens=None, *, tokens: int, h
     if out is None:
         K = T.empty(shape, dtype=dt, device=cache.device)
         V = T.empty_like(K)
+        pk, pv = K.data_ptr(), V.data_ptr()
     else:
         K, V = out
-    pk, pv = _arg(T, K, "K", dev, (dt,), shape), _arg(T, V, "V", dev, (dt,), shape)
+        pk, pv = _arg(T, K, "K", dev, (dt,), shape), _arg(T, V, "V", dev, (dt,), shape)
     _check(lib.hsq_kv_cache_read(pc, pages, page, heads, head_dim, pt, width, pl, pq, batch, tokens, top, pk, pv,
                                  T.code[dt], T.stream(dev)), "hsq_kv_cache_read")
     return K, V
