@@ -27,20 +27,24 @@ def w4a16_64(X, codes, sw, lam, L1, L2, bias, residual, group, y_dtype):
     at most (2 U32) of at most 32 |x| times the scale.  With lambda, x is off by
     three roundings of fp32 and that of its fp16 terms: 2^-11 (one, for a bf16 Y)
     or 2^-22 of itself, not below 2^-37 of its group's largest; in the rank branch
-    too."""
+    too.  Its codes are then subnormal numbers, of which the matrix unit keeps no
+    more than 2^-24 of 2^-14 times the largest x: a term of the sum of the codes or of
+    the constant, codes of 2^-24 (2^-18 against two terms), is cut at 2^-14
+    (2^-20) of it."""
     x = X.double()
-    ex = torch.zeros_like(x)
+    ex, cut = torch.zeros_like(x), torch.zeros_like(x)
     M, K = x.shape
     if lam is not None:
         x = x / lam.double()
         top = x.abs().view(M, K // group, group).amax(2).repeat_interleave(group, 1)
         ex = x.abs() * (4 * U32 + (2.0 ** -11 if y_dtype == torch.bfloat16 else 2.0 ** -22)) + top * 2.0 ** -37
+        cut = 2 * top * (2.0 ** -14 if y_dtype == torch.bfloat16 else 2.0 ** -20)
     ys, ts = [], []
     for b in range(codes.shape[0]):
         s = sw[b].double().repeat_interleave(group, 0)
         w = codes[b].double() * s
         y = torch.mm(x, w)
-        t = torch.mm(ex, w.abs()) + 2 * (K + 4) * U32 * 2 * 32 * torch.mm(x.abs(), s)
+        t = torch.mm(ex, w.abs()) + torch.mm(cut, s) + 2 * (K + 4) * U32 * 2 * 32 * torch.mm(x.abs(), s)
         if L1 is not None:
             u = torch.mm(x, L1[b].double())
             au = torch.mm(x.abs(), L1[b].double().abs())
@@ -88,11 +92,15 @@ def attention64(Q, k, v, ks, vs, pos, scale, causal, window, y_dtype):
 
     Returns (y, lse, tolerance of y after the store, tolerance of lse).  With U
     half a unit: a group's score is the difference of two sums of 64 terms below
-    31 |q|, each addition off by 2 U, then a few roundings; exp2's argument is off
+    31 |q|, each addition off by 2 U, then a few roundings; the codes are subnormal
+    numbers, whose exponent the matrix unit takes to be that of 2^-14, so that 64
+    terms and the sum before each instruction, 16 at most, are cut at 2^-14 of the
+    largest |q|, or 2^-20 where the result is fp32; exp2's argument is off
     by U (4 |e| log2(e) + 64) and its result by two units (so eta, relative);
     p s is rounded to fp16 (2^-11) or to two (2^-21), not below 2^-32 of the row's
     largest; the sums over N tokens add 2 N U: of |v|, or, where the result has 16
-    bits, of p s n and p s z apart, 30 p s in all."""
+    bits, of p s n and p s z apart, 30 p s in all; and their terms, N and an instruction's
+    start every four, are cut likewise at 2^-14 (2^-20) of the largest p s."""
     n, Hq, D = Q.shape
     N, H, _ = k.shape
     G = D // 64
@@ -108,6 +116,7 @@ def attention64(Q, k, v, ks, vs, pos, scale, causal, window, y_dtype):
     lse = torch.full((n, Hq), -math.inf, dtype=torch.float64, device=dev)
     tl = torch.zeros_like(lse)
     h = 2.0 ** -21 if y_dtype == torch.float32 else 2.0 ** -11
+    unit = 2.0 ** -20 if y_dtype == torch.float32 else 2.0 ** -14
     if N == 0:
         return y, lse, ty, tl
     for hq in range(Hq):
@@ -123,17 +132,22 @@ def attention64(Q, k, v, ks, vs, pos, scale, causal, window, y_dtype):
         yy = torch.mm(p, vh) / div
         aa = torch.mm(p, vh.abs()) / div
         a = q[:, hq].abs().view(n, G, 64).sum(2)
-        de = scale * 31 * 264 * U32 * torch.mm(a, ks[:, hk].double().t().contiguous())
+        most = q[:, hq].abs().view(n, G, 64).amax(2)
+        de = scale * torch.mm(31 * 264 * U32 * a + 80 * unit * most, ks[:, hk].double().t().contiguous())
         de = torch.where(seen, de, torch.zeros_like(de)).amax(1, keepdim=True)
         big = torch.where(seen, e.abs(), torch.zeros_like(e)).amax(1, keepdim=True)
         eta = de + U32 * (4 * 1.45 * big + 64) * 0.7 + 8 * U32
-        ps = (p[:, :, None] * vs[None, :, hk].double()).amax(1)                       # n, G
+        ps = p[:, :, None] * vs[None, :, hk].double()                                 # n, N, G
+        cut = unit * ps.amax(1, keepdim=True)
+        cut = 2 * (torch.minimum(15 * ps, cut).sum(1) + (N / 4 + 8) * cut[:, 0]) / div
+        cut = cut.repeat_interleave(64, 1)
+        ps = ps.amax(1)                                                               # n, G
         floor = (15 * N * 2.0 ** -32 * ps / div).repeat_interleave(64, 1)
         apart = 0.0
         if y_dtype != torch.float32:
             sums = (torch.mm(p, vs[:, hk].double()) / div).repeat_interleave(64, 1)
             apart = 30 * sums * 2 * (N + 64) * U32
-        t1 = aa * (eta + h + 2 * (N + 64) * U32) + apart + yy.abs() * (eta + 2 * (N + 64) * U32 + 8 * U32) + floor
+        t1 = aa * (eta + h + 2 * (N + 64) * U32) + apart + yy.abs() * (eta + 2 * (N + 64) * U32 + 8 * U32) + floor + cut
         y[:, hq] = yy
         ty[:, hq] = t1 + half_step(y_dtype) * (yy.abs() + t1) + tiny(y_dtype)
         l = torch.log(tot[:, 0]) + top

@@ -265,3 +265,26 @@ def test_result_does_not_depend_on_the_rest():
     y = hsq.kv_attention(Q, cache, table, i32(*lens))
     for _ in range(5):
         assert torch.equal(y, hsq.kv_attention(Q, cache, table, i32(*lens)))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("heads", [1, 4, 8, 16, 80])
+def test_small_channels_count_beside_a_large_one(D, heads):
+    # one channel of 1 and the others 2^-19, their codes 15 and the large one's 0, over
+    # zeros from 0 to 8: with fp32 results the small ones are not lost.  Each of up to 16
+    # instructions a group and the steps around them rounds at 2^-20 of the largest product
+    # per term: 80 terms and 16 steps
+    q = torch.full((1, heads, D), 2.0 ** -19)
+    q[..., ::64] = 1.0
+    k = torch.empty(9, 1, D)
+    for z in range(9):
+        k[z] = float(15 - z)
+        k[z, :, ::64] = float(-z)
+    k, v = k.bfloat16().to(DEV), torch.ones(9, 1, D, dtype=torch.bfloat16, device=DEV)
+    for z in range(9):
+        cache, table = fill(k[z:z + 1], v[z:z + 1], [1], 32)
+        y, lse = hsq.kv_attention(q.bfloat16().to(DEV), cache, table, i32(1), scale=1.0, y_dtype="f32", return_lse=True)
+        want = D // 64 * (-z + 63 * (15 - z) * 2.0 ** -19)
+        assert bool(((lse.double() - want).abs() <= D // 64 * 96 * 2.0 ** -20 + 4 * U32 * abs(want)).all()), z
+        held = held64(v[z:z + 1], "asym")                # 15 times the fp16 scale 1 / 15
+        assert bool(((y.double() - held.view(-1)[0]).abs() <= 2.0 ** -20).all())

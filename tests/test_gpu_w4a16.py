@@ -164,3 +164,22 @@ def test_layer_object_weight_only():
     # the quantized form of the same layer: 4-bit activations, a few percent away
     q = lay(X, "f32")
     assert float((q.double() - want).norm() / want.norm()) < 0.15
+
+
+@pytest.mark.parametrize("M", [1, 3, 16, 40])
+@pytest.mark.parametrize("smooth", [False, True])
+def test_small_channels_count_beside_a_large_one(M, smooth):
+    # one channel of 1 in each group and the others 2^-19, codes 7 against -8: an fp32 result
+    # holds them.  The sums of the codes and of the constant cut their terms, 64 and 64 of two
+    # parts each, at 2^-20 of the largest product's unit
+    K, N = 256, 48
+    X = torch.full((M, K), 2.0 ** -19)
+    X[:, ::64] = 1.0
+    codes = torch.full((1, K, N), 7, dtype=torch.int8)
+    codes[:, ::64] = -8
+    s = dict(X=X.bfloat16(), codes=codes, sw=torch.ones(1, K // 64, N).half(), lam=torch.ones(K).half() if smooth else None,
+             L1=None, L2=None, bias=None, residual=None)
+    s = {k: None if v is None else v.to(DEV) for k, v in s.items()}
+    y = call(s, 64, "f32").double()
+    want = 4 * (-8 + 63 * 7 * 2.0 ** -19)
+    assert bool(((y - want).abs() <= 4 * 256 * 2.0 ** -20).all()), (y - want).abs().max().item()

@@ -12,16 +12,23 @@
 // (where the result is fp32 the second is summed as (p_t s_g) (n_d - z_g), which
 // costs a subtraction a pair of codes and keeps what the difference cancels).
 // A nibble n in the lowest bits of a 16-bit half is the subnormal fp16 number n
-// 2^-24, and in the next four n 2^-20; the matrix unit takes both exactly.  A dword
-// of eight codes is thus four masks and one shift; the powers of two go into the
-// queries and the end.  Queries are held in fp16 under a power of two per row
-// (what that loses is below 2^-38 of the row's largest channel).  Products are exact
-// and sums fp32.  p s is the only value that is rounded: to fp16 (11 bits), or,
-// where the result is fp32, to the sum of two.  Its range is kept by the row's offset
-// o, a whole number: p = 2^(e log2(e) - o) with o such that p s stays below 2^15; o
-// moves, and the sums with it by an exact power of two, only when a tile would
-// exceed that (seven doublings above the tile that set it), so the running
-// maximum of the softmax costs one comparison a tile.
+// 2^-24, and in the next four n 2^-20; the matrix unit takes both without loss.  A
+// dword of eight codes is thus four masks and one shift; the powers of two go into
+// the queries and the end.  But the unit aligns the terms of a sum by the exponents
+// that their operands have, which for every subnormal number is that of 2^-14: with
+// codes of 2^-24 a sum keeps 2^-14 of its largest q (or p s), a sixteenth of
+// what rounding p s leaves.  Where the result is fp32 (FINE) the codes are shifted
+// to n 2^-18 instead, which leaves fp32's 2^-20 of it: scores of about 30 then are
+// off by 2e-6 and not by 3e-4, for three more shifts a dword (64 sequences of 4096
+// tokens: 64 us, with the rest that fp32 costs, against 58).
+// Queries are held in fp16 under a power of two per row
+// (what that loses is below 2^-34 of the row's largest channel), their sums
+// against 1 and not against a code of 1.  p s is the only value that is rounded: to
+// fp16 (11 bits), or, where the result is fp32, to the sum of two.  Its range is
+// kept by the row's offset o, a whole number: p = 2^(e log2(e) - o) with o such
+// that p s stays below 2^15; o moves, and the sums with it by an exact power of
+// two, only when a tile would exceed that (seven doublings above the tile that set
+// it), so the running maximum of the softmax costs one comparison a tile.
 //
 // Three forms, by the query rows that share a head of the cache in one sequence:
 //
@@ -70,7 +77,24 @@ __device__ __forceinline__ v4f mfma4(v2u a, v2u b, v4f c) {
                                             BLOCK >= 0 ? BLOCK : 0, 0);
 }
 
-constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;   // codes as n 2^-24 and n 2^-20
+// Eight codes as subnormal numbers: the low nibbles of a dword's bytes 0, 2 and 1, 3
+// and the high ones.  FINE: all n 2^-18, otherwise n 2^-24 and n 2^-20, which saves
+// three shifts a dword.
+constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u, kTopBits = 0x03C003C0u;
+template <bool FINE>
+struct Unit {
+  static constexpr float low = FINE ? 262144.0f : 16777216.0f, high = FINE ? 262144.0f : 1048576.0f;   // one code is 1 / low
+  static constexpr float less = high / low;     // of the queries that meet the high ones
+  static constexpr uint32_t one_low = 0x3C003C00u, one_high = FINE ? 0x3C003C00u : 0x4C004C00u;   // 1 and 1 / less
+};
+template <bool FINE>
+__device__ __forceinline__ v2u low_codes(uint32_t w) {
+  return FINE ? (v2u){w << 6 & kTopBits, w >> 2 & kTopBits} : (v2u){w & kLow, w >> 8 & kLow};
+}
+template <bool FINE>
+__device__ __forceinline__ v2u high_codes(uint32_t w) {
+  return FINE ? (v2u){w << 2 & kTopBits, w >> 6 & kTopBits} : (v2u){w & kHigh, w >> 8 & kHigh};
+}
 
 __device__ __forceinline__ uint32_t pack_h(float a, float b) {
   v2h h = {(_Float16)a, (_Float16)b};
@@ -106,8 +130,6 @@ __device__ __forceinline__ float sum_over(float v) {
   return v;
 }
 
-// Eight channels of a query as fp16 under 2^-ex, the last four by another 1/16 (they
-// meet the codes of the high nibbles).
 __device__ __forceinline__ void unpack8(v4u w, int dtype, float *f) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -129,18 +151,21 @@ __device__ __forceinline__ float magnitude(uint32_t top, int dtype) {
   const uint32_t h = max(top & 0xFFFFu, top >> 16);
   return dtype == kBf16 ? bf16_to_f32(h) : f16_to_f32((uint16_t)h);
 }
+// Eight channels of a query as fp16 by `by`, the last four less where they meet larger codes.
+template <bool FINE>
 __device__ __forceinline__ v4u scaled8(v4u w, int dtype, float by) {
   float f[8];
   unpack8(w, dtype, f);
-  const float high = by * 0.0625f;
+  const float high = by * Unit<FINE>::less;
   return (v4u){pack_h(f[0] * by, f[1] * by), pack_h(f[2] * by, f[3] * by), pack_h(f[4] * high, f[5] * high),
                pack_h(f[6] * high, f[7] * high)};
 }
 // The power of two that takes a row's largest channel to [2^13, 2^14), and the
 // factor from the products' sums to scores in powers of two.
+template <bool FINE>
 __device__ __forceinline__ float row_power(float top, float scale2, float &to_score) {
   const int ex = min(max((int)(__float_as_uint(top) >> 23) - 13, 1), 240);
-  to_score = __uint_as_float((uint32_t)ex << 23) * 16777216.0f * scale2;
+  to_score = __uint_as_float((uint32_t)ex << 23) * Unit<FINE>::low * scale2;
   return __uint_as_float((uint32_t)(254 - ex) << 23);
 }
 
@@ -228,7 +253,7 @@ struct Sums {
 };
 
 // The scores of 32 tokens: e[m][4 a + r] of token 16 a + 4 q + r.
-template <int D, int MT>
+template <int D, int MT, bool FINE>
 __device__ __forceinline__ void scores(const Side<D> &t, const v4u (&Q)[MT][D / 32], const float (&qs)[MT][D / 64],
                                        float (&e)[MT][8]) {
   constexpr int G = D / kKvGroup;
@@ -240,8 +265,8 @@ __device__ __forceinline__ void scores(const Side<D> &t, const v4u (&Q)[MT][D / 
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int i = a * (D / 32) + 2 * g + x;
-        const uint32_t w = t.code[i >> 2][i & 3], v = w >> 8;
-        k[x] = (v4u){w & kLow, v & kLow, w & kHigh, v & kHigh};
+        const v2u low = low_codes<FINE>(t.code[i >> 2][i & 3]), high = high_codes<FINE>(t.code[i >> 2][i & 3]);
+        k[x] = (v4u){low[0], low[1], high[0], high[1]};
       }
       const uint32_t zw = zeros_of(t.z[g][a]);
 #pragma unroll
@@ -348,8 +373,8 @@ __device__ __forceinline__ void values(const Side<D> &t, const v4u (&w)[MT][D / 
 #pragma unroll
   for (int g = 0; g < D / kKvGroup; ++g) {
     const uint32_t z0 = t.z[g][0], z1 = t.z[g][1];
-    const v4u zz = {z0 & kLow, z0 >> 8 & kLow, z1 & kLow, z1 >> 8 & kLow};
-    const v4u zh = {z0 << 4 & kHigh, z0 >> 4 & kHigh, z1 << 4 & kHigh, z1 >> 4 & kHigh};
+    const v2u l0 = low_codes<SPLIT>(z0), l1 = low_codes<SPLIT>(z1);
+    const v4u zz = {l0[0], l0[1], l1[0], l1[1]};
     if (!SPLIT) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) s.zero[m][g] = mfma16(zz, w[m][g], s.zero[m][g]);
@@ -357,13 +382,14 @@ __device__ __forceinline__ void values(const Side<D> &t, const v4u (&w)[MT][D / 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {         // channels 32 p ..: 32 tokens in two dwords
       const int pr = 2 * g + h;
-      const uint32_t v0 = t.code[pr >> 1][2 * (pr & 1)], v1 = t.code[pr >> 1][2 * (pr & 1) + 1], u0 = v0 >> 8, u1 = v1 >> 8;
-      v4u b0 = {v0 & kLow, u0 & kLow, v1 & kLow, u1 & kLow}, b1 = {v0 & kHigh, u0 & kHigh, v1 & kHigh, u1 & kHigh};
+      const uint32_t v0 = t.code[pr >> 1][2 * (pr & 1)], v1 = t.code[pr >> 1][2 * (pr & 1) + 1];
+      const v2u low0 = low_codes<SPLIT>(v0), low1 = low_codes<SPLIT>(v1), high0 = high_codes<SPLIT>(v0), high1 = high_codes<SPLIT>(v1);
+      v4u b0 = {low0[0], low0[1], low1[0], low1[1]}, b1 = {high0[0], high0[1], high1[0], high1[1]};
       if (SPLIT) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           b0[i] = minus_h(b0[i], zz[i]);
-          b1[i] = minus_h(b1[i], zh[i]);
+          b1[i] = minus_h(b1[i], zz[i]);
         }
       }
 #pragma unroll
@@ -473,15 +499,15 @@ __global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) 
       Q[m][x] = live[m] ? *reinterpret_cast<const v4u *>(src + 32 * x) : (v4u){0u, 0u, 0u, 0u};
       top = larger8(top, Q[m][x]);
     }
-    const float by = row_power(max_over<16, 32>(magnitude(top, a.dtype)), a.scale2, c2[m]);
+    const float by = row_power<SPLIT>(max_over<16, 32>(magnitude(top, a.dtype)), a.scale2, c2[m]);
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) Q[m][x] = scaled8(Q[m][x], a.dtype, by);
-    const v4u ones = {0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u};   // codes of 1
+    for (int x = 0; x < D / 32; ++x) Q[m][x] = scaled8<SPLIT>(Q[m][x], a.dtype, by);
+    const v4u ones = {Unit<SPLIT>::one_low, Unit<SPLIT>::one_low, Unit<SPLIT>::one_high, Unit<SPLIT>::one_high};
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       v4f d = mfma16(ones, Q[m][2 * g], (v4f){0.0f, 0.0f, 0.0f, 0.0f});
       d = mfma16(ones, Q[m][2 * g + 1], d);
-      qs[m][g] = d[0];
+      qs[m][g] = d[0] * (1.0f / Unit<SPLIT>::low);
     }
   }
   // tokens that every row of the wave sees
@@ -514,7 +540,7 @@ __global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) 
       const bool there_n = pn != nullptr;
       if (!there_n) pn = a.c.cache;
       float e[MT][8];
-      scores<D, MT>(tk, Q, qs, e);
+      scores<D, MT, SPLIT>(tk, Q, qs, e);
       __builtin_amdgcn_sched_barrier(0);
       load_side<D, false>(pn, lane, tk);
       __builtin_amdgcn_sched_barrier(0);
@@ -545,8 +571,8 @@ __global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) 
     s.l[m] = sum_over<16, 32>(s.l[m]);
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
-      const float up = x & 1 ? 1048576.0f : 16777216.0f;
-      s.acc[m][x] = s.acc[m][x] * up - s.zero[m][x / 4] * 16777216.0f;
+      const float up = x & 1 ? Unit<SPLIT>::high : Unit<SPLIT>::low;
+      s.acc[m][x] = s.acc[m][x] * up - s.zero[m][x / 4] * Unit<SPLIT>::low;
     }
   }
   if (ROWS) {
@@ -644,12 +670,11 @@ __device__ __forceinline__ void values4(const Side4<D> &t, const v2u (&w)[R][Sid
     constexpr int c = decltype(ic)::value;     // tokens 4 c ..: a = c / 4, q = c % 4
 #pragma unroll
     for (int j = 0; j < Side4<D>::kSets; ++j) {
-      const uint32_t v = t.code[j][c & 3][c >> 2], u = v >> 8;
-      v2u lo = {v & kLow, u & kLow}, hi = {v & kHigh, u & kHigh};
+      v2u lo = low_codes<SPLIT>(t.code[j][c & 3][c >> 2]), hi = high_codes<SPLIT>(t.code[j][c & 3][c >> 2]);
       if (SPLIT) {
-        const uint32_t x = z[j][c & 3][c >> 2];
-        lo = (v2u){minus_h(lo[0], x & kLow), minus_h(lo[1], x >> 8 & kLow)};
-        hi = (v2u){minus_h(hi[0], x << 4 & kHigh), minus_h(hi[1], x >> 4 & kHigh)};
+        const v2u x = low_codes<SPLIT>(z[j][c & 3][c >> 2]);
+        lo = (v2u){minus_h(lo[0], x[0]), minus_h(lo[1], x[1])};
+        hi = (v2u){minus_h(hi[0], x[0]), minus_h(hi[1], x[1])};
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -730,17 +755,17 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
       }
     float top = magnitude(most, a.dtype);
     if (G > 1) top = max_over<32, 32>(top);
-    const float by = row_power(top, a.scale2, c2[r]);
+    const float by = row_power<SPLIT>(top, a.scale2, c2[r]);
 #pragma unroll
     for (int j = 0; j < kSets; ++j) {
       v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        Q[r][j][n] = scaled8(Q[r][j][n], a.dtype, by);
-        d = mfma4<-1>((v2u){0x00010001u, 0x00010001u}, (v2u){Q[r][j][n][0], Q[r][j][n][1]}, d);   // codes of 1
-        d = mfma4<-1>((v2u){0x00100010u, 0x00100010u}, (v2u){Q[r][j][n][2], Q[r][j][n][3]}, d);
+        Q[r][j][n] = scaled8<SPLIT>(Q[r][j][n], a.dtype, by);
+        d = mfma4<-1>((v2u){Unit<SPLIT>::one_low, Unit<SPLIT>::one_low}, (v2u){Q[r][j][n][0], Q[r][j][n][1]}, d);
+        d = mfma4<-1>((v2u){Unit<SPLIT>::one_high, Unit<SPLIT>::one_high}, (v2u){Q[r][j][n][2], Q[r][j][n][3]}, d);
       }
-      qs[r][j] = d[0];
+      qs[r][j] = d[0] * (1.0f / Unit<SPLIT>::low);
     }
   }
   const int full_lo = seen_by(a, (r1 - 1) / a.gr, c.p0, c.len).lo, full_hi = seen_by(a, r0 / a.gr, c.p0, c.len).hi;
@@ -770,8 +795,7 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
       for (int r = 0; r < R; ++r) d[r][0] = d[r][1] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        const uint32_t w = tk.code[j][n >> 1][n & 1], v = w >> 8;
-        const v2u lo2 = {w & kLow, v & kLow}, hi2 = {w & kHigh, v & kHigh};
+        const v2u lo2 = low_codes<SPLIT>(tk.code[j][n >> 1][n & 1]), hi2 = high_codes<SPLIT>(tk.code[j][n >> 1][n & 1]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           d[r][0] = mfma4<-1>(lo2, (v2u){Q[r][j][n][0], Q[r][j][n][1]}, d[r][0]);
@@ -900,7 +924,7 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
     for (int j = 0; j < kSets; ++j) {
       const float z = sum_over<4, 16>(s.zero[r][j]);
       const v4f zr = {quad<0>(z), quad<1>(z), quad<2>(z), quad<3>(z)};
-      v4f y0 = s.low[r][j] * 16777216.0f - zr, y1 = s.high[r][j] * 1048576.0f - zr;
+      v4f y0 = s.low[r][j] * Unit<SPLIT>::low - zr, y1 = s.high[r][j] * Unit<SPLIT>::high - zr;
       if (G == 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
