@@ -573,7 +573,8 @@ int hsq_layer_norm_backward(const void *dY, int y_dtype, const void *X, int x_dt
  *                  calls that overlap in time need one each
  * Products and sums are fp32, rounded once at the store.  With lambda, xh enters
  * them as fp16 numbers under a power of two per row and group: 11 bits where Y is
- * bf16, 22 bits where it is fp16 or fp32.  A row of xh that
+ * bf16, 22 bits where it is fp16 or fp32; and the terms of their sums are cut at
+ * 2^-14, or 2^-20, of the row's largest |xh| in the group.  A row of xh that
  * holds an infinity or a NaN gives NaN; one whose 31 |xh| do not sum within
  * fp32 over a group may.  Sizes as for the linear (K % 64, r, batch), with
  * M * K, M * N, K * N < 2^31.  No output (the workspace among them) may overlap
@@ -664,8 +665,10 @@ int hsq_kv_cache_read(const uint8_t *cache, int num_pages, int page_size, int kv
  *                kv_heads, head_dim, batch, max_tokens, table_width * page_size)
  *                device bytes (NULL is fine where that is 0); contents do not
  *                matter; calls that overlap in time need one each
- * (max_tokens is T / batch where cu_tokens is NULL.)  The scores are fp32; exp(e)
- * times a value's scale is rounded to 11 bits for a 16-bit Y, to 22 for fp32.
+ * (max_tokens is T / batch where cu_tokens is NULL.)  The scores are fp32 sums,
+ * whose terms q n of a group of 64 channels are cut at 2^-14 of the row's largest |q|
+ * for a 16-bit Y (lse with it), at 2^-20 for fp32; exp(e) times a value's scale is
+ * rounded to 11 bits, or to 22, and the sums of values cut likewise.
  * Results do not depend on timing: sums run in a fixed order.  No output (the
  * workspace among them) may overlap another operand: HSQ_E_INVAL.
  * Errors: HSQ_E_INVAL, HSQ_E_SHAPE (as above, or kv_heads does not divide
