@@ -546,9 +546,12 @@ __device__ __forceinline__ int kv_len(const KvCache &c, int b) {
   return (int)min((int64_t)max(c.lens[b], 0), cap);
 }
 
-// Tile `tile` of sequence b, head h; null where the table names no page.
+// Tile `tile` of sequence b, head h; null where the table names no page.  The table
+// is read as constant memory, by the scalar unit: a vector load between others would
+// have to wait for all of them.
 __device__ __forceinline__ const uint8_t *kv_tile_at(const KvCache &c, int b, int h, int tile) {
-  const int page = c.table[(size_t)b * c.width + (tile >> c.page_shift)];
+  typedef const int32_t __attribute__((address_space(4))) *Constant;
+  const int page = *(Constant)(uintptr_t)(c.table + (size_t)b * c.width + (tile >> c.page_shift));
   if ((unsigned)page >= (unsigned)c.num_pages) return nullptr;
   const size_t at = (((size_t)page * c.H + h) << c.page_shift) + (tile & ((1 << c.page_shift) - 1));
   return c.cache + at * (size_t)kv_tile_bytes(c.D);
