@@ -94,13 +94,14 @@ def attention64(Q, k, v, ks, vs, pos, scale, causal, window, y_dtype):
     half a unit: a group's score is the difference of two sums of 64 terms below
     31 |q|, each addition off by 2 U, then a few roundings; the codes are subnormal
     numbers, whose exponent the matrix unit takes to be that of 2^-14, so that 64
-    terms and the sum before each instruction, 16 at most, are cut at 2^-14 of the
-    largest |q|, or 2^-20 where the result is fp32; exp2's argument is off
+    terms and the sum before each instruction, 16 at most, are cut at 2^-20 of the
+    largest |q| with codes of 2^-18; exp2's argument is off
     by U (4 |e| log2(e) + 64) and its result by two units (so eta, relative);
     p s is rounded to fp16 (2^-11) or to two (2^-21), not below 2^-32 of the row's
     largest; the sums over N tokens add 2 N U: of |v|, or, where the result has 16
     bits, of p s n and p s z apart, 30 p s in all; and their terms, N and an instruction's
-    start every four, are cut likewise at 2^-14 (2^-20) of the largest p s."""
+    start every four, are cut likewise at 2^-14 (codes of 2^-24; 2^-20 where the result is
+    fp32) of the largest p s."""
     n, Hq, D = Q.shape
     N, H, _ = k.shape
     G = D // 64
@@ -133,7 +134,7 @@ def attention64(Q, k, v, ks, vs, pos, scale, causal, window, y_dtype):
         aa = torch.mm(p, vh.abs()) / div
         a = q[:, hq].abs().view(n, G, 64).sum(2)
         most = q[:, hq].abs().view(n, G, 64).amax(2)
-        de = scale * torch.mm(31 * 264 * U32 * a + 80 * unit * most, ks[:, hk].double().t().contiguous())
+        de = scale * torch.mm(31 * 264 * U32 * a + 80 * 2.0 ** -20 * most, ks[:, hk].double().t().contiguous())
         de = torch.where(seen, de, torch.zeros_like(de)).amax(1, keepdim=True)
         big = torch.where(seen, e.abs(), torch.zeros_like(e)).amax(1, keepdim=True)
         eta = de + U32 * (4 * 1.45 * big + 64) * 0.7 + 8 * U32

@@ -11,16 +11,15 @@
 //
 // (where the result is fp32 the second is summed as (p_t s_g) (n_d - z_g), which
 // costs a subtraction a pair of codes and keeps what the difference cancels).
-// A nibble n in the lowest bits of a 16-bit half is the subnormal fp16 number n
-// 2^-24, and in the next four n 2^-20; the matrix unit takes both without loss.  A
-// dword of eight codes is thus four masks and one shift; the powers of two go into
-// the queries and the end.  But the unit aligns the terms of a sum by the exponents
-// that their operands have, which for every subnormal number is that of 2^-14: with
-// codes of 2^-24 a sum keeps 2^-14 of its largest q (or p s), a sixteenth of
-// what rounding p s leaves.  Where the result is fp32 (FINE) the codes are shifted
-// to n 2^-18 instead, which leaves fp32's 2^-20 of it: scores of about 30 then are
-// off by 2e-6 and not by 3e-4, for three more shifts a dword (64 sequences of 4096
-// tokens: 64 us, with the rest that fp32 costs, against 58).
+// A nibble n at the low end of a 16-bit half is a subnormal fp16 number, which the
+// matrix unit takes without loss; the powers of two go into the factors and the end.
+// But the unit aligns the terms of a sum by the exponents that their operands have,
+// which for every subnormal number is that of 2^-14.  Shifted to n 2^-18 (FINE: four
+// masks and four shifts for eight codes) a sum keeps fp32's 2^-20 of its largest q
+// (or p s).  As n 2^-24 and n 2^-20, where the nibbles lie (four masks and one shift),
+// it keeps 2^-14: scores of about 30, and lse, would be off by 3e-4 instead of 2e-6, so
+// the keys are shifted; for the values that is a sixteenth of what rounding p s
+// leaves, and they are shifted where the result is fp32.
 // Queries are held in fp16 under a power of two per row
 // (what that loses is below 2^-34 of the row's largest channel), their sums
 // against 1 and not against a code of 1.  p s is the only value that is rounded: to
@@ -80,12 +79,10 @@ __device__ __forceinline__ v4f mfma4(v2u a, v2u b, v4f c) {
 // Eight codes as subnormal numbers: the low nibbles of a dword's bytes 0, 2 and 1, 3
 // and the high ones.  FINE: all n 2^-18, otherwise n 2^-24 and n 2^-20, which saves
 // three shifts a dword.
-constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u, kTopBits = 0x03C003C0u;
+constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u, kTopBits = 0x03C003C0u, kOnes = 0x3C003C00u;
 template <bool FINE>
 struct Unit {
   static constexpr float low = FINE ? 262144.0f : 16777216.0f, high = FINE ? 262144.0f : 1048576.0f;   // one code is 1 / low
-  static constexpr float less = high / low;     // of the queries that meet the high ones
-  static constexpr uint32_t one_low = 0x3C003C00u, one_high = FINE ? 0x3C003C00u : 0x4C004C00u;   // 1 and 1 / less
 };
 template <bool FINE>
 __device__ __forceinline__ v2u low_codes(uint32_t w) {
@@ -151,21 +148,18 @@ __device__ __forceinline__ float magnitude(uint32_t top, int dtype) {
   const uint32_t h = max(top & 0xFFFFu, top >> 16);
   return dtype == kBf16 ? bf16_to_f32(h) : f16_to_f32((uint16_t)h);
 }
-// Eight channels of a query as fp16 by `by`, the last four less where they meet larger codes.
-template <bool FINE>
+// Eight channels of a query as fp16 by `by`.
 __device__ __forceinline__ v4u scaled8(v4u w, int dtype, float by) {
   float f[8];
   unpack8(w, dtype, f);
-  const float high = by * Unit<FINE>::less;
-  return (v4u){pack_h(f[0] * by, f[1] * by), pack_h(f[2] * by, f[3] * by), pack_h(f[4] * high, f[5] * high),
-               pack_h(f[6] * high, f[7] * high)};
+  return (v4u){pack_h(f[0] * by, f[1] * by), pack_h(f[2] * by, f[3] * by), pack_h(f[4] * by, f[5] * by),
+               pack_h(f[6] * by, f[7] * by)};
 }
 // The power of two that takes a row's largest channel to [2^13, 2^14), and the
 // factor from the products' sums to scores in powers of two.
-template <bool FINE>
 __device__ __forceinline__ float row_power(float top, float scale2, float &to_score) {
   const int ex = min(max((int)(__float_as_uint(top) >> 23) - 13, 1), 240);
-  to_score = __uint_as_float((uint32_t)ex << 23) * Unit<FINE>::low * scale2;
+  to_score = __uint_as_float((uint32_t)ex << 23) * Unit<true>::low * scale2;
   return __uint_as_float((uint32_t)(254 - ex) << 23);
 }
 
@@ -253,7 +247,7 @@ struct Sums {
 };
 
 // The scores of 32 tokens: e[m][4 a + r] of token 16 a + 4 q + r.
-template <int D, int MT, bool FINE>
+template <int D, int MT>
 __device__ __forceinline__ void scores(const Side<D> &t, const v4u (&Q)[MT][D / 32], const float (&qs)[MT][D / 64],
                                        float (&e)[MT][8]) {
   constexpr int G = D / kKvGroup;
@@ -265,7 +259,7 @@ __device__ __forceinline__ void scores(const Side<D> &t, const v4u (&Q)[MT][D / 
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int i = a * (D / 32) + 2 * g + x;
-        const v2u low = low_codes<FINE>(t.code[i >> 2][i & 3]), high = high_codes<FINE>(t.code[i >> 2][i & 3]);
+        const v2u low = low_codes<true>(t.code[i >> 2][i & 3]), high = high_codes<true>(t.code[i >> 2][i & 3]);
         k[x] = (v4u){low[0], low[1], high[0], high[1]};
       }
       const uint32_t zw = zeros_of(t.z[g][a]);
@@ -499,15 +493,15 @@ __global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) 
       Q[m][x] = live[m] ? *reinterpret_cast<const v4u *>(src + 32 * x) : (v4u){0u, 0u, 0u, 0u};
       top = larger8(top, Q[m][x]);
     }
-    const float by = row_power<SPLIT>(max_over<16, 32>(magnitude(top, a.dtype)), a.scale2, c2[m]);
+    const float by = row_power(max_over<16, 32>(magnitude(top, a.dtype)), a.scale2, c2[m]);
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x) Q[m][x] = scaled8<SPLIT>(Q[m][x], a.dtype, by);
-    const v4u ones = {Unit<SPLIT>::one_low, Unit<SPLIT>::one_low, Unit<SPLIT>::one_high, Unit<SPLIT>::one_high};
+    for (int x = 0; x < D / 32; ++x) Q[m][x] = scaled8(Q[m][x], a.dtype, by);
+    const v4u ones = {kOnes, kOnes, kOnes, kOnes};
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       v4f d = mfma16(ones, Q[m][2 * g], (v4f){0.0f, 0.0f, 0.0f, 0.0f});
       d = mfma16(ones, Q[m][2 * g + 1], d);
-      qs[m][g] = d[0] * (1.0f / Unit<SPLIT>::low);
+      qs[m][g] = d[0] * (1.0f / Unit<true>::low);
     }
   }
   // tokens that every row of the wave sees
@@ -540,7 +534,7 @@ __global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) 
       const bool there_n = pn != nullptr;
       if (!there_n) pn = a.c.cache;
       float e[MT][8];
-      scores<D, MT, SPLIT>(tk, Q, qs, e);
+      scores<D, MT>(tk, Q, qs, e);
       __builtin_amdgcn_sched_barrier(0);
       load_side<D, false>(pn, lane, tk);
       __builtin_amdgcn_sched_barrier(0);
@@ -755,17 +749,17 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
       }
     float top = magnitude(most, a.dtype);
     if (G > 1) top = max_over<32, 32>(top);
-    const float by = row_power<SPLIT>(top, a.scale2, c2[r]);
+    const float by = row_power(top, a.scale2, c2[r]);
 #pragma unroll
     for (int j = 0; j < kSets; ++j) {
       v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        Q[r][j][n] = scaled8<SPLIT>(Q[r][j][n], a.dtype, by);
-        d = mfma4<-1>((v2u){Unit<SPLIT>::one_low, Unit<SPLIT>::one_low}, (v2u){Q[r][j][n][0], Q[r][j][n][1]}, d);
-        d = mfma4<-1>((v2u){Unit<SPLIT>::one_high, Unit<SPLIT>::one_high}, (v2u){Q[r][j][n][2], Q[r][j][n][3]}, d);
+        Q[r][j][n] = scaled8(Q[r][j][n], a.dtype, by);
+        d = mfma4<-1>((v2u){kOnes, kOnes}, (v2u){Q[r][j][n][0], Q[r][j][n][1]}, d);
+        d = mfma4<-1>((v2u){kOnes, kOnes}, (v2u){Q[r][j][n][2], Q[r][j][n][3]}, d);
       }
-      qs[r][j] = d[0] * (1.0f / Unit<SPLIT>::low);
+      qs[r][j] = d[0] * (1.0f / Unit<true>::low);
     }
   }
   const int full_lo = seen_by(a, (r1 - 1) / a.gr, c.p0, c.len).lo, full_hi = seen_by(a, r0 / a.gr, c.p0, c.len).hi;
@@ -795,7 +789,7 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
       for (int r = 0; r < R; ++r) d[r][0] = d[r][1] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int n = 0; n < 8; ++n) {
-        const v2u lo2 = low_codes<SPLIT>(tk.code[j][n >> 1][n & 1]), hi2 = high_codes<SPLIT>(tk.code[j][n >> 1][n & 1]);
+        const v2u lo2 = low_codes<true>(tk.code[j][n >> 1][n & 1]), hi2 = high_codes<true>(tk.code[j][n >> 1][n & 1]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           d[r][0] = mfma4<-1>(lo2, (v2u){Q[r][j][n][0], Q[r][j][n][1]}, d[r][0]);
