@@ -613,7 +613,8 @@ int hsq_w4a16_lowrank_linear(const uint16_t *X, int M, int K, int N, int batch, 
  *   cu_tokens   in : batch + 1 int32, sequence b's rows of the call are
  *                    [cu_tokens[b], cu_tokens[b+1]) of T; or NULL: T / batch rows
  *                    each.  Its n rows are positions kv_lens[b] - n and on.
- *   max_tokens     : no sequence has more rows (ignored where cu_tokens is NULL);
+ *   max_tokens     : no sequence has more rows (a bound, which may be above T;
+ *                    ignored where cu_tokens is NULL);
  *                    rows beyond it are left alone
  * (these three arrays are 4-byte aligned).  They are read on the device only, and
  * whatever they hold, no access leaves the operands: a position that is
@@ -666,9 +667,9 @@ int hsq_kv_cache_read(const uint8_t *cache, int num_pages, int page_size, int kv
  *                device bytes (NULL is fine where that is 0); contents do not
  *                matter; calls that overlap in time need one each
  * (max_tokens is T / batch where cu_tokens is NULL.)  The scores are fp32 sums,
- * whose terms q n of a group of 64 channels are cut at 2^-14 of the row's largest |q|
- * for a 16-bit Y (lse with it), at 2^-20 for fp32; exp(e) times a value's scale is
- * rounded to 11 bits, or to 22, and the sums of values cut likewise.
+ * whose terms q n of a group of 64 channels are cut at 2^-20 of the row's largest |q|;
+ * exp(e) times a value's scale is rounded to 11 bits for a 16-bit Y, to 22 for fp32,
+ * and the terms of the sums of values are cut at 2^-14, or 2^-20, of the largest.
  * Results do not depend on timing: sums run in a fixed order.  No output (the
  * workspace among them) may overlap another operand: HSQ_E_INVAL.
  * Errors: HSQ_E_INVAL, HSQ_E_SHAPE (as above, or kv_heads does not divide

@@ -94,7 +94,7 @@ WHERE = [
     (dict(D=32), hsq.E_SHAPE), (dict(page=16), hsq.E_SHAPE), (dict(page=96), hsq.E_SHAPE), (dict(page=1 << 21), hsq.E_SHAPE),
     (dict(page=0), hsq.E_SHAPE), (dict(page=-64), hsq.E_SHAPE), (dict(pages=0), hsq.E_INVAL), (dict(width=0), hsq.E_INVAL),
     (dict(width=1 << 25), hsq.E_INVAL), (dict(cu=None, T=13), hsq.E_SHAPE), (dict(top=0), hsq.E_INVAL),
-    (dict(top=13), hsq.E_INVAL), (dict(cache=None), hsq.E_INVAL), (dict(table=None), hsq.E_INVAL),
+    (dict(top=-13), hsq.E_INVAL), (dict(cache=None), hsq.E_INVAL), (dict(table=None), hsq.E_INVAL),
     (dict(lens=None), hsq.E_INVAL), (dict(cache=at(0) + 8), hsq.E_ALIGN), (dict(table=at(1) + 2), hsq.E_ALIGN),
     (dict(lens=at(2) + 1), hsq.E_ALIGN), (dict(cu=at(3) + 2), hsq.E_ALIGN), (dict(table=at(1) + 4), None),
     (dict(cu=None, top=-9), None), (dict(b=65535, T=1 << 24, top=1 << 24), hsq.E_INVAL),
@@ -164,6 +164,8 @@ def test_sizes():
                 n = g(200 * B, 8, 2, D, B, m, 1 << 17)
                 assert last is None or n <= last
                 last = n
+    # above the rows there are it is their number
+    assert g(5, 8, 2, 128, 1, 5, 1 << 17) == g(5, 8, 2, 128, 1, 6, 1 << 17) == g(5, 8, 2, 128, 1, 1 << 30, 1 << 17) > 0
 
 
 def test_sizes_beyond_an_int():

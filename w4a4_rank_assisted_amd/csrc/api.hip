@@ -182,7 +182,7 @@ int kv_check(KvCache &c, const uint8_t *cache, int num_pages, int page_size, int
              const int32_t *table, int width, const int32_t *lens, const int32_t *cu, int batch, int T,
              int max_tokens) {
   if (T < 1 || T > kKvMaxRows || batch < 1 || batch > kKvMaxBatch || kv_heads < 1 || kv_heads > kKvMaxHeads ||
-      num_pages < 1 || width < 1 || (cu && (max_tokens < 1 || max_tokens > T)))
+      num_pages < 1 || width < 1 || (cu && max_tokens < 1))
     return HSQ_E_INVAL;
   const int shift = kv_page_shift(page_size);
   if (!kv_dim_ok(head_dim) || shift < 0 || (!cu && T % batch != 0)) return HSQ_E_SHAPE;
@@ -191,7 +191,7 @@ int kv_check(KvCache &c, const uint8_t *cache, int num_pages, int page_size, int
   if (!aligned16(cache)) return HSQ_E_ALIGN;
   for (const int32_t *p : {table, lens, cu})
     if ((uintptr_t)p & 3u) return HSQ_E_ALIGN;
-  c = KvCache{cache, num_pages, shift, kv_heads, head_dim, table, width, lens, cu, batch, T, cu ? max_tokens : T / batch};
+  c = KvCache{cache, num_pages, shift, kv_heads, head_dim, table, width, lens, cu, batch, T, cu ? std::min(max_tokens, T) : T / batch};
   const long long tiles = (c.max_tokens + 2LL * kKvTile - 2) / kKvTile;
   return tiles * batch * kv_heads < kKvMaxBlocks ? HSQ_OK : HSQ_E_INVAL;
 }
@@ -205,7 +205,7 @@ size_t rows_bytes(int T, int stride, size_t row, int elem) { return ((size_t)(T 
 
 int kv_attention_sizes(int T, int q_heads, int kv_heads, int head_dim, int batch, int max_tokens, int capacity) {
   if (T < 1 || T > kKvMaxRows || batch < 1 || batch > kKvMaxBatch || kv_heads < 1 || kv_heads > kKvMaxHeads ||
-      q_heads < 1 || q_heads > kKvMaxHeads || max_tokens < 1 || max_tokens > T || capacity < 1 ||
+      q_heads < 1 || q_heads > kKvMaxHeads || max_tokens < 1 || capacity < 1 ||
       capacity > kKvMaxCapacity)
     return HSQ_E_INVAL;
   if (!kv_dim_ok(head_dim) || q_heads % kv_heads != 0) return HSQ_E_SHAPE;
@@ -1113,6 +1113,7 @@ int hsq_kv_cache_read(const uint8_t *cache, int num_pages, int page_size, int kv
 
 size_t hsq_kv_attention_workspace_bytes(int T, int q_heads, int kv_heads, int head_dim, int batch, int max_tokens,
                                         int capacity) {
+  max_tokens = std::min(max_tokens, T);
   if (kv_attention_sizes(T, q_heads, kv_heads, head_dim, batch, max_tokens, capacity) != HSQ_OK) return 0;
   return plan_kv_attention(T, q_heads, kv_heads, head_dim, batch, max_tokens, capacity).total;
 }
