@@ -240,16 +240,15 @@ __global__ __launch_bounds__(kPrepThreads) void k_w4a16_prep(W4a16Args a) {
       uw[(size_t)j * M16 + m] = v;
     }
   } else {
-    // a thread a column, and a part of the channels
-    const int per = max(1, kPrepThreads / a.r), at_once = kPrepThreads / per, col = tid / per, sub = tid % per;
-    for (int c0 = 0; c0 < a.r; c0 += at_once) {
-      const int c = c0 + col;
-      const bool mine = c < a.r && col < at_once;
+    // a thread a column and every per-th channel, so that neighbours read neighbours;
+    // then eight lanes a sum
+    const int per = kPrepThreads / a.r, col = tid % a.r, sub = tid / a.r;
+    if (sub < per) {
       float u[kPrepRows] = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int k = sub; mine && k < nk; k += per * kPrepLoads) {
+      for (int k = sub; k < nk; k += per * kPrepLoads) {
         uint16_t w[kPrepLoads];
 #pragma unroll
-        for (int e = 0; e < kPrepLoads; ++e) w[e] = k + e * per < nk ? l1[(k + e * per) * a.r + c] : (uint16_t)0;
+        for (int e = 0; e < kPrepLoads; ++e) w[e] = k + e * per < nk ? l1[(k + e * per) * a.r + col] : (uint16_t)0;
 #pragma unroll
         for (int e = 0; e < kPrepLoads; ++e) {
           if (k + e * per >= nk) continue;
@@ -261,13 +260,16 @@ __global__ __launch_bounds__(kPrepThreads) void k_w4a16_prep(W4a16Args a) {
       }
 #pragma unroll
       for (int m = 0; m < kPrepRows; ++m) red[m * kPrepThreads + tid] = u[m];
-      __syncthreads();
-      for (int m = sub; mine && m < rows; m += per) {
-        float v = 0.0f;
-        for (int p = 0; p < per; ++p) v += red[m * kPrepThreads + tid - sub + p];
-        uw[(size_t)c * M16 + m] = v;
-      }
-      __syncthreads();
+    }
+    __syncthreads();
+    for (int p = tid >> 3; p < rows * a.r; p += kPrepThreads / 8) {
+      const int m = p / a.r, c = p % a.r;
+      float v = 0.0f;
+      for (int n = tid & 7; n < per; n += 8) v += red[m * kPrepThreads + n * a.r + c];
+      v += __shfl_xor(v, 1);
+      v += __shfl_xor(v, 2);
+      v += __shfl_xor(v, 4);
+      if ((tid & 7) == 0) uw[(size_t)c * M16 + m] = v;
     }
   }
 }
@@ -920,7 +922,7 @@ W4a16Plan plan_w4a16(int M, int K, int N, int r, int batch, int group, bool smoo
   // Parts of K until there is a workgroup per compute unit.  They cost a launch, so none
   // has fewer than eight pairs (16 x 1024 x 4096 takes 4.9 us whole and 6.3 in two, 8 x
   // 4096 x 1024 8.2 and in four 6.4), or about four where that launch then has the rank
-  // branch (37 x 1088 x 1000, rank 5: 16.9 whole, 14.1 in three; 16 x 512 x 1024, rank 8: 8.7
+  // branch (37 x 1088 x 1000, rank 5: 16.9 whole, 14.1 in three, 12.5 since U is read in order; 16 x 512 x 1024, rank 8: 8.7
   // whole, 10.0 in two).
   const int wgs = ceil_div(tiles, kColumnTiles) * batch * (M <= kTile ? 1 : ceil_div(M, 2 * kTile));
   p.splits = std::max(1, std::min({kW4a16Splits, kCUs / wgs, r > 0 ? ceil_div(K, 8 * kGroup) : K / (16 * kGroup)}));
