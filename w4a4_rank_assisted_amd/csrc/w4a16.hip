@@ -922,8 +922,8 @@ W4a16Plan plan_w4a16(int M, int K, int N, int r, int batch, int group, bool smoo
   // Parts of K until there is a workgroup per compute unit.  They cost a launch, so none
   // has fewer than eight pairs (16 x 1024 x 4096 takes 4.9 us whole and 6.3 in two, 8 x
   // 4096 x 1024 8.2 and in four 6.4), or about four where that launch then has the rank
-  // branch (37 x 1088 x 1000, rank 5: 16.9 whole, 14.1 in three, 12.5 since U is read in order; 16 x 512 x 1024, rank 8: 8.7
-  // whole, 10.0 in two).
+  // branch (37 x 1088 x 1000, rank 5: 16.9 whole, 14.1 in three, and 12.5 since L1 is
+  // read in order; 16 x 512 x 1024, rank 8: 8.7 whole, 10.0 in two).
   const int wgs = ceil_div(tiles, kColumnTiles) * batch * (M <= kTile ? 1 : ceil_div(M, 2 * kTile));
   p.splits = std::max(1, std::min({kW4a16Splits, kCUs / wgs, r > 0 ? ceil_div(K, 8 * kGroup) : K / (16 * kGroup)}));
   size_t off = 0;
