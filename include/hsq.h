@@ -659,7 +659,8 @@ int hsq_kv_cache_read(const uint8_t *cache, int num_pages, int page_size, int kv
  * with lse = -infinity; what it does not see has no part in it, NaN either.
  *   Q       in : T x q_heads x head_dim of `dtype` (HSQ_BF16 or HSQ_F16), row
  *                stride q_stride
- *   scale      : positive, 1e30 at most
+ *   scale      : positive, 1e30 at most; where it takes a row's largest |q| to 2^122
+ *                or beyond, that row's lse is cut (Y, of finite scores, is not affected)
  *   Y       out: T x q_heads x head_dim dense of y_dtype (HSQ_F32 or `dtype`)
  *   lse     out: T x q_heads fp32, or NULL
  *   workspace  : ws_bytes >= hsq_kv_attention_workspace_bytes(T, q_heads,

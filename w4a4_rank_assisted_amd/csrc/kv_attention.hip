@@ -156,10 +156,14 @@ __device__ __forceinline__ v4u scaled8(v4u w, int dtype, float by) {
                pack_h(f[6] * by, f[7] * by)};
 }
 // The power of two that takes a row's largest channel to [2^13, 2^14), and the
-// factor from the products' sums to scores in powers of two.
+// factor from the products' sums to scores in powers of two.  The factor stays a normal
+// number: as 0 it would make NaN of a hidden token's -infinity, as an infinity of a sum
+// of 0.  Below 2^-126 it leaves every weight 1 as it was (sums are below 2^40); beyond
+// fp32 any two sums that differ are more than 2^60 apart, and only lse is cut.
 __device__ __forceinline__ float row_power(float top, float scale2, float &to_score) {
   const int ex = min(max((int)(__float_as_uint(top) >> 23) - 13, 1), 240);
-  to_score = __uint_as_float((uint32_t)ex << 23) * Unit<true>::low * scale2;
+  to_score = __uint_as_float((uint32_t)ex << 23) * (Unit<true>::low * scale2);
+  to_score = fminf(fmaxf(to_score, 0x1p-126f), 0x1.fffffep127f);
   return __uint_as_float((uint32_t)(254 - ex) << 23);
 }
 
