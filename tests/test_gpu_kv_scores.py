@@ -96,3 +96,77 @@ def test_the_largest_queries_and_scales(D, q):
         wl = 2.0 ** power * scale
         if wl < 2.0 ** 122:
             assert bool(((lse.double() - wl).abs() <= 8 * U32 * wl).all())
+
+
+# Channel 0 of the queries is 2^p, p another for every row and head, so that rows of
+# scores near zero and far ones share a wave; one key a head holds 7 there and the others
+# less, by 1 at least, which for 2^7 and more is a weight below 2^-180: y is its value.  The
+# values' scales are powers of two from 2^-14 to 2^12.  A weight times its scale is rounded
+# once to fp16 for bf16 results, to two terms for the others (2^-21); the rest is a few
+# roundings of fp32.
+@pytest.mark.parametrize("form", FORMS, **ids)
+@pytest.mark.parametrize("ydt", ["f32", "bf16"])
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+def test_one_token_at_every_distance(form, ydt, where):
+    Hq, H, D, q, n = form
+    G, last = Hq // H, n - q + 1
+    g = torch.Generator().manual_seed(103)
+    v = torch.randint(-7, 8, (n, H, D), generator=g).float()
+    v[:, :, ::64] = 7.0
+    v = (v * torch.exp2(torch.randint(-14, 13, (n, H, 1), generator=g).float())).to(torch.bfloat16).to(DEV)
+    # the others rise along the sequence, so that offsets move
+    codes = (torch.linspace(-7.0, 6.49, n).round()[:, None]).repeat(1, H)
+    at = {"first": 0, "middle": last // 2, "last": last - 1}[where]
+    pick = torch.tensor([max(0, at - 7 * h) for h in range(H)])
+    codes[pick, torch.arange(H)] = 7.0
+    k = one_channel_keys(g, codes, H, D)
+    cache, table = fill(k, v, [n], 32, "sym", spare=160)
+    powers = [7, 13, 20, 22, 24, 26, 27, 28, 30, 45, 61, 99, 110]
+    p = torch.tensor([[powers[(3 * i + h) % len(powers)] for h in range(Hq)] for i in range(q)]).double()
+    Q = torch.zeros(q, Hq, D, dtype=torch.bfloat16, device=DEV)
+    Q[:, :, 0] = torch.exp2(p).to(torch.bfloat16).to(DEV)
+    print(f"[scores] {form} {ydt} {where}", flush=True)
+    y, lse = hsq.kv_attention(Q, cache, table, i32(n), scale=1.0, y_dtype=ydt, return_lse=True)
+    want = held64(v, "sym")[pick.to(DEV), torch.arange(H, device=DEV)].repeat_interleave(G, 0)[None].expand(q, -1, -1)
+    rel = 8 * U32 + (2.0 ** -21 if ydt == "f32" else 2.0 ** -11 + half_step(DT[ydt]) * (1 + 2.0 ** -10))
+    assert bool(((y.double() - want).abs() <= want.abs() * rel + 1e-30).all())
+    wl = 7 * torch.exp2(p).to(DEV)
+    assert bool(((lse.double() - wl).abs() <= 8 * U32 * wl.abs()).all())
+
+
+@pytest.mark.parametrize("form", FORMS, **ids)
+@pytest.mark.parametrize("power", [24, 28, 33, 100])
+def test_many_tokens_far_above_zero(form, power):
+    # tokens of one score count alike, however far it is
+    Hq, H, D, q, n = form
+    g = torch.Generator().manual_seed(104)
+    v = whole_values(g, n, H, D)
+    k = one_channel_keys(g, torch.full((n, H), 7.0), H, D)
+    cache, table = fill(k, v, [n], 32, "sym", spare=160)
+    Q = torch.zeros(q, Hq, D, dtype=torch.bfloat16, device=DEV)
+    Q[:, :, 0] = 2.0 ** power
+    print(f"[scores] {form} 2^{power}", flush=True)
+    y, lse = hsq.kv_attention(Q, cache, table, i32(n), scale=1.0, y_dtype="f32", return_lse=True)
+    check_means(y, v, q, Hq // H, "f32")
+    wl = 7 * 2.0 ** power + torch.log(means(v, q, Hq // H)[1])
+    assert bool(((lse.double() - wl).abs() <= 8 * U32 * wl.abs()).all())
+
+
+@pytest.mark.parametrize("form", FORMS, **ids)
+def test_a_far_row_that_rises_to_zero(form):
+    # the tokens of score 0 come behind others of -7 |q|, which are far below
+    Hq, H, D, q, n = form
+    g = torch.Generator().manual_seed(106)
+    v = whole_values(g, n, H, D)
+    codes = torch.full((n, H), -7.0)
+    codes[n - q - 2:] = 0.0
+    k = one_channel_keys(g, codes, H, D)
+    cache, table = fill(k, v, [n], 32, "sym", spare=160)
+    for power in (23, 40, 90):
+        Q = torch.zeros(q, Hq, D, dtype=torch.bfloat16, device=DEV)
+        Q[:, :, 0] = 2.0 ** power
+        print(f"[scores] {form} 2^{power}", flush=True)
+        y, lse = hsq.kv_attention(Q, cache, table, i32(n), scale=1.0, y_dtype="f32", return_lse=True)
+        check_means(y, v[n - q - 2:], q, Hq // H, "f32")
+        wl = torch.log(means(v[n - q - 2:], q, Hq // H)[1])
+        assert bool(((lse.double() - wl).abs() <= 8 * U32 * (wl + 1)).all())

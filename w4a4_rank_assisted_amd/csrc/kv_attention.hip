@@ -27,7 +27,13 @@
 // kept by the row's offset o, a whole number: p = 2^(e log2(e) - o) with o such
 // that p s stays below 2^15; o moves, and the sums with it by an exact power of
 // two, only when a tile would exceed that (seven doublings above the tile that set
-// it), so the running maximum of the softmax costs one comparison a tile.
+// it), so the running maximum of the softmax costs one comparison a tile.  Whole numbers
+// are exact up to 2^24, and e log2(e) - o is then one fused operation.  A row whose scores go
+// beyond 2^22 (kFar) has a base b besides, its largest score as fp32 rounds it: the
+// difference to it is 0 for that token and all that tie with it, and p = 2^((e log2(e) - b)
+// - o).  b and o of such rows lie in LDS, and the loop holds the offset of a row that has
+// seen nothing for them, which every tile exceeds: they cost the others nothing (as a branch
+// around them in the loop they took 3 % of a prompt's time).
 //
 // Three forms, by the query rows that share a head of the cache in one sequence:
 //
@@ -61,6 +67,7 @@ constexpr float kTop = 8.0f;             // p s of the tile that sets the offset
 constexpr float kMaxPs = 32768.0f;       // what moves the offset
 constexpr float kMaxP = 1099511627776.0f;   // 2^40: the same for tokens of scale 0
 constexpr float kHidden = -__builtin_inff();   // the score of a token that is not seen
+constexpr float kFar = 4194304.0f;             // 2^22: scores from which a row has a base of its own
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTiny = 5.9604644775390625e-8f;   // 2^-24: of a code in the lowest bits
 
@@ -111,6 +118,13 @@ __device__ __forceinline__ uint32_t zeros_of(uint32_t w) {
 }
 __device__ __forceinline__ float zero_of(uint32_t w, int r) {
   return (float)(w >> (8 * (((r & 1) << 1) | (r >> 1))) & 0xFFu);
+}
+
+// The lane's number, formed where it is used: no register holds it through the loop.
+__device__ __forceinline__ int lane_here() {
+  uint32_t all = ~0u;
+  asm volatile("" : "+s"(all));
+  return (int)__builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0u));
 }
 
 // Reductions over lanes that differ in the bits of FROM .. TO.
@@ -282,15 +296,27 @@ __device__ __forceinline__ void scores(const Side<D> &t, const v4u (&Q)[MT][D / 
   }
 }
 
+// The base of a row that had `had` (0: none) and whose tile's largest score is `high`.
+__device__ __forceinline__ float base_with(float2 had, float high) {
+  const float b = had.x != 0.0f ? fmaxf(had.x, high) : high;
+  return b == 0.0f ? 0x1p-126f : b;      // 0 is none, and scores do not tell the two apart
+}
+// The offset beside base b, where the tile's largest p s is at `near` from it: it moves down
+// only with the base.
+__device__ __forceinline__ float rebase(float near, float b, float2 had) {
+  const float o = __builtin_ceilf(near) - kTop;
+  return had.x == b ? fmaxf(o, had.y) : o;
+}
+
 // Their weights: l, and p s as the second product's operand (w, and w2 what its
 // rounding leaves).  vs: the values' scales; c2: from e to powers of two; masked:
-// some e is hidden.
+// some e is hidden; base: the wave's rows' b and o, b = 0 where a row has none.
 template <int D, int MT, bool SPLIT>
 __device__ __forceinline__ void weigh(const float (&e)[MT][8], v4u (&vs)[D / 64], const float (&c2)[MT], bool masked,
-                                      Sums<D, MT> &s, v4u (&w)[MT][D / 64], v4u (&w2)[MT][D / 64]) {
+                                      float2 *base, Sums<D, MT> &s, v4u (&w)[MT][D / 64], v4u (&w2)[MT][D / 64]) {
   constexpr int G = D / kKvGroup;
   float p[MT][8], top[MT], topp[MT];
-  auto form = [&]() __attribute__((always_inline)) {
+  auto form = [&](auto again) __attribute__((always_inline)) {
     // the scales stay packed: converted for both uses at once they would hold 8 G registers
 #pragma unroll
     for (int g = 0; g < G; ++g) asm volatile("" : "+v"(vs[g]));
@@ -299,8 +325,15 @@ __device__ __forceinline__ void weigh(const float (&e)[MT][8], v4u (&vs)[D / 64]
     for (int m = 0; m < MT; ++m) {
       topp[m] = 0.0f;
 #pragma unroll
+      for (int i = 0; i < 8; ++i) p[m][i] = __builtin_fmaf(e[m][i], c2[m], -s.o[m]);
+      if constexpr (decltype(again)::value) {
+        const float2 b = base[16 * m + (lane_here() & 15)];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[m][i] = b.x != 0.0f ? (e[m][i] * c2[m] - b.x) - b.y : p[m][i];
+      }
+#pragma unroll
       for (int i = 0; i < 8; ++i) {
-        p[m][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(e[m][i], c2[m], -s.o[m]));
+        p[m][i] = __builtin_amdgcn_exp2f(p[m][i]);
         topp[m] = fmaxf(topp[m], p[m][i]);
       }
       top[m] = 0.0f;
@@ -329,15 +362,19 @@ __device__ __forceinline__ void weigh(const float (&e)[MT][8], v4u (&vs)[D / 64]
     }
     return __any(moved) != 0;
   };
-  if (__builtin_expect(form(), 0)) {
+  if (__builtin_expect(form(std::false_type{}), 0)) {
     // rare: the rows that exceed the range take the offset of this tile's largest
     // p s; one value at a time, since the registers used here are the kernel's
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const float mine = top[m] > kMaxPs || topp[m] > kMaxP ? 1.0f : 0.0f;
-      float most = kHidden;
+      const bool move = max_over<16, 32>(mine) > 0.0f;
+      float2 &own = base[16 * m + (lane_here() & 15)];
+      const float2 had = own;
+      float most = kHidden, high = kHidden;      // of e + log2(s), and of e
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
+        high = fmaxf(high, e[m][i] * c2[m]);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           asm volatile("" : "+v"(vs[g]));
@@ -346,9 +383,28 @@ __device__ __forceinline__ void weigh(const float (&e)[MT][8], v4u (&vs)[D / 64]
         __builtin_amdgcn_sched_barrier(0);
       }
       most = max_over<16, 32>(most);
-      const bool move = max_over<16, 32>(mine) > 0.0f;
-      const float o = move ? __builtin_ceilf(most) - kTop : s.o[m];
-      const float al = move ? __builtin_amdgcn_exp2f(s.o[m] - o) : 1.0f;
+      float o = move ? __builtin_ceilf(most) - kTop : s.o[m], al = move ? __builtin_amdgcn_exp2f(s.o[m] - o) : 1.0f;
+      const bool based = move && (had.x != 0.0f || fabsf(most) >= kFar);
+      if (__any(based)) {
+        high = max_over<16, 32>(high);
+        const float b = base_with(had, high);
+        float near = kHidden;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            asm volatile("" : "+v"(vs[g]));
+            near = fmaxf(near, (e[m][i] * c2[m] - b) + __builtin_amdgcn_logf(fmaxf(half_of(vs[g], i), kTiny)));
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        near = rebase(max_over<16, 32>(near), b, had);
+        if (based) {
+          al = __builtin_amdgcn_exp2f((had.x - b) + ((had.x != 0.0f ? had.y : s.o[m]) - near));
+          o = kNoOffset;
+          own = make_float2(b, near);
+        }
+      }
       s.o[m] = o;
       s.l[m] *= al;
 #pragma unroll
@@ -356,7 +412,7 @@ __device__ __forceinline__ void weigh(const float (&e)[MT][8], v4u (&vs)[D / 64]
 #pragma unroll
       for (int g = 0; g < G; ++g) s.zero[m][g] *= al;
     }
-    form();
+    form(std::true_type{});
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -460,8 +516,11 @@ template <int D, int MT, int W, bool SPLIT, bool ROWS>
 __global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) void k_kv_attention(KvAttnArgs a) {
   constexpr int G = D / kKvGroup, kRows = 16 * MT * (ROWS ? W : 1), kLd = D + 4;
   extern __shared__ float lds[];
+  __shared__ float2 base_of[W][16 * MT];
   const int lane = threadIdx.x & 63, q = lane >> 4, col = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float2 *base = base_of[wave];
+  if (lane < 16 * MT) base[lane] = make_float2(0.0f, 0.0f);
   const Place c = place_of(a, ROWS ? 1 : a.splits);
   // the last rows see the most: first
   const int r0 = (int)(gridDim.x - 1 - blockIdx.x) * kRows + (ROWS ? wave * 16 * MT : 0);
@@ -554,7 +613,7 @@ __global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) 
           }
       }
       v4u w[MT][G], w2[MT][G];
-      weigh<D, MT, SPLIT>(e, tv.s, c2, masked, s, w, w2);
+      weigh<D, MT, SPLIT>(e, tv.s, c2, masked, base, s, w, w2);
       values<D, MT, SPLIT>(tv, w, w2, s);
       if (next >= last) break;
       __builtin_amdgcn_sched_barrier(0);
@@ -567,10 +626,17 @@ __global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) 
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     s.l[m] = sum_over<16, 32>(s.l[m]);
+    float back = 1.0f;          // a row with a base leaves with that as its offset: it would swallow o
+    const float2 b = base[16 * m + col];
+    if (b.x != 0.0f) {
+      back = __builtin_amdgcn_exp2f(b.y);
+      s.l[m] *= back;
+      s.o[m] = b.x;
+    }
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
       const float up = x & 1 ? Unit<SPLIT>::high : Unit<SPLIT>::low;
-      s.acc[m][x] = s.acc[m][x] * up - s.zero[m][x / 4] * Unit<SPLIT>::low;
+      s.acc[m][x] = (s.acc[m][x] * up - s.zero[m][x / 4] * Unit<SPLIT>::low) * back;
     }
   }
   if (ROWS) {
@@ -693,8 +759,11 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
   constexpr int G = D / kKvGroup, kSets = Side4<D>::kSets, kTiles = G == 1 ? 2 : 1, kRows = 4 * R, kLd = D + 4;
   __shared__ float lds[W * kRows * kLd];
   __shared__ float2 ol[W * kRows];
+  __shared__ float2 base_of[W][kRows];
   const int lane = threadIdx.x & 63, half = lane >> 5, c4 = (lane >> 2) & 7, j4 = lane & 3;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float2 *base = base_of[wave];         // as in weigh
+  if (lane < kRows) base[lane] = make_float2(0.0f, 0.0f);
   const Place c = place_of(a, a.splits);
   const int r0 = blockIdx.x * kRows;
   if (r0 >= c.rows) return;
@@ -835,14 +904,21 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
     // weights
     v2u w[R][kSets], w2[R][kSets];
     float pw[R][4], ps[R][kSets][4], top[R], topp[R];
-    auto form = [&]() __attribute__((always_inline)) {
+    auto form = [&](auto again) __attribute__((always_inline)) {
       bool moved = false;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         top[r] = topp[r] = 0.0f;
 #pragma unroll
+        for (int i = 0; i < 4; ++i) pw[r][i] = __builtin_fmaf(e[r][i], c2[r], -s.o[r]);
+        if constexpr (decltype(again)::value) {
+          const float2 b = base[4 * r + (lane_here() & 3)];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pw[r][i] = b.x != 0.0f ? (e[r][i] * c2[r] - b.x) - b.y : pw[r][i];
+        }
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
-          pw[r][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(e[r][i], c2[r], -s.o[r]));
+          pw[r][i] = __builtin_amdgcn_exp2f(pw[r][i]);
           topp[r] = fmaxf(topp[r], pw[r][i]);
         }
 #pragma unroll
@@ -858,21 +934,42 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
       }
       return __any(moved) != 0;
     };
-    if (__builtin_expect(form(), 0)) {
+    if (__builtin_expect(form(std::false_type{}), 0)) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const float mine = top[r] > kMaxPs || topp[r] > kMaxP ? 1.0f : 0.0f;
-        float most = kHidden;
+        const bool move = max_over<4, 32>(mine) > 0.0f;
+        float2 &own = base[4 * r + (lane_here() & 3)];
+        const float2 had = own;
+        float most = kHidden, high = kHidden;
 #pragma unroll
-        for (int j = 0; j < kSets; ++j)
+        for (int i = 0; i < 4; ++i) {
+          high = fmaxf(high, e[r][i] * c2[r]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int j = 0; j < kSets; ++j)
             if (!masked || e[r][i] != kHidden)
               most = fmaxf(most, __builtin_fmaf(e[r][i], c2[r], __builtin_amdgcn_logf(fmaxf(half_of(tv.s[j], i), kTiny))));
+        }
         most = max_over<4, 32>(most);
-        const bool move = max_over<4, 32>(mine) > 0.0f;
-        const float o = move ? __builtin_ceilf(most) - kTop : s.o[r];
-        const float al = move ? __builtin_amdgcn_exp2f(s.o[r] - o) : 1.0f;
+        float o = move ? __builtin_ceilf(most) - kTop : s.o[r], al = move ? __builtin_amdgcn_exp2f(s.o[r] - o) : 1.0f;
+        const bool based = move && (had.x != 0.0f || fabsf(most) >= kFar);
+        if (__any(based)) {
+          high = max_over<4, 32>(high);
+          const float b = base_with(had, high);
+          float near = kHidden;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < kSets; ++j)
+              if (!masked || e[r][i] != kHidden)
+                near = fmaxf(near, (e[r][i] * c2[r] - b) + __builtin_amdgcn_logf(fmaxf(half_of(tv.s[j], i), kTiny)));
+          near = rebase(max_over<4, 32>(near), b, had);
+          if (based) {
+            al = __builtin_amdgcn_exp2f((had.x - b) + ((had.x != 0.0f ? had.y : s.o[r]) - near));
+            o = kNoOffset;
+            own = make_float2(b, near);
+          }
+        }
         s.o[r] = o;
         s.l[r] *= al;
         const v4f rows = {quad<0>(al), quad<1>(al), quad<2>(al), quad<3>(al)};
@@ -883,7 +980,7 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
           s.high[r][j] *= rows;
         }
       }
-      form();
+      form(std::true_type{});
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -917,12 +1014,15 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const float l = G == 1 ? sum_over<4, 32>(s.l[r]) : sum_over<4, 16>(s.l[r]);
-    if (lane < 4) ol[wave * kRows + 4 * r + lane] = make_float2(s.o[r], l);
+    const float2 b = base[4 * r + j4];
+    const float back = b.x != 0.0f ? __builtin_amdgcn_exp2f(b.y) : 1.0f;
+    if (lane < 4) ol[wave * kRows + 4 * r + lane] = make_float2(b.x != 0.0f ? b.x : s.o[r], l * back);
+    const v4f backs = {quad<0>(back), quad<1>(back), quad<2>(back), quad<3>(back)};
 #pragma unroll
     for (int j = 0; j < kSets; ++j) {
       const float z = sum_over<4, 16>(s.zero[r][j]);
       const v4f zr = {quad<0>(z), quad<1>(z), quad<2>(z), quad<3>(z)};
-      v4f y0 = s.low[r][j] * Unit<SPLIT>::low - zr, y1 = s.high[r][j] * Unit<SPLIT>::high - zr;
+      v4f y0 = (s.low[r][j] * Unit<SPLIT>::low - zr) * backs, y1 = (s.high[r][j] * Unit<SPLIT>::high - zr) * backs;
       if (G == 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
