@@ -170,3 +170,23 @@ def test_a_far_row_that_rises_to_zero(form):
         check_means(y, v[n - q - 2:], q, Hq // H, "f32")
         wl = torch.log(means(v[n - q - 2:], q, Hq // H)[1])
         assert bool(((lse.double() - wl).abs() <= 8 * U32 * (wl + 1)).all())
+
+
+@pytest.mark.parametrize("form", FORMS, **ids)
+@pytest.mark.parametrize("ydt", ["f32", "bf16"])
+def test_scores_far_below_zero(form, ydt):
+    # all tokens of one score: -7 |q|.  lse: three roundings in the score, and those of the
+    # logarithm's sum and product
+    Hq, H, D, q, n = form
+    g = torch.Generator().manual_seed(102)
+    v = whole_values(g, n, H, D)
+    k = one_channel_keys(g, torch.full((n, H), -7.0), H, D)
+    cache, table = fill(k, v, [n], 32, "sym", spare=160)
+    for power in (20, 60, 97, 100, 112):
+        print(f"[scores] {form} {ydt} 2^{power}", flush=True)
+        Q = torch.zeros(q, Hq, D, dtype=torch.bfloat16, device=DEV)
+        Q[:, :, 0] = 2.0 ** power
+        y, lse = hsq.kv_attention(Q, cache, table, i32(n), scale=1.0, y_dtype=ydt, return_lse=True)
+        check_means(y, v, q, Hq // H, ydt)
+        wl = -7 * 2.0 ** power + torch.log(means(v, q, Hq // H)[1])
+        assert bool(((lse.double() - wl).abs() <= 8 * U32 * wl.abs()).all())

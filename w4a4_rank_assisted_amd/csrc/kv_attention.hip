@@ -62,7 +62,7 @@ namespace {
 
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
-constexpr float kNoOffset = -1e30f;      // of a row that has seen nothing
+constexpr float kNoOffset = -0x1.fffffep127f;   // of a row that has seen nothing: no score lies below
 constexpr float kTop = 8.0f;             // p s of the tile that sets the offset stays below 2^kTop
 constexpr float kMaxPs = 32768.0f;       // what moves the offset
 constexpr float kMaxP = 1099511627776.0f;   // 2^40: the same for tokens of scale 0
