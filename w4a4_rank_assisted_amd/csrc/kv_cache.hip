@@ -10,7 +10,11 @@
 // returns a quotient exactly where fp32 holds it, and a tie is such a quotient (others
 // are 2^-12 away from one, since x and s have 11 bits); 1/s may be off by a few units
 // for that.  (hi - lo) / 15 is the same with 1/15 rounded correctly, which makes it
-// the rounded quotient.
+// the rounded quotient; fp32 holds hi - lo unless one of the two is below 2^-12 of the
+// other, and its quotient is then more than half a unit of fp32 from any tie of fp16 but
+// an exact one, so that rounding it again is harmless.  Where fp32 does not hold it
+// (span_scale's branch, which data of one spread never take), the quotient is rounded to
+// odd, by the sign of what is left, before it is rounded to fp16.
 //
 // A workgroup owns one tile of 32 token positions of one head: it quantises
 // what of them the call brings (eight lanes a group, 16 bytes a lane), lays the
@@ -101,6 +105,20 @@ __device__ __forceinline__ float quotient(float x, float s, float inv) {
   return __builtin_fmaf(__builtin_fmaf(-r, s, x), inv, r);
 }
 
+// (hi - lo) / 15 as fp16, rounded once, lo <= 0 <= hi
+__device__ __forceinline__ uint16_t span_scale(float hi, float lo) {
+  // (fp16 ends at 65504: nothing is lost, and no product overflows)
+  const float d = fminf(hi - lo, 2097152.0f);
+  float q = quotient(d, 15.0f, 1.0f / 15.0f);
+  const float lost = fminf(hi, -lo) - (d - fmaxf(hi, -lo));     // of the sum, exactly, where it is not cut
+  if (__builtin_expect(__any(lost != 0.0f), 0)) {
+    const float left = __builtin_fmaf(-q, 15.0f, d) + lost;     // 15 times what the quotient lacks, its sign exact
+    const uint32_t u = __float_as_uint(q);
+    if (left != 0.0f && d < 2097152.0f) q = __uint_as_float((left < 0.0f ? u - 1 : u) | 1u);
+  }
+  return scale16(q);
+}
+
 // Eight lanes quantise one group; this lane's eight channels -> the codes less the
 // zero, the group's scale and zero.
 template <bool ASYM>
@@ -125,9 +143,7 @@ __device__ __forceinline__ float quantise(const float *x, uint16_t &s16, float *
     for (int e = 0; e < 8; ++e) m[e] = 0.0f;
     return 0.0f;
   }
-  // (fp16 ends at 65504: nothing is lost, and no product overflows)
-  constexpr float kSteps = ASYM ? 15.0f : 7.0f;
-  s16 = scale16(quotient(fminf(ASYM ? hi - lo : __uint_as_float(ab), 2097152.0f), kSteps, 1.0f / kSteps));
+  s16 = ASYM ? span_scale(hi, lo) : scale16(quotient(fminf(__uint_as_float(ab), 2097152.0f), 7.0f, 1.0f / 7.0f));
   const float s = f16_to_f32(s16), inv = s > 0.0f ? __builtin_amdgcn_rcpf(s) : 0.0f;
   const float z = ASYM ? fminf(__builtin_rintf(quotient(-lo, s, inv)), 15.0f) : 8.0f;
 #pragma unroll
