@@ -970,7 +970,7 @@ def kv_cache_write(K, V, cache, block_table, kv_lens, cu_tokens=None, *, quant: 
     cache (in place).  Sequence b's tokens are rows cu_tokens[b] .. cu_tokens[b+1]
     (int32, None: T / batch each) and its last positions: kv_lens[b] (int32) counts
     them already.  block_table (batch, pages) int32.  max_tokens: no sequence has
-    more rows (None: T).  quant "asym" or "sym".  K and V may be slices of one
+    more rows (None: T); rows beyond it are left alone.  quant "asym" or "sym".  K and V may be slices of one
     joint projection."""
     T = _t()
     lib = _load()

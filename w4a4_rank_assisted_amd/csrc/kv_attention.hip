@@ -470,7 +470,7 @@ __device__ __forceinline__ Place place_of(const KvAttnArgs &a, int splits) {
   c.b = splits == 1 ? blockIdx.z : blockIdx.z / splits;
   int n;
   kv_rows(a.c, c.b, c.start, n);
-  c.rows = n * a.gr;
+  c.rows = min(n, a.c.max_tokens) * a.gr;      // positions count all rows, the others are left alone
   c.len = kv_len(a.c, c.b);
   c.p0 = max(a.c.lens[c.b], 0) - n;
   return c;
@@ -1054,7 +1054,7 @@ __global__ __launch_bounds__(256) void k_kv_join(KvAttnArgs a, int block_rows) {
   const int tid = threadIdx.x, lane = tid % kLanes, grp = tid / kLanes, r = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   int start, n;
   kv_rows(a.c, b, start, n);
-  const int rows = n * a.gr, r0 = r / block_rows * block_rows;
+  const int rows = min(n, a.c.max_tokens) * a.gr, r0 = r / block_rows * block_rows;
   if (r >= rows) return;
   const int len = kv_len(a.c, b), p0 = max(a.c.lens[b], 0) - n;
   int first, last;

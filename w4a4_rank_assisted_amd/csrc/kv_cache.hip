@@ -72,7 +72,8 @@ __device__ __forceinline__ bool span_of(const KvCache &c, int tiles, Span &s) {
   const int len = max(c.lens[s.b], 0), p0 = len - n, first = max(p0, 0);
   s.tile = first / kKvTile + (int)(blockIdx.x % tiles);
   s.lo = (int)max((int64_t)first, min((int64_t)s.tile * kKvTile, (int64_t)len));
-  s.hi = (int)min((int64_t)kv_len(c, s.b), (int64_t)(s.tile + 1) * kKvTile);
+  // rows beyond max_tokens are left alone: they may lie in a tile that others begin
+  s.hi = (int)min((int64_t)min(kv_len(c, s.b), p0 + min(n, c.max_tokens)), (int64_t)(s.tile + 1) * kKvTile);
   s.row0 = start - p0;
   return s.lo < s.hi;
 }
@@ -254,11 +255,11 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvMoveArgs a, int tiles) {
   kv_rows(a.c, b, start, n);
   // row i of the sequence is position p0 + i; one that holds nothing (negative,
   // past the table, on no page) is a row all the same, and reads zero
-  const int p0 = max(a.c.lens[b], 0) - n, len = kv_len(a.c, b);
+  const int p0 = max(a.c.lens[b], 0) - n, len = kv_len(a.c, b), rows = min(n, a.c.max_tokens);
   const int first = p0 >= 0 ? p0 / kKvTile : -((kKvTile - 1 - p0) / kKvTile);
   const int tile = first + (int)(blockIdx.x % tiles);
   const int64_t base = (int64_t)tile * kKvTile;
-  if (base >= (int64_t)p0 + n) return;
+  if (base >= (int64_t)p0 + rows) return;
   const uint8_t *src = base >= 0 && base < len ? kv_tile_at(a.c, b, h, tile) : nullptr;
   if (src) {
     for (int i = tid; i < L::kBytes / 16; i += kThreads)
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvMoveArgs a, int tiles) {
     const int side = it / G, i = (it % G) * kThreads + tid;
     const int g = (i >> 3) % G, t = (i >> 3) / G;
     const int64_t p = base + t, row = p - p0;
-    if (row < 0 || row >= n) continue;
+    if (row < 0 || row >= rows) continue;
     float y[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (src && p < len) {
       const float s = f16_to_f32(*reinterpret_cast<const uint16_t *>(buf + L::scale(side, t, g)));
