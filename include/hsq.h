@@ -669,7 +669,7 @@ int hsq_kv_cache_read(const uint8_t *cache, int num_pages, int page_size, int kv
  *                matter; calls that overlap in time need one each
  * (max_tokens is T / batch where cu_tokens is NULL.)  The scores are fp32 sums,
  * whose terms q n of a group of 64 channels are cut at 2^-20 of the row's largest |q|;
- * exp(e) times a value's scale is rounded to 11 bits for a 16-bit Y, to 22 for fp32,
+ * exp(e) times a value's scale is rounded to 11 bits for a bf16 Y, to 22 for fp16 and fp32,
  * and the terms of the sums of values are cut at 2^-14, or 2^-20, of the largest.
  * Results do not depend on timing: sums run in a fixed order.  No output (the
  * workspace among them) may overlap another operand: HSQ_E_INVAL.
