@@ -670,7 +670,10 @@ int hsq_kv_cache_read(const uint8_t *cache, int num_pages, int page_size, int kv
  * (max_tokens is T / batch where cu_tokens is NULL.)  The scores are fp32 sums,
  * whose terms q n of a group of 64 channels are cut at 2^-20 of the row's largest |q|;
  * exp(e) times a value's scale is rounded to 11 bits for a bf16 Y, to 22 for fp16 and fp32,
- * and the terms of the sums of values are cut at 2^-14, or 2^-20, of the largest.
+ * neither finer than 2^-32 of the row's largest over all groups of 64 channels (so a group
+ * whose scales are 2^-10 of another's loses bits of an fp32 Y, 2^-21 of a 16-bit one, and
+ * is 0 below 2^-33);
+ * and the terms of the sums of values are cut at 2^-14, or 2^-20, of the group's largest.
  * Results do not depend on timing: sums run in a fixed order.  No output (the
  * workspace among them) may overlap another operand: HSQ_E_INVAL.
  * Errors: HSQ_E_INVAL, HSQ_E_SHAPE (as above, or kv_heads does not divide

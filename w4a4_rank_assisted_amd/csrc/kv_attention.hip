@@ -30,7 +30,9 @@
 // kept by the row's offset o, a whole number: p = 2^(e log2(e) - o) with o such
 // that p s stays below 2^15; o moves, and the sums with it by an exact power of
 // two, only when a tile would exceed that (seven doublings above the tile that set
-// it), so the running maximum of the softmax costs one comparison a tile.  Whole numbers
+// it), so the running maximum of the softmax costs one comparison a tile.  All groups
+// share it, and fp16 ends at 2^-24: p s is not held finer than 2^-32 of the row's largest,
+// which a group of values that small beside another feels.  Whole numbers
 // are exact up to 2^24, and e log2(e) - o is then one fused operation.  A row whose scores go
 // beyond 2^22 (kFar) has a base b besides, its largest score as fp32 rounds it: the
 // difference to it is 0 for that token and all that tie with it, and p = 2^((e log2(e) - b)
