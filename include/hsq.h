@@ -623,9 +623,10 @@ int hsq_w4a16_lowrank_linear(const uint16_t *X, int M, int K, int N, int batch, 
  * in the attention.  Rows of no sequence are left as they were.  Two rows of one
  * call must not be written to the same place (a page named twice).
  * Limits: batch <= 65535, heads <= 4096, T <= 2^24, table_width * page_size <=
- * 2^30, and launches of fewer than 2^23 workgroups: HSQ_E_INVAL.  Strides are in elements from
- * row to row, multiples of 8 and no less than a dense row; the heads of a row are
- * dense. */
+ * 2^30, batch * max_tokens < 2^36, and launches of fewer than 2^23 workgroups (which
+ * follow T, not batch * max_tokens, where that is a loose bound): HSQ_E_INVAL.
+ * Strides are in elements from row to row, multiples of 8 and no less than a dense
+ * row; the heads of a row are dense. */
 size_t hsq_kv_page_bytes(int page_size, int kv_heads, int head_dim);
 
 /* Writes T rows of keys and values (T x kv_heads x head_dim, HSQ_BF16 or HSQ_F16,

@@ -970,8 +970,8 @@ def kv_cache_write(K, V, cache, block_table, kv_lens, cu_tokens=None, *, quant: 
     cache (in place).  Sequence b's tokens are rows cu_tokens[b] .. cu_tokens[b+1]
     (int32, None: T / batch each) and its last positions: kv_lens[b] (int32) counts
     them already.  block_table (batch, pages) int32.  max_tokens: no sequence has
-    more rows (None: T); rows beyond it are left alone.  quant "asym" or "sym".  K and V may be slices of one
-    joint projection."""
+    more rows (None: T); rows beyond it are left alone.  quant "asym" or "sym".  K
+    and V may be slices of one joint projection."""
     T = _t()
     lib = _load()
     dev = _device(T, K, "K")
@@ -1035,7 +1035,10 @@ def kv_attention(Q, cache, block_table, kv_lens, cu_tokens=None, *, scale=None, 
     causal: it sees no later token, and with window > 0 only less than window
     back; otherwise all kv_lens[b].  scale: head_dim ** -0.5 unless given.  Y is of
     Q's type, or fp32 with y_dtype="f32"; return_lse: (Y, log of the sums of exp,
-    (T, q_heads) fp32).  Q may be a slice of a joint projection."""
+    (T, q_heads) fp32).  Q may be a slice of a joint projection.  Give max_tokens with
+    cu_tokens where it is known: without it any sequence may have all T rows, and a
+    batch of single tokens is worked on as prompts are, whose histories no two
+    workgroups share."""
     T = _t()
     lib = _load()
     dts = T.code

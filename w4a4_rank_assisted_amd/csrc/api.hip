@@ -169,7 +169,7 @@ size_t type_bytes(int dtype) { return dtype == HSQ_F32 ? 4 : 2; }
 
 // 4-bit cache: what every call says of the sequences.  On success c is filled in.
 constexpr int kKvMaxRows = 1 << 24, kKvMaxHeads = 4096, kKvMaxBatch = 65535, kKvMaxCapacity = 1 << 30;
-constexpr long long kKvMaxBlocks = 1LL << 23;
+constexpr long long kKvMaxBlocks = 1LL << 23, kKvMaxBound = 1LL << 36;
 
 bool kv_dim_ok(int head_dim) { return head_dim == 64 || head_dim == 128 || head_dim == 256; }
 
@@ -192,8 +192,8 @@ int kv_check(KvCache &c, const uint8_t *cache, int num_pages, int page_size, int
   for (const int32_t *p : {table, lens, cu})
     if ((uintptr_t)p & 3u) return HSQ_E_ALIGN;
   c = KvCache{cache, num_pages, shift, kv_heads, head_dim, table, width, lens, cu, batch, T, cu ? std::min(max_tokens, T) : T / batch};
-  const long long tiles = (c.max_tokens + 2LL * kKvTile - 2) / kKvTile;
-  return tiles * batch * kv_heads < kKvMaxBlocks ? HSQ_OK : HSQ_E_INVAL;
+  if ((long long)batch * c.max_tokens >= kKvMaxBound) return HSQ_E_INVAL;
+  return plan_kv_move(c).total * kv_heads < kKvMaxBlocks ? HSQ_OK : HSQ_E_INVAL;
 }
 
 size_t kv_cache_bytes(const KvCache &c) {
@@ -209,9 +209,13 @@ int kv_attention_sizes(int T, int q_heads, int kv_heads, int head_dim, int batch
       capacity > kKvMaxCapacity)
     return HSQ_E_INVAL;
   if (!kv_dim_ok(head_dim) || q_heads % kv_heads != 0) return HSQ_E_SHAPE;
-  const long long rows = (long long)max_tokens * (q_heads / kv_heads);
-  // workgroups of 16 rows, and the parts of few
-  return (rows + 15) / 16 * kv_heads * batch < kKvMaxBlocks && rows < (1LL << 30) ? HSQ_OK : HSQ_E_INVAL;
+  // rows of one sequence: workgroups of 16 where there are few, and their parts; of many the
+  // blocks may be dealt out from row to row, which the call checks
+  const long long gr = q_heads / kv_heads, rows = max_tokens * gr, each = (rows + 15) / 16 * batch;
+  return (rows < 64 ? each : std::min(each, T * gr / 64 + batch)) * kv_heads < kKvMaxBlocks && rows < (1LL << 30) &&
+                 (long long)batch * max_tokens < kKvMaxBound
+             ? HSQ_OK
+             : HSQ_E_INVAL;
 }
 
 size_t workspace_bytes(int M, int K, int N, int r, int batch, int group) {
@@ -1139,6 +1143,7 @@ int hsq_kv_attention(const uint16_t *Q, int q_stride, int T, int dtype, int q_he
   for (const void *p : ptrs)
     if (p && !aligned16(p)) return HSQ_E_ALIGN;
   const KvAttnPlan P = plan_kv_attention(T, q_heads, kv_heads, head_dim, batch, a.c.max_tokens, capacity);
+  if (plan_kv_attention_blocks(a.c, q_heads / kv_heads, P).total * kv_heads >= kKvMaxBlocks) return HSQ_E_INVAL;
   if (P.total > 0 && (!workspace || ws_bytes < P.total)) return HSQ_E_WORKSPACE;
   const size_t b = batch, t = T;
   if (!written_apart({{Y, t * row * type_bytes(y_dtype)}, {lse, t * q_heads * 4}, {workspace, P.total}},

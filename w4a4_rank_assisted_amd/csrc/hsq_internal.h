@@ -474,7 +474,20 @@ struct KvCache {
   const int32_t *lens;     // B: tokens of each sequence, the call's own included
   const int32_t *cu;       // B + 1 first rows, or null: T / B rows each
   int B, T, max_tokens;
+  int searched = 0;        // blocks are dealt out by cu (kv_block)
 };
+
+// Blocks of `rows` rows (per_token to a token) for sequences of at most c.max_tokens
+// tokens, of which one takes `extra` blocks more than its rows fill: as many to each, or,
+// where max_tokens is so loose a bound that this is more than four times as many as the
+// rows need, from row to row, each workgroup looking its sequence up in cu.  1024
+// sequences of 8 tokens, 8 heads of 128, without a bound: written in 55 us, 903 with blocks to
+// each; 16 of 400 (16 times the blocks): 13.8 and 20.5, with the bound of 400 13.0.
+struct KvBlocks { int searched; long long each, total; };   // blocks to a sequence (not searched), in all
+inline KvBlocks kv_blocks(const KvCache &c, long long each, int per_token, int rows, int extra) {
+  const long long all = each * c.B, need = (long long)c.T * per_token / rows + (long long)extra * c.B;
+  return c.cu && all > 4 * need ? KvBlocks{1, 0, need} : KvBlocks{0, each, all};
+}
 
 struct KvMoveArgs {
   KvCache c;
@@ -482,8 +495,9 @@ struct KvMoveArgs {
   int k_stride, v_stride;  // elements from token to token
   int dtype, asym;
 };
-hipError_t launch_kv_write(const KvMoveArgs &a, hipStream_t s);
-hipError_t launch_kv_read(const KvMoveArgs &a, hipStream_t s);
+KvBlocks plan_kv_move(const KvCache &c);
+hipError_t launch_kv_write(KvMoveArgs a, hipStream_t s);
+hipError_t launch_kv_read(KvMoveArgs a, hipStream_t s);
 
 struct KvAttnArgs {
   KvCache c;
@@ -510,8 +524,10 @@ struct KvAttnPlan {
   int splits = 1;
   size_t part_off = 0, total = 0;
 };
+// Blocks of rows of one head of the cache.
+KvBlocks plan_kv_attention_blocks(const KvCache &c, int gr, const KvAttnPlan &p);
 KvAttnPlan plan_kv_attention(int T, int Hq, int H, int D, int B, int max_tokens, int64_t capacity);
-hipError_t launch_kv_attention(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s);
+hipError_t launch_kv_attention(KvAttnArgs a, const KvAttnPlan &p, hipStream_t s);
 
 }  // namespace hsq
 
@@ -537,6 +553,22 @@ __device__ __forceinline__ void kv_rows(const KvCache &c, int b, int &start, int
     n = c.T / c.B;
     start = b * n;
   }
+}
+
+// The sequence of block `block` of a launch that kv_blocks deals out from row to row, and
+// the block's number in it; -1 where cu names none.  Sequence b's blocks begin at
+// start per_token / rows + extra b, which leaves it what its rows fill, rounded down,
+// and `extra` more.
+__device__ __forceinline__ int kv_block(const KvCache &c, int block, int per_token, int rows, int extra, int &at) {
+  auto begin = [&](int b) { return (int)((int64_t)min(max(c.cu[b], 0), c.T) * per_token / rows) + extra * b; };
+  int lo = 0, hi = c.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (begin(mid) <= block) lo = mid;
+    else hi = mid - 1;
+  }
+  at = block - begin(lo);
+  return at < 0 ? -1 : lo;
 }
 
 // Tokens of sequence b that the cache can hold: its length, cut at the end of

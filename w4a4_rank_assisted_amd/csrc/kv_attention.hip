@@ -466,13 +466,22 @@ __device__ __forceinline__ void values(const Side<D> &t, const v4u (&w)[MT][D / 
 
 // Where a workgroup of rows [r0, ..) of a sequence stands.
 struct Place {
-  int b, h, part, start, rows, len, p0;
+  int b, h, block, part, start, rows, len, p0;
 };
-__device__ __forceinline__ Place place_of(const KvAttnArgs &a, int splits) {
+__device__ __forceinline__ Place place_of(const KvAttnArgs &a, int splits, int block, int block_rows) {
   Place c;
   c.h = blockIdx.y;
   c.part = splits == 1 ? 0 : blockIdx.z % splits;
   c.b = splits == 1 ? blockIdx.z : blockIdx.z / splits;
+  c.block = block;
+  c.rows = 0;
+  if (a.c.searched) {
+    c.b = kv_block(a.c, block, a.gr, block_rows, 1, c.block);
+    if (c.b < 0) {
+      c.block = 0;                        // no rows: every wave returns
+      return c;
+    }
+  }
   int n;
   kv_rows(a.c, c.b, c.start, n);
   c.rows = min(n, a.c.max_tokens) * a.gr;      // positions count all rows, the others are left alone
@@ -526,9 +535,9 @@ __global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float2 *base = base_of[wave];
   if (lane < 16 * MT) base[lane] = make_float2(0.0f, 0.0f);
-  const Place c = place_of(a, ROWS ? 1 : a.splits);
   // the last rows see the most: first
-  const int r0 = (int)(gridDim.x - 1 - blockIdx.x) * kRows + (ROWS ? wave * 16 * MT : 0);
+  const Place c = place_of(a, ROWS ? 1 : a.splits, (int)(gridDim.x - 1 - blockIdx.x), kRows);
+  const int r0 = c.block * kRows + (ROWS ? wave * 16 * MT : 0);
   if (r0 >= c.rows) return;
   const int r1 = min(r0 + 16 * MT, c.rows);
   int first, last;
@@ -769,8 +778,8 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   float2 *base = base_of[wave];         // as in weigh
   if (lane < kRows) base[lane] = make_float2(0.0f, 0.0f);
-  const Place c = place_of(a, a.splits);
-  const int r0 = blockIdx.x * kRows;
+  const Place c = place_of(a, a.splits, blockIdx.x, kRows);
+  const int r0 = c.block * kRows;
   if (r0 >= c.rows) return;
   const int r1 = min(r0 + kRows, c.rows);
   int first, last;
@@ -1140,7 +1149,9 @@ hipError_t launch4(const KvAttnArgs &a, dim3 grid, hipStream_t s) {
 
 template <int D>
 hipError_t launch_d(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s) {
-  const dim3 grid((unsigned)ceil_div(a.c.max_tokens * a.gr, p.rows), (unsigned)a.c.H, (unsigned)(a.c.B * p.splits));
+  const KvBlocks blocks = plan_kv_attention_blocks(a.c, a.gr, p);
+  const dim3 grid = blocks.searched ? dim3((unsigned)blocks.total, (unsigned)a.c.H)
+                                    : dim3((unsigned)blocks.each, (unsigned)a.c.H, (unsigned)(a.c.B * p.splits));
   hipError_t e;
   constexpr int kMt = D == 256 ? 1 : 2;      // two row tiles of 256 channels would not fit the registers
   if (p.by_rows) return launch16<D, kMt, true>(a, grid, s);
@@ -1179,7 +1190,13 @@ KvAttnPlan plan_kv_attention(int T, int Hq, int H, int D, int B, int max_tokens,
   return p;
 }
 
-hipError_t launch_kv_attention(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s) {
+KvBlocks plan_kv_attention_blocks(const KvCache &c, int gr, const KvAttnPlan &p) {
+  const long long each = ((long long)c.max_tokens * gr + p.rows - 1) / p.rows;
+  return p.by_rows ? kv_blocks(c, each, gr, p.rows, 1) : KvBlocks{0, each, each * c.B};
+}
+
+hipError_t launch_kv_attention(KvAttnArgs a, const KvAttnPlan &p, hipStream_t s) {
+  a.c.searched = plan_kv_attention_blocks(a.c, a.gr, p).searched;
   switch (a.c.D) {
     case 64: return launch_d<64>(a, p, s);
     case 128: return launch_d<128>(a, p, s);

@@ -62,15 +62,24 @@ struct Tile {
   }
 };
 
+// Sequence of a workgroup, and which of its tiles it has.  n positions touch n / 32 tiles,
+// rounded down, and two more at most.
+__device__ __forceinline__ int block_of(const KvCache &c, int tiles, int &at) {
+  if (c.searched) return kv_block(c, blockIdx.x, 1, kKvTile, 2, at);
+  at = (int)(blockIdx.x % tiles);
+  return (int)(blockIdx.x / tiles);
+}
+
 // The positions of a workgroup: tile number, and [lo, hi) of the positions that
 // the call brings there; false where there are none.
 struct Span { int b, tile, lo, hi, row0; };   // row of position p: row0 + p
 __device__ __forceinline__ bool span_of(const KvCache &c, int tiles, Span &s) {
-  s.b = blockIdx.x / tiles;
-  int start, n;
+  int at, start, n;
+  s.b = block_of(c, tiles, at);
+  if (s.b < 0) return false;
   kv_rows(c, s.b, start, n);
   const int len = max(c.lens[s.b], 0), p0 = len - n, first = max(p0, 0);
-  s.tile = first / kKvTile + (int)(blockIdx.x % tiles);
+  s.tile = first / kKvTile + at;
   s.lo = (int)max((int64_t)first, min((int64_t)s.tile * kKvTile, (int64_t)len));
   // rows beyond max_tokens are left alone: they may lie in a tile that others begin
   s.hi = (int)min((int64_t)min(kv_len(c, s.b), p0 + min(n, c.max_tokens)), (int64_t)(s.tile + 1) * kKvTile);
@@ -250,14 +259,15 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvMoveArgs a, int tiles) {
   using L = Tile<D>;
   constexpr int G = L::G;
   __shared__ __attribute__((aligned(16))) uint8_t buf[L::kBytes];
-  const int b = blockIdx.x / tiles, h = blockIdx.y, tid = threadIdx.x, c = tid & 7;
-  int start, n;
+  int at, start, n;
+  const int b = block_of(a.c, tiles, at), h = blockIdx.y, tid = threadIdx.x, c = tid & 7;
+  if (b < 0) return;
   kv_rows(a.c, b, start, n);
   // row i of the sequence is position p0 + i; one that holds nothing (negative,
   // past the table, on no page) is a row all the same, and reads zero
   const int p0 = max(a.c.lens[b], 0) - n, len = kv_len(a.c, b), rows = min(n, a.c.max_tokens);
   const int first = p0 >= 0 ? p0 / kKvTile : -((kKvTile - 1 - p0) / kKvTile);
-  const int tile = first + (int)(blockIdx.x % tiles);
+  const int tile = first + at;
   const int64_t base = (int64_t)tile * kKvTile;
   if (base >= (int64_t)p0 + rows) return;
   const uint8_t *src = base >= 0 && base < len ? kv_tile_at(a.c, b, h, tile) : nullptr;
@@ -312,13 +322,10 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvMoveArgs a, int tiles) {
   }
 }
 
-// Tiles that max_tokens positions in a row can touch.
-int tiles_of(const KvCache &c) { return (c.max_tokens + 2 * kKvTile - 2) / kKvTile; }
-
 template <int D>
-hipError_t write_d(const KvMoveArgs &a, hipStream_t s) {
-  const int tiles = tiles_of(a.c);
-  const dim3 grid((unsigned)(tiles * a.c.B), (unsigned)a.c.H);
+hipError_t write_d(const KvMoveArgs &a, const KvBlocks &p, hipStream_t s) {
+  const int tiles = (int)p.each;
+  const dim3 grid((unsigned)p.total, (unsigned)a.c.H);
   if (a.dtype == kBf16) {
     if (a.asym) hipLaunchKernelGGL((k_kv_write<kBf16, D, true>), grid, dim3(kThreads), 0, s, a, tiles);
     else hipLaunchKernelGGL((k_kv_write<kBf16, D, false>), grid, dim3(kThreads), 0, s, a, tiles);
@@ -330,9 +337,9 @@ hipError_t write_d(const KvMoveArgs &a, hipStream_t s) {
 }
 
 template <int D>
-hipError_t read_d(const KvMoveArgs &a, hipStream_t s) {
-  const int tiles = tiles_of(a.c);
-  const dim3 grid((unsigned)(tiles * a.c.B), (unsigned)a.c.H);
+hipError_t read_d(const KvMoveArgs &a, const KvBlocks &p, hipStream_t s) {
+  const int tiles = (int)p.each;
+  const dim3 grid((unsigned)p.total, (unsigned)a.c.H);
   if (a.dtype == kBf16) hipLaunchKernelGGL((k_kv_read<kBf16, D>), grid, dim3(kThreads), 0, s, a, tiles);
   else if (a.dtype == kF16) hipLaunchKernelGGL((k_kv_read<kF16, D>), grid, dim3(kThreads), 0, s, a, tiles);
   else hipLaunchKernelGGL((k_kv_read<kF32, D>), grid, dim3(kThreads), 0, s, a, tiles);
@@ -341,20 +348,29 @@ hipError_t read_d(const KvMoveArgs &a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_kv_write(const KvMoveArgs &a, hipStream_t s) {
+// Tiles that max_tokens positions in a row can touch, to each sequence.
+KvBlocks plan_kv_move(const KvCache &c) {
+  return kv_blocks(c, (c.max_tokens + 2LL * kKvTile - 2) / kKvTile, 1, kKvTile, 2);
+}
+
+hipError_t launch_kv_write(KvMoveArgs a, hipStream_t s) {
+  const KvBlocks p = plan_kv_move(a.c);
+  a.c.searched = p.searched;
   switch (a.c.D) {
-    case 64: return write_d<64>(a, s);
-    case 128: return write_d<128>(a, s);
-    case 256: return write_d<256>(a, s);
+    case 64: return write_d<64>(a, p, s);
+    case 128: return write_d<128>(a, p, s);
+    case 256: return write_d<256>(a, p, s);
     default: return hipErrorInvalidValue;
   }
 }
 
-hipError_t launch_kv_read(const KvMoveArgs &a, hipStream_t s) {
+hipError_t launch_kv_read(KvMoveArgs a, hipStream_t s) {
+  const KvBlocks p = plan_kv_move(a.c);
+  a.c.searched = p.searched;
   switch (a.c.D) {
-    case 64: return read_d<64>(a, s);
-    case 128: return read_d<128>(a, s);
-    case 256: return read_d<256>(a, s);
+    case 64: return read_d<64>(a, p, s);
+    case 128: return read_d<128>(a, p, s);
+    case 256: return read_d<256>(a, p, s);
     default: return hipErrorInvalidValue;
   }
 }
