@@ -1,5 +1,5 @@
 """Calls of the 4-bit cache and of the weight-only layer on the host: batches whose
-bound on the rows is loose."""
+bound on the rows is loose, a choice that there is not."""
 
 import pytest
 
@@ -17,3 +17,10 @@ def test_a_ragged_batch_without_a_bound(b, T, code):
     refused(write(b=b, T=T, top=T, K=1 << 44, ks=512, V=1 << 45, vs=512, **FAR), code)
     refused(read(b=b, T=T, top=T, K=1 << 44, V=1 << 45, **FAR), code)
     refused(attend(b=b, T=T, top=T, Q=1 << 44, Hq=32, qs=2048, Y=1 << 45, lse=1 << 46, ws=None, wsb=0, **FAR), code)
+
+
+@pytest.mark.parametrize("kernel", ["tiled", "skinny", "other"])
+def test_a_weight_only_layer_has_one_kernel(kernel):
+    layer = object.__new__(hsq.Layer)
+    with pytest.raises(ValueError, match="weight_only has one kernel"):
+        layer(None, kernel=kernel, weight_only=True)

@@ -389,8 +389,11 @@ class Layer:
                  residual=None):
         """Y (batch, M, N) on the current stream.  weight_only leaves the
         activations in 16 bits (w4a16_lowrank_linear, M <= 64), the form for
-        decoding single tokens; it may add a residual, and has one kernel."""
+        decoding single tokens; it may add a residual, and has one kernel (no
+        choice of it: refused)."""
         if weight_only:
+            if kernel != "auto":
+                raise ValueError(f"kernel {kernel!r}: weight_only has one kernel")
             need = w4a16_workspace_bytes(X.shape[0], self.K, self.N, self.r, self.batch, self.group, True, y_dtype)
             ws = self.workspace if self.workspace is not None and self.workspace.numel() >= need else None
             return w4a16_lowrank_linear(X, self.packed, self.sw, self.lam, self.L1, self.L2, self.bias, residual,
