@@ -321,6 +321,7 @@ __device__ __forceinline__ void weigh(const float (&e)[MT][8], v4u (&vs)[D / 64]
                                       float2 *base, Sums<D, MT> &s, v4u (&w)[MT][D / 64], v4u (&w2)[MT][D / 64]) {
   constexpr int G = D / kKvGroup;
   float p[MT][8], top[MT], topp[MT];
+  bool any_base = false;                  // of this tile: such a row exceeds the range in every one
   auto form = [&](auto again) __attribute__((always_inline)) {
     // the scales stay packed: converted for both uses at once they would hold 8 G registers
 #pragma unroll
@@ -331,7 +332,7 @@ __device__ __forceinline__ void weigh(const float (&e)[MT][8], v4u (&vs)[D / 64]
       topp[m] = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[m][i] = __builtin_fmaf(e[m][i], c2[m], -s.o[m]);
-      if constexpr (decltype(again)::value) {
+      if (decltype(again)::value && any_base) {
         const float2 b = base[16 * m + (lane_here() & 15)];
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[m][i] = b.x != 0.0f ? (e[m][i] * c2[m] - b.x) - b.y : p[m][i];
@@ -376,10 +377,9 @@ __device__ __forceinline__ void weigh(const float (&e)[MT][8], v4u (&vs)[D / 64]
       const bool move = max_over<16, 32>(mine) > 0.0f;
       float2 &own = base[16 * m + (lane_here() & 15)];
       const float2 had = own;
-      float most = kHidden, high = kHidden;      // of e + log2(s), and of e
+      float most = kHidden;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        high = fmaxf(high, e[m][i] * c2[m]);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           asm volatile("" : "+v"(vs[g]));
@@ -391,6 +391,10 @@ __device__ __forceinline__ void weigh(const float (&e)[MT][8], v4u (&vs)[D / 64]
       float o = move ? __builtin_ceilf(most) - kTop : s.o[m], al = move ? __builtin_amdgcn_exp2f(s.o[m] - o) : 1.0f;
       const bool based = move && (had.x != 0.0f || fabsf(most) >= kFar);
       if (__any(based)) {
+        any_base = true;
+        float high = kHidden;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) high = fmaxf(high, e[m][i] * c2[m]);
         high = max_over<16, 32>(high);
         const float b = base_with(had, high);
         float near = kHidden;
@@ -527,7 +531,7 @@ __device__ __forceinline__ void join_waves(const KvAttnArgs &a, const Place &c, 
 }
 
 template <int D, int MT, int W, bool SPLIT, bool ROWS>
-__global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) void k_kv_attention(KvAttnArgs a) {
+__global__ __launch_bounds__(64 * W, D == 64 ? (MT == 2 ? 3 : 4) : MT == 2 || D == 256 ? 2 : 3) void k_kv_attention(KvAttnArgs a) {
   constexpr int G = D / kKvGroup, kRows = 16 * MT * (ROWS ? W : 1), kLd = D + 4;
   extern __shared__ float lds[];
   __shared__ float2 base_of[W][16 * MT];
@@ -640,17 +644,18 @@ __global__ __launch_bounds__(64 * W, MT == 2 || D == 256 ? 2 : D == 64 ? 4 : 3) 
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     s.l[m] = sum_over<16, 32>(s.l[m]);
-    float back = 1.0f;          // a row with a base leaves with that as its offset: it would swallow o
-    const float2 b = base[16 * m + col];
-    if (b.x != 0.0f) {
-      back = __builtin_amdgcn_exp2f(b.y);
-      s.l[m] *= back;
-      s.o[m] = b.x;
-    }
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
       const float up = x & 1 ? Unit<SPLIT>::high : Unit<SPLIT>::low;
-      s.acc[m][x] = (s.acc[m][x] * up - s.zero[m][x / 4] * Unit<SPLIT>::low) * back;
+      s.acc[m][x] = s.acc[m][x] * up - s.zero[m][x / 4] * Unit<SPLIT>::low;
+    }
+    const float2 b = base[16 * m + col];
+    if (__any(b.x != 0.0f)) {             // such rows leave with b as their offset: it would swallow o
+      const float back = b.x != 0.0f ? __builtin_amdgcn_exp2f(b.y) : 1.0f;
+      s.l[m] *= back;
+      s.o[m] = b.x != 0.0f ? b.x : s.o[m];
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) s.acc[m][x] *= back;
     }
   }
   if (ROWS) {
@@ -918,6 +923,7 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
     // weights
     v2u w[R][kSets], w2[R][kSets];
     float pw[R][4], ps[R][kSets][4], top[R], topp[R];
+    bool any_base = false;
     auto form = [&](auto again) __attribute__((always_inline)) {
       bool moved = false;
 #pragma unroll
@@ -925,7 +931,7 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
         top[r] = topp[r] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) pw[r][i] = __builtin_fmaf(e[r][i], c2[r], -s.o[r]);
-        if constexpr (decltype(again)::value) {
+        if (decltype(again)::value && any_base) {
           const float2 b = base[4 * r + (lane_here() & 3)];
 #pragma unroll
           for (int i = 0; i < 4; ++i) pw[r][i] = b.x != 0.0f ? (e[r][i] * c2[r] - b.x) - b.y : pw[r][i];
@@ -955,19 +961,21 @@ __global__ __launch_bounds__(64 * W, R == 1 && D < 256 ? 4 : 2) void k_kv_attent
         const bool move = max_over<4, 32>(mine) > 0.0f;
         float2 &own = base[4 * r + (lane_here() & 3)];
         const float2 had = own;
-        float most = kHidden, high = kHidden;
+        float most = kHidden;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          high = fmaxf(high, e[r][i] * c2[r]);
+        for (int j = 0; j < kSets; ++j)
 #pragma unroll
-          for (int j = 0; j < kSets; ++j)
+          for (int i = 0; i < 4; ++i)
             if (!masked || e[r][i] != kHidden)
               most = fmaxf(most, __builtin_fmaf(e[r][i], c2[r], __builtin_amdgcn_logf(fmaxf(half_of(tv.s[j], i), kTiny))));
-        }
         most = max_over<4, 32>(most);
         float o = move ? __builtin_ceilf(most) - kTop : s.o[r], al = move ? __builtin_amdgcn_exp2f(s.o[r] - o) : 1.0f;
         const bool based = move && (had.x != 0.0f || fabsf(most) >= kFar);
         if (__any(based)) {
+          any_base = true;
+          float high = kHidden;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) high = fmaxf(high, e[r][i] * c2[r]);
           high = max_over<4, 32>(high);
           const float b = base_with(had, high);
           float near = kHidden;
