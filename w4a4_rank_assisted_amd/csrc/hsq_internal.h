@@ -455,10 +455,9 @@ hipError_t launch_w4a16(const W4a16Args &a, hipStream_t s);
 //            nibble and 32 p + 16 + c in its high one: no byte is shared by two
 //            tokens, so appending one never reads another
 //   scales   fp16, K then V: [group][q][4 a + r] for token 16 a + 4 q + r
-//   zeros    bytes 16 + z (as the attention adds them), K then V: [q][group][a][b], b as in the V codes
-//
-// 16 + n is a code as the matrix operand sees it: the nibble under a constant
-// exponent, in bf16 and in fp16 alike.
+//   zeros    bytes 16 + z, K then V: [q][group][a][b], b as in the V codes.  The 16 is part
+//            of the format and of no use: readers mask it off (four zeros at once) or
+//            subtract it
 // ---------------------------------------------------------------------------
 constexpr int kKvTile = 32;                  // tokens per tile
 constexpr int kKvGroup = 64;                 // channels per scale

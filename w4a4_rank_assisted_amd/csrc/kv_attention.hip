@@ -42,9 +42,9 @@
 //
 // Three forms, by the query rows that share a head of the cache in one sequence:
 //
-// - Up to 8 rows (a token or two of a few heads each): the 4 x 4 products.  A lane
-//   is a token of its group's channels in the first and two channels in the
-//   second, so no lane's work is lost on rows that do not exist, which in 16 x 16
+// - Up to 8 rows (a token or two of a few heads each), 4 with heads of 256: the 4 x 4
+//   products.  A lane is a token of its group's channels in the first and two channels in
+//   the second, so no lane's work is lost on rows that do not exist, which in 16 x 16
 //   tiles is three quarters at four rows.  The first product leaves tokens 4 c .. 4 c + 3
 //   of row j in lane 4 c + j, which is the second's operand.  The call is bound by
 //   the read of the cache.
@@ -53,7 +53,8 @@
 //   the first one gave it.
 // - More (prompts): the same, two row tiles to a wave, and each wave has rows of its own.
 //
-// In none of them p leaves the registers, and the loop has no LDS and no barrier.
+// In none of them p leaves the registers, and the loop has no barrier and no LDS but a
+// base's.
 // In the first two the waves of a workgroup deal out its tokens, and
 // workgroups split long sequences (k_kv_join adds their parts).
 #include "hsq_internal.h"
@@ -264,8 +265,8 @@ __device__ __forceinline__ void load_side(const uint8_t *p, int lane, Side<D> &t
 template <int D, int MT>
 struct Sums {
   static constexpr int G = D / kKvGroup;
-  v4f acc[MT][D / 16];     // channels 16 nt + 4 (lane / 16) + r, times 2^-24 (nt even) and 2^-20
-  v4f zero[MT][G];         // the sums of (p s) z, times 2^-24: all four alike
+  v4f acc[MT][D / 16];     // channels 16 nt + 4 (lane / 16) + r, under the codes' Unit (nt even low, odd high)
+  v4f zero[MT][G];         // the sums of (p s) z, under Unit's low: all four alike; 0 with two terms
   float o[MT], l[MT];      // l: this lane's tokens only
 };
 
@@ -735,7 +736,7 @@ __device__ __forceinline__ void load_zeros4(const uint8_t *p, int lane, v2u (&z)
 template <int D, int R>
 struct Sums4 {
   static constexpr int kSets = Side4<D>::kSets;
-  v4f low[R][kSets], high[R][kSets];   // channels 32 p + lane % 16 (times 2^-24), and 16 more (2^-20)
+  v4f low[R][kSets], high[R][kSets];   // channels 32 p + lane % 16, and 16 more, under the codes' Unit
   float zero[R][kSets], o[R], l[R];
 };
 
@@ -1164,9 +1165,9 @@ hipError_t launch_d(const KvAttnArgs &a, const KvAttnPlan &p, hipStream_t s) {
   constexpr int kMt = D == 256 ? 1 : 2;      // two row tiles of 256 channels would not fit the registers
   if (p.by_rows) return launch16<D, kMt, true>(a, grid, s);
   if (p.rows == 4) e = p.waves == 8 ? launch4<D, 1, 8>(a, grid, s) : launch4<D, 1, 4>(a, grid, s);
-  else if (p.rows == 8) e = launch4<D, D == 256 ? 1 : 2, kWaves>(a, grid, s);
   else if (p.rows == 16) e = launch16<D, 1, false>(a, grid, s);
-  else e = launch16<D, kMt, false>(a, grid, s);
+  else if constexpr (D == 256) e = hipErrorInvalidValue;      // the plan has no others for these heads
+  else e = p.rows == 8 ? launch4<D, 2, kWaves>(a, grid, s) : launch16<D, kMt, false>(a, grid, s);
   if (e == hipSuccess && p.splits > 1) {
     hipLaunchKernelGGL((k_kv_join<D>), dim3((unsigned)(a.c.max_tokens * a.gr), (unsigned)a.c.H, (unsigned)a.c.B), dim3(256),
                        0, s, a, p.rows);

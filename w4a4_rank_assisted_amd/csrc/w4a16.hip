@@ -32,7 +32,9 @@
 // codes are shifted to (8 + code) 2^-18, which keeps 2^-20, for three shifts a dword
 // (12288 x 4096, 16 rows: 21.8 us either way).  The 24 or 8 times the sum of xh that
 // is too much in every column is the accumulator's first value, the product of the
-// same xh with a constant, one for all column tiles.  U is formed in fp32.
+// same xh with a constant, one for all column tiles.  U's products and sums are fp32: up
+// to four rows of xh as its terms hold it (the same xh as in the other sum: 11 bits for a bf16
+// Y), above of xh before it is rounded.
 #include "hsq_internal.h"
 
 #include <algorithm>
