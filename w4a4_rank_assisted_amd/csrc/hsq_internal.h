@@ -481,7 +481,8 @@ struct KvCache {
 // where max_tokens is so loose a bound that this is more than four times as many as the
 // rows need, from row to row, each workgroup looking its sequence up in cu.  1024
 // sequences of 8 tokens, 8 heads of 128, without a bound: written in 55 us, 903 with blocks to
-// each; 16 of 400 (16 times the blocks): 13.8 and 20.5, with the bound of 400 13.0.
+// each; 16 of 400 (14 times the blocks): 13.8 and 20.5, with the bound of 400 13.0; 6 of 300
+// (5 times): 7.7 and 8.0; 5 of 333 (4 times): 5.1 and 4.9.
 struct KvBlocks { int searched; long long each, total; };   // blocks to a sequence (not searched), in all
 inline KvBlocks kv_blocks(const KvCache &c, long long each, int per_token, int rows, int extra) {
   const long long all = each * c.B, need = (long long)c.T * per_token / rows + (long long)extra * c.B;

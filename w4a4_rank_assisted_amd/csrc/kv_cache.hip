@@ -21,10 +21,10 @@
 // tile out in LDS, and stores it whole, or, at the ends of a run, token by token
 // (no byte belongs to two tokens, so nothing is read back).  A tile per workgroup is
 // also what a token of a long batch needs: its 32 positions hold one row, and the
-// call is as long as a launch and one read (5.0 us for 64 sequences of 8 heads).
+// call is as long as a launch and one read (5.2 us for 64 sequences of 8 heads).
 //
-// Measured, bf16, 8 heads of 128: 8192 tokens are written in 13.2 us (3.2 TB/s; 11.0
-// symmetric) and read back in 11.4 (3.8), 16384 in 21.6 and 17.4 (4.9).  Writing is
+// Measured, bf16, 8 heads of 128: 8192 tokens are written in 13.5 us (3.2 TB/s; 11.0
+// symmetric) and read back in 11.4 (3.8), 16384 in 22.1 and 17.4 (4.9).  Writing is
 // bound by its arithmetic, 80 instructions for eight channels: with IEEE divisions
 // and codes packed by shifts it took 16.7 us, with one load on its way at a time 13.9.
 #include "hsq_internal.h"
