@@ -64,7 +64,8 @@ extern "C" {
 /* ---- status codes ---- */
 #define HSQ_OK            0
 #define HSQ_E_INVAL      -1  /* null pointer, size out of range, bad dtype or kernel choice; the
-                              * 16-bit linear and the norm: an output over another operand */
+                              * 16-bit linear, the norm, the layer with 16-bit activations and
+                              * the 4-bit cache: an output over another operand */
 #define HSQ_E_SHAPE      -2  /* K not a positive multiple of 64, a window outside the matrix, sizes
                               * that do not divide or that no kernel has (the 4-bit cache) */
 #define HSQ_E_ALIGN      -3  /* a pointer is not 16-byte aligned */
